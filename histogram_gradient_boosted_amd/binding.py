@@ -10,7 +10,7 @@ from __future__ import annotations
 
 import ctypes
 import os
-from typing import Optional
+from typing import NamedTuple, Optional
 
 import numpy as np
 
@@ -36,19 +36,32 @@ EXPORTED = ("hgb_available", "hgb_create", "hgb_destroy", "hgb_last_error", "hgb
             "hgb_profile_query", "hgb_set_precision", "hgb_partition_level",
             "hgb_subtract_find_splits", "hgb_begin_tree_objective", "hgb_copy_quantized",
             "hgb_find_level_split", "hgb_find_splits_noalloc", "hgb_set_async_begin",
-            "hgb_grow_level")
+            "hgb_grow_level",
+            "hgb_embed", "hgb_embed_backward", "hgb_embed_backward_workspace",
+            "hgb_layer_norm", "hgb_layer_norm_backward", "hgb_layer_norm_backward_workspace",
+            "hgb_route", "hgb_route_workspace", "hgb_route_gather", "hgb_route_gather_backward",
+            "hgb_route_combine", "hgb_route_combine_backward")
 
 # hgb_objective
 OBJECTIVES = {"squared": 0, "logistic": 1, "poisson": 2}
 
 KERNELS = {"quantize": 0, "gather": 1, "zero": 2, "fill": 3, "subtract": 4, "split": 5,
-           "partition": 6, "fill_root": 7, "fill_level": 8, "merge": 9}
+           "partition": 6, "fill_root": 7, "fill_level": 8, "merge": 9, "embed": 10, "norm": 11,
+           "route": 12}
 
 
 class HGBError(RuntimeError):
     def __init__(self, status: int, message: str):
         super().__init__(f"{_STATUS_NAMES.get(status, status)}: {message}")
         self.status = status
+
+
+class Route(NamedTuple):
+    """Where Context.route sends each slot (row r's k-th expert is slot
+    r * top + k): int32 CUDA tensors."""
+    order: object      # [rows * top]: the slot at each place, -1 past the last
+    position: object   # [rows, top]: the place of each slot, -1 when dropped
+    offsets: object    # [experts + 1]: the first place of each expert
 
 
 _lib = None
@@ -117,6 +130,23 @@ def load():
     lib.hgb_profile_query.argtypes = [vp, c_int, ctypes.POINTER(ctypes.c_double),
                                       ctypes.POINTER(ctypes.c_int64)]
     lib.hgb_profile_query.restype = c_int
+    i64, f32 = ctypes.c_int64, ctypes.c_float
+    lib.hgb_embed.argtypes = [vp, vp, i32, i64, i64, i64, vp, i64, i32, f32, vp, i32, i64]
+    lib.hgb_embed_backward.argtypes = [vp, vp, i32, i64, i64, i64, vp, i32, f32, i64, vp, i32, i64, vp, i64]
+    lib.hgb_embed_backward_workspace.argtypes = [i64, i64, i64]
+    lib.hgb_layer_norm.argtypes = [vp, vp, i32, i64, i64, i64, vp, vp, i32, f32, vp, i64, vp, vp]
+    lib.hgb_layer_norm_backward.argtypes = [vp, vp, i64, vp, i64, i32, i64, i64, vp, vp, vp, i32, vp, i64,
+                                            vp, vp, vp, i64]
+    lib.hgb_layer_norm_backward_workspace.argtypes = [i64, i64]
+    lib.hgb_route.argtypes = [vp, vp, i64, i32, i32, vp, vp, vp, vp, i64]
+    lib.hgb_route_workspace.argtypes = [i64, i32, i32]
+    lib.hgb_route_gather.argtypes = [vp, vp, i32, i64, i64, i32, i64, vp, vp, i32, vp, i64]
+    lib.hgb_route_gather_backward.argtypes = [vp, vp, i32, i64, i64, i32, i64, vp, vp, i64]
+    lib.hgb_route_combine.argtypes = [vp, vp, i32, i64, i64, i32, i64, vp, vp, vp, i64]
+    lib.hgb_route_combine_backward.argtypes = [vp, vp, i32, i64, vp, i64, i64, i32, i64, vp, vp, i32, vp, vp,
+                                               i64, vp]
+    for name in EXPORTED[-12:]:
+        getattr(lib, name).restype = i64 if name.endswith("_workspace") else c_int
     _lib = lib
     return lib
 
@@ -148,6 +178,8 @@ class Context:
         self._torch = torch
         self._lib = load()
         self.device = int(device)
+        self._torch_device = torch.device("cuda", self.device)
+        self._types = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}   # hgb_dtype
         if stream is None:
             stream = torch.cuda.current_stream(self.device)
         self.stream = stream
@@ -416,3 +448,253 @@ class Context:
         op = self._dev(out, "out", torch.uint8, int(n_nodes) * SPLIT_BYTES)
         self._check(self._lib.hgb_find_splits(self._h, hp, int(n_nodes), float(lam),
                                               float(gamma), op), "find_splits")
+
+    # -- the vector verbs ---------------------------------------------------
+    # Tensors must be on the context's device.  A call whose tensors were made
+    # on another stream than the context's is ordered after that (the current)
+    # stream's work, and the current stream after the call.
+    def _rows(self, t, name, dim=None, rows=None, dtype=None):
+        """A [..., dim] vector argument as (pointer, type code, rows, dim, row stride)."""
+        torch = self._torch
+        if not isinstance(t, torch.Tensor) or t.device.type != "cuda" or t.device.index != self.device:
+            raise ValueError(f"{name} must be a CUDA tensor on device {self.device}")
+        if t.dtype not in self._types:
+            raise ValueError(f"{name} must be float32, bfloat16 or float16, got {t.dtype}")
+        if dtype is not None and t.dtype != dtype:
+            raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+        if t.dim() == 0:
+            raise ValueError(f"{name} must have a last dimension")
+        d = t.shape[-1]
+        n = t.numel() // d if d else 0
+        if t.dim() == 2:
+            n = t.shape[0]
+            stride = t.stride(0) if n > 1 else d
+            if (d > 1 and t.stride(1) != 1) or stride < d:
+                raise ValueError(f"{name}'s rows must be contiguous and apart")
+        else:
+            stride = d
+            if not t.is_contiguous():
+                raise ValueError(f"{name} must be contiguous, or two-dimensional with contiguous rows")
+        if d < 1:
+            raise ValueError(f"{name} has rows of no values")
+        if dim is not None and d != dim:
+            raise ValueError(f"{name} has rows of {d} values, needs {dim}")
+        if rows is not None and n != rows:
+            raise ValueError(f"{name} holds {n} rows, needs {rows}")
+        return t.data_ptr(), self._types[t.dtype], n, d, stride
+
+    def _param(self, t, name, dim, x_dtype):
+        """A [dim] parameter (x's type or float32), or None."""
+        torch = self._torch
+        if t is None:
+            return None
+        self._dev(t, name)
+        if t.dtype != torch.float32 and t.dtype != x_dtype:
+            raise ValueError(f"{name} must be float32 or {x_dtype}, got {t.dtype}")
+        if t.dim() != 1 or t.shape[0] != dim:
+            raise ValueError(f"{name} must have shape [{dim}]")
+        return t.data_ptr()
+
+    def _ints(self, t, name, shape=None):
+        torch = self._torch
+        p = self._dev(t, name, torch.int32)
+        if shape is not None and tuple(t.shape) != tuple(shape):
+            raise ValueError(f"{name} has shape {tuple(t.shape)}, needs {tuple(shape)}")
+        return p
+
+    def _vec(self, what, fn, tensors, *args):
+        """One vector verb: fn(ctx, *args), ordered between the current stream's
+        work before and after it when that is not the context's stream."""
+        torch = self._torch
+        cur = torch.cuda.current_stream(self.device)
+        if cur.cuda_stream == self.stream.cuda_stream:
+            st = fn(self._h, *args)
+        else:
+            self.stream.wait_stream(cur)
+            st = fn(self._h, *args)
+            for t in tensors:
+                if t is not None:
+                    t.record_stream(self.stream)
+            cur.wait_stream(self.stream)
+        if st != HGB_OK:
+            self._check(st, what)
+
+    def _workspace(self, nbytes):
+        torch = self._torch
+        if nbytes < 0:
+            raise HGBError(HGB_E_UNSUPPORTED, "sizes beyond the verb's limits")
+        return torch.empty(nbytes, dtype=torch.uint8, device=self._torch_device) if nbytes else None
+
+    def embed(self, table, tokens, scale: float = 1.0, pad: int = -1, dtype=None, out=None):
+        """scale * table[tokens]: [*tokens.shape, dim] of `dtype` (the table's
+        type, or a 16-bit one beside a float32 table).  The token `pad` gives
+        zeros; so does one out of range, which the next sync() reports."""
+        torch = self._torch
+        tp, tt, vocab, dim, ts = self._rows(table, "table")
+        if table.dim() != 2:
+            raise ValueError("table must be two-dimensional")
+        ip = self._ints(tokens, "tokens")
+        n = tokens.numel()
+        if out is None:
+            out = torch.empty((*tokens.shape, dim), dtype=dtype or table.dtype, device=table.device)
+        op, ot, _, _, os_ = self._rows(out, "out", dim, n, dtype)
+        self._vec("embed", self._lib.hgb_embed, (table, tokens, out), tp, tt, ts, vocab, dim, ip, n, int(pad),
+                  float(scale), op, ot, os_)
+        return out
+
+    def embed_backward(self, grad, tokens, vocab: int, scale: float = 1.0, pad: int = -1, dtype=None, out=None):
+        """The gradient of embed's table: [vocab, dim] of `dtype` (grad's type, or
+        float32 beside a 16-bit one), zeros for tokens that do not occur."""
+        torch = self._torch
+        gp, gt, n, dim, gs = self._rows(grad, "grad")
+        ip = self._ints(tokens, "tokens")
+        if tokens.numel() != n:
+            raise ValueError(f"grad holds {n} rows for {tokens.numel()} tokens")
+        vocab = int(vocab)
+        if out is None:
+            out = torch.empty((max(vocab, 0), dim), dtype=dtype or grad.dtype, device=grad.device)
+        op, ot, _, _, os_ = self._rows(out, "out", dim, vocab, dtype)
+        nbytes = self._lib.hgb_embed_backward_workspace(n, vocab, dim)
+        ws = self._workspace(nbytes)
+        self._vec("embed_backward", self._lib.hgb_embed_backward, (grad, tokens, out, ws), gp, gt, gs, n, dim, ip,
+                  int(pad), float(scale), vocab, op, ot, os_, ws.data_ptr() if nbytes else None, nbytes)
+        return out
+
+    def layer_norm(self, x, weight=None, bias=None, eps: float = 1e-5, out=None):
+        """Rows of x normalised: (y, mean, rstd); y has x's shape and type, mean
+        and rstd are float32 [x.shape[:-1]].  weight and bias: [dim], float32 or
+        x's type (both the same), or None."""
+        torch = self._torch
+        xp, xt, n, dim, xs = self._rows(x, "x")
+        wp, bp = self._param(weight, "weight", dim, x.dtype), self._param(bias, "bias", dim, x.dtype)
+        pt = self._param_type(weight, bias)
+        if out is None:
+            out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        yp, _, _, _, ys = self._rows(out, "out", dim, n, x.dtype)
+        mean = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
+        rstd = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
+        self._vec("layer_norm", self._lib.hgb_layer_norm, (x, weight, bias, out, mean, rstd), xp, xt, xs, n, dim, wp, bp,
+                  pt, float(eps), yp, ys, mean.data_ptr(), rstd.data_ptr())
+        return out, mean, rstd
+
+    def _param_type(self, *params):
+        types = {t.dtype for t in params if t is not None}
+        if len(types) > 1:
+            raise ValueError("the parameters must have one type")
+        return self._types[types.pop()] if types else 0
+
+    def layer_norm_backward(self, grad, x, mean, rstd, weight=None, bias: bool = True, out=None):
+        """Gradients of layer_norm: (dx, dweight, dbias), dweight None without a
+        weight and dbias None where `bias` is false.  The parameters' gradients
+        have the weight's type (float32 without one)."""
+        torch = self._torch
+        gp, gt, n, dim, gs = self._rows(grad, "grad")
+        xp, _, _, _, xs = self._rows(x, "x", dim, n, grad.dtype)
+        wp = self._param(weight, "weight", dim, x.dtype)
+        mp, rp = self._dev(mean, "mean", torch.float32, n), self._dev(rstd, "rstd", torch.float32, n)
+        pt = self._param_type(weight)
+        if out is None:
+            out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        dp, _, _, _, ds = self._rows(out, "out", dim, n, x.dtype)
+        ptype = weight.dtype if weight is not None else torch.float32
+        dw = torch.empty(dim, dtype=ptype, device=x.device) if weight is not None else None
+        db = torch.empty(dim, dtype=ptype, device=x.device) if bias else None
+        nbytes = self._lib.hgb_layer_norm_backward_workspace(n, dim) if dw is not None or db is not None else 0
+        ws = self._workspace(nbytes)
+        self._vec("layer_norm_backward", self._lib.hgb_layer_norm_backward,
+                  (grad, x, mean, rstd, weight, out, dw, db, ws), gp, gs, xp, xs, gt, n, dim, mp, rp, wp, pt, dp, ds,
+                  dw.data_ptr() if dw is not None else None, db.data_ptr() if db is not None else None,
+                  ws.data_ptr() if nbytes else None, nbytes)
+        return out, dw, db
+
+    def route(self, experts, n_experts: int) -> Route:
+        """Sort the slots of experts ([rows, top] int32, -1: dropped) by expert."""
+        torch = self._torch
+        if not isinstance(experts, torch.Tensor) or experts.dim() != 2:
+            raise ValueError("experts must be a two-dimensional tensor")
+        ep = self._ints(experts, "experts")
+        n, top = experts.shape
+        E = int(n_experts)
+        nbytes = self._lib.hgb_route_workspace(n, top, E)
+        ws = self._workspace(nbytes)
+        order = torch.empty(n * top, dtype=torch.int32, device=experts.device)
+        position = torch.empty((n, top), dtype=torch.int32, device=experts.device)
+        offsets = torch.empty(E + 1, dtype=torch.int32, device=experts.device)
+        self._vec("route", self._lib.hgb_route, (experts, order, position, offsets, ws), ep, n, top, E,
+                  order.data_ptr(), position.data_ptr(), offsets.data_ptr(), ws.data_ptr() if nbytes else None, nbytes)
+        return Route(order, position, offsets)
+
+    def _routed(self, route, n=None):
+        """(position pointer, offsets pointer, rows, top, experts) of a Route."""
+        pp, op = self._ints(route.position, "route.position"), self._ints(route.offsets, "route.offsets")
+        if route.position.dim() != 2 or route.offsets.dim() != 1 or route.offsets.shape[0] < 2:
+            raise ValueError("route is not what Context.route returns")
+        rows, top = route.position.shape
+        if n is not None and n != rows:
+            raise ValueError(f"{n} rows for a route of {rows}")
+        return pp, op, rows, top, route.offsets.shape[0] - 1
+
+    def route_gather(self, x, route: Route, out=None):
+        """x's rows in the experts' order: [rows * top, dim], zeros past the last
+        routed place."""
+        torch = self._torch
+        xp, xt, n, dim, xs = self._rows(x, "x")
+        pp, fp, n, top, E = self._routed(route, n)
+        if out is None:
+            out = torch.empty((n * top, dim), dtype=x.dtype, device=x.device)
+        op, _, _, _, os_ = self._rows(out, "out", dim, n * top, x.dtype)
+        self._vec("route_gather", self._lib.hgb_route_gather, (x, *route, out), xp, xt, xs, n, top, dim, pp, fp, E, op, os_)
+        return out
+
+    def route_gather_backward(self, grad, route: Route, out=None):
+        """The gradient of route_gather's x: [rows, dim] sums of grad's rows
+        ([rows * top, dim])."""
+        torch = self._torch
+        pp, _, n, top, _ = self._routed(route)
+        gp, gt, _, dim, gs = self._rows(grad, "grad", rows=n * top)
+        if out is None:
+            out = torch.empty((n, dim), dtype=grad.dtype, device=grad.device)
+        op, _, _, _, os_ = self._rows(out, "out", dim, n, grad.dtype)
+        self._vec("route_gather_backward", self._lib.hgb_route_gather_backward, (grad, *route, out), gp, gt, gs, n, top,
+                  dim, pp, op, os_)
+        return out
+
+    def _weights(self, weights, n, top):
+        torch = self._torch
+        if weights is None:
+            return None
+        p = self._dev(weights, "weights", torch.float32)
+        if tuple(weights.shape) != (n, top):
+            raise ValueError(f"weights has shape {tuple(weights.shape)}, needs {(n, top)}")
+        return p
+
+    def route_combine(self, y, route: Route, weights=None, out=None):
+        """The experts' answers y ([rows * top, dim], in their order) back in the
+        rows' order and summed with `weights` (float32 [rows, top], None: ones):
+        [rows, dim]."""
+        torch = self._torch
+        pp, _, n, top, _ = self._routed(route)
+        yp, yt, _, dim, ys = self._rows(y, "y", rows=n * top)
+        wp = self._weights(weights, n, top)
+        if out is None:
+            out = torch.empty((n, dim), dtype=y.dtype, device=y.device)
+        op, _, _, _, os_ = self._rows(out, "out", dim, n, y.dtype)
+        self._vec("route_combine", self._lib.hgb_route_combine, (y, *route, weights, out), yp, yt, ys, n, top, dim, pp, wp,
+                  op, os_)
+        return out
+
+    def route_combine_backward(self, grad, y, route: Route, weights=None, out=None):
+        """Gradients of route_combine: (dy [rows * top, dim], dweights [rows, top],
+        None without weights)."""
+        torch = self._torch
+        gp, gt, n, dim, gs = self._rows(grad, "grad")
+        pp, fp, n, top, E = self._routed(route, n)
+        yp, _, _, _, ys = self._rows(y, "y", dim, n * top, grad.dtype)
+        wp = self._weights(weights, n, top)
+        if out is None:
+            out = torch.empty((n * top, dim), dtype=grad.dtype, device=grad.device)
+        op, _, _, _, os_ = self._rows(out, "out", dim, n * top, grad.dtype)
+        dw = torch.empty((n, top), dtype=torch.float32, device=grad.device) if weights is not None else None
+        self._vec("route_combine_backward", self._lib.hgb_route_combine_backward, (grad, y, *route, weights, out, dw), gp,
+                  gt, gs, yp, ys, n, top, dim, pp, fp, E, wp, op, os_, dw.data_ptr() if dw is not None else None)
+        return out, dw

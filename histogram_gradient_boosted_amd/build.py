@@ -11,12 +11,13 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libhgb.so")
-SOURCES = [os.path.join(CSRC, "hgb.hip")]
+SOURCES = [os.path.join(CSRC, "hgb.hip"), os.path.join(CSRC, "hgb_vectors.hip")]
 # the LDS atomic-rate microbenchmark that bench.py reports beside the fill
 PROBE_LIB = os.path.join(PKG, "liblds_rate.so")
 PROBE_SOURCES = [os.path.join(CSRC, "lds_rate.hip")]
 HEADERS = [os.path.join(CSRC, "hgb_kernels.h"), os.path.join(CSRC, "hgb_layout.h"), os.path.join(CSRC, "hgb_plan.h"),
-           os.path.join(INCLUDE, "hgb.h")]
+           os.path.join(CSRC, "hgb_ctx.h"), os.path.join(CSRC, "hgb_vector_kernels.h"),
+           os.path.join(CSRC, "hgb_vector_plan.h"), os.path.join(INCLUDE, "hgb.h")]
 ARCH = "gfx950"
 
 HIPCC_FLAGS = [

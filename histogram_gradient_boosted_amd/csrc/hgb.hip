@@ -4,6 +4,7 @@
 // planning and the staging of small plans to the device.  The kernels live in
 // hgb_kernels.h.
 #include "hgb.h"
+#include "hgb_ctx.h"
 #include "hgb_kernels.h"
 #include "hgb_plan.h"
 
@@ -45,11 +46,6 @@ constexpr int64_t kTransposeMaxBlocks = 65536;   // k_transpose's blocks per fea
 // begin_tree's max pass: at most this many blocks, each writing its pair of
 // maxima for k_max_final.
 constexpr int kMaxBlocks = 4096;
-// Default fixed-point precision of begin_tree (bits below the largest value).
-constexpr int kDefaultPrecision = 30;
-constexpr int kStages = 16;
-constexpr int kEpochEvents = 4;
-constexpr int kEpochUses = 6;
 // Pinned host words (host_words, 16 of them): [0..1] the maxima, [2] the
 // error word, and the sequence numbers kernels post after their results.
 constexpr int kHostTreeSeq = 8;
@@ -69,149 +65,9 @@ static __device__ __align__(256) unsigned char scratch[kNoAllocScratchBytes];
 std::mutex g_scratch_mu;
 std::vector<void*> g_scratch_dev;   // per device: the address of `scratch` there
 
-struct Stage {
-    void* host = nullptr;   // pinned
-    void* dev = nullptr;
-    size_t cap = 0;
-    uint64_t release_seq = 0;    // the context's release count when its consumers were enqueued
-    bool pending = false;
-    const void* use = nullptr;   // what the kernels read: dev, or the pinned host copy
-};
-
 }  // namespace
 
-struct hgb_ctx {
-    int device = 0;
-    int n_cu = 256;
-    hipStream_t stream = nullptr;
-    std::string err;
-
-    // dataset plane: feature-major bins, plus a row-major copy when rows are
-    // narrow enough for a row to sit in a cache line or two
-    void* bins = nullptr;
-    void* bins_rm = nullptr;
-    int64_t rm_stride = 0;   // bytes per row of the row-major copy (multiple of 16)
-    int bin_bytes = 0;
-    int64_t n = 0;
-    int F = 0, B = 0, S = 0, has_missing = 0;
-    bool have_data = false;
-
-    // gradient plane
-    int2* q = nullptr;
-    int64_t q_cap = 0;
-    int precision = kDefaultPrecision;
-    int k_g = 0, k_h = 0;
-    bool have_tree = false;
-    // hgb_set_async_begin: begin_tree returns without waiting for the maxima;
-    // the host reads them (and checks them) at the next call that needs them
-    bool async_begin = false;
-    bool scales_pending = false;          // the current tree's maxima are not read yet
-    int tree_precision = 30;              // the precision the current tree was started with
-    hgb_status deferred = HGB_OK;         // a started tree's non-finite values, for hgb_sync
-    std::string deferred_msg;
-
-    // level scratch
-    int2* gh = nullptr;
-    int64_t gh_cap = 0;
-    long long* partial = nullptr;   // partial histograms of nodes split over several blocks
-    int64_t partial_cap = 0;
-    int32_t* part = nullptr;        // partition: chunk counts, left bases, per-node records
-    int64_t part_cap = 0;
-    int32_t* part_host = nullptr;   // pinned copy of the per-node records
-    int64_t part_host_cap = 0;
-    uint8_t* part_flags = nullptr;  // partition: direction of each position (1 = left)
-    int64_t part_flags_cap = 0;
-    FeatureBest* best = nullptr;
-    int64_t best_cap = 0;
-    long long* totals = nullptr;
-    int64_t totals_cap = 0;
-    double* level_terms = nullptr;        // find_level_split: [n_nodes][candidates] gains
-    int64_t level_terms_cap = 0;
-    LevelBest* level_best = nullptr;      // find_level_split: per-block winners
-    int64_t level_best_cap = 0;
-
-    // this device's copy of the no-allocation scratch array (set up by hgb_create)
-    unsigned char* noalloc_scratch = nullptr;
-
-    // small device words: [0..1] max patterns, [2] error flags, [3] 1 when the
-    // quantize pass must encode the rows again, [4..11] the quantize scales
-    // 2^k (also the next tree's guess) and the split scales 2^-k (four doubles)
-    uint32_t* dev_words = nullptr;
-    uint32_t* host_words = nullptr;   // pinned
-    uint32_t* max_part = nullptr;     // begin_tree: per-block maxima, 2 x kMaxBlocks
-    int32_t* rot = nullptr;           // per feature: the skipped slot (stored bins are rotated by it)
-    bool skip = false;                // the fills skip each feature's slot 0 (a hot slot exists)
-    hipEvent_t host_ready = nullptr;  // hgb_sync: the stream has drained
-
-    Stage stage[kStages];
-    int stage_next = 0;
-    // Stage releases record no event of their own (an event on the stream
-    // costs the device about 3 us): every kEpochUses releases, one event of a
-    // small ring marks the stream, and a stage is reused once an event
-    // recorded after its release has passed.
-    uint64_t stage_seq = 0;                     // releases so far
-    hipEvent_t epoch_ev[kEpochEvents] = {};
-    uint64_t epoch_seq[kEpochEvents] = {};      // releases covered by each event
-    int epoch_next = 0;
-    uint64_t last_epoch_seq = 0;
-    // sequence numbers of the results kernels post to pinned host memory:
-    // the maxima of each tree (host_words[8]) and the node records of each
-    // partition (host_words[9])
-    uint32_t tree_seq = 0;
-    uint32_t part_seq = 0;
-
-    // HGB_DEBUG_PLAN=1 in the environment prints each fill plan to stderr
-    bool debug_plan = false;
-    // kernels read the launch plans from pinned host memory (HGB_PLAN_HOST=0:
-    // from a device copy)
-    bool plan_host = true;
-    // HGB_FILL_TUNE="key=value,..." overrides the fill planner (developer
-    // tuning): root_lc, root_tile, root_ipc, level_lc, level_tile, level_ipc
-    // (ipc = items per CU), align (rows an item boundary is a multiple of),
-    // piece (fixed cost of a level item, in rows), il (row-major level fill,
-    // wide sums) and root_il (root fill, wide or packed sums): 1 slot-major
-    // interleaved tile, 0 feature-major; pair (row-major interleaved level
-    // fills with 32-byte chunks: 1 two lanes per row, 0 one); -1 keeps the
-    // planner's choice.
-    int tune[kTuneKeys] = {-1, -1, -1, -1, -1, -1, -1, -1, -1, -1, -1};
-
-    // optional per-kernel timing
-    bool prof = false;
-    std::vector<hipEvent_t> ev_pool;
-    // kernels whose dynamic-LDS limit has been raised, and to what
-    std::vector<std::pair<const void*, size_t>> lds_set;
-    std::vector<std::pair<hipEvent_t, hipEvent_t>> ev_pending[HGB_KERNEL_COUNT];
-    double prof_ms[HGB_KERNEL_COUNT] = {};
-    int64_t prof_launches[HGB_KERNEL_COUNT] = {};
-};
-
 namespace {
-
-hgb_status fail(hgb_ctx* c, hgb_status st, const char* fmt, ...)
-{
-    char buf[512];
-    va_list ap;
-    va_start(ap, fmt);
-    vsnprintf(buf, sizeof buf, fmt, ap);
-    va_end(ap);
-    c->err = buf;
-    return st;
-}
-
-#define HGB_HIP(c, expr)                                                                   \
-    do {                                                                                   \
-        hipError_t e_ = (expr);                                                            \
-        if (e_ != hipSuccess)                                                              \
-            return fail((c), HGB_E_DEVICE, "%s failed: %s", #expr, hipGetErrorString(e_)); \
-    } while (0)
-
-#define HGB_LAUNCHED(c, what)                                                              \
-    do {                                                                                   \
-        hipError_t e_ = hipGetLastError();                                                 \
-        if (e_ != hipSuccess)                                                              \
-            return fail((c), HGB_E_DEVICE, "launch of %s failed: %s", what,                \
-                        hipGetErrorString(e_));                                            \
-    } while (0)
 
 template <typename T>
 hgb_status grow(hgb_ctx* c, T** p, int64_t* cap, int64_t need)
@@ -386,45 +242,6 @@ hgb_status wait_here(hgb_ctx* c, hipEvent_t* ev)
     HGB_HIP(c, hipEventRecord(*ev, c->stream));
     return poll_event(c, *ev);
 }
-
-hipEvent_t pool_event(hgb_ctx* c)
-{
-    if (!c->ev_pool.empty()) {
-        hipEvent_t e = c->ev_pool.back();
-        c->ev_pool.pop_back();
-        return e;
-    }
-    hipEvent_t e = nullptr;
-    if (hipEventCreate(&e) != hipSuccess) return nullptr;
-    return e;
-}
-
-// Brackets the launches of one kernel class with events when timing is on.
-struct ProfScope {
-    hgb_ctx* c;
-    int kernel;
-    hipEvent_t start = nullptr;
-    ProfScope(hgb_ctx* ctx, int k) : c(ctx), kernel(k)
-    {
-        if (!c->prof) return;
-        start = pool_event(c);
-        if (start && hipEventRecord(start, c->stream) != hipSuccess) {
-            c->ev_pool.push_back(start);
-            start = nullptr;
-        }
-    }
-    ~ProfScope()
-    {
-        if (!start) return;
-        hipEvent_t stop = pool_event(c);
-        if (stop && hipEventRecord(stop, c->stream) == hipSuccess) {
-            c->ev_pending[kernel].emplace_back(start, stop);
-        } else {
-            c->ev_pool.push_back(start);
-            if (stop) c->ev_pool.push_back(stop);
-        }
-    }
-};
 
 int grid_for(int64_t work, int threads, int cap)
 {
@@ -994,18 +811,33 @@ static hgb_status take_flags(hgb_ctx* c)
     return HGB_OK;
 }
 
+// The same for the vector verbs' word.  A failed row index is reported first.
+static hgb_status take_vector_flags(hgb_ctx* c)
+{
+    const uint32_t flags = c->host_words[kWordVectors];
+    if (!flags) return HGB_OK;
+    k_clear_u32<<<1, 64, 0, c->stream>>>(c->dev_words + kWordVectors, 1);
+    HGB_LAUNCHED(c, "k_clear_u32");
+    HGB_HIP(c, hipStreamSynchronize(c->stream));
+    if (!c->err.empty()) return HGB_E_INVALID;
+    if (flags & kVecErrToken) return fail(c, HGB_E_INVALID, "a token outside [0, vocab) was taken as padding");
+    return fail(c, HGB_E_INVALID, "an expert outside [0, n_experts) was dropped");
+}
+
 hgb_status hgb_sync(hgb_ctx* c)
 {
     if (!c) return HGB_E_INVALID;
     c->err.clear();
     HGB_HIP(c, hipSetDevice(c->device));
-    k_post_u32<<<1, 64, 0, c->stream>>>(c->dev_words + 2, c->host_words + 2);
+    k_post_u32<<<1, 64, 0, c->stream>>>(c->dev_words, c->host_words, 2, kWordVectors);
     HGB_LAUNCHED(c, "k_post_u32");
     hgb_status st = wait_here(c, &c->host_ready);
     if (st != HGB_OK) return st;
     st = resolve_scales(c);
     if (st != HGB_OK) return st;
     st = take_flags(c);
+    const hgb_status vt = take_vector_flags(c);
+    if (st == HGB_OK) st = vt;
     if (c->deferred != HGB_OK) {   // reported once, before a skipped row index
         const hgb_status d = c->deferred;
         c->deferred = HGB_OK;

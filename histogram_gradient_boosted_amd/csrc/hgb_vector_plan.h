@@ -1,0 +1,127 @@
+// Launch plans of the vector verbs (embedding, layer norm, routing): sizes in,
+// launch shapes and workspace layouts out.  Plain C++, like hgb_plan.h: no HIP
+// header, so it is compiled and tested on the host alone.
+#pragma once
+
+#include <algorithm>
+#include <cstdint>
+
+namespace hgb {
+
+constexpr int64_t kVecMaxDim = 1 << 20;
+constexpr int64_t kVecMaxRows = 2147483647;      // rows, tokens and routed slots are int32
+constexpr int64_t kVecMaxVocab = 2147483646;     // the key of a dropped token is `vocab`
+constexpr int kRouteMaxExperts = 1023;           // one digit holds every expert and the dropped slots' key
+constexpr int kRouteMaxTop = 64;
+
+inline int64_t vec_up(int64_t v, int64_t m) { return (v + m - 1) / m * m; }
+inline int64_t vec_ceil(int64_t a, int64_t b) { return (a + b - 1) / b; }
+inline int vec_bits(int64_t v)   // bits of the values [0, v]
+{
+    int b = 1;
+    while (v >> b) ++b;
+    return b;
+}
+inline int vec_pow2(int64_t v)   // the smallest power of two >= v
+{
+    int p = 1;
+    while (p < v) p *= 2;
+    return p;
+}
+
+// Stable sort of n keys in [0, limit], least significant digit first.
+// Up to kSortSmall keys one block sorts in LDS; above that, each pass is a
+// count and a scatter over `blocks` equal shares of the keys, a share being
+// `tiles` tiles of kSortTile keys taken one after the other.
+constexpr int kSortThreads = 1024;
+constexpr int kSortItems = 16;
+constexpr int kSortTile = kSortThreads * kSortItems;
+constexpr int kSortSmall = kSortTile;
+constexpr int kSortSmallBits = 8;
+constexpr int kSortBits = 10;
+constexpr int kSortMaxBlocks = 512;
+
+struct SortPlan {
+    int64_t n = 0;
+    int passes = 0;
+    int bits = 0;        // of every digit
+    int radix = 0;       // digits' values: 2^bits, or limit + 1 for one pass
+    bool small = false;
+    int blocks = 0;
+    int tiles = 0;
+};
+
+inline SortPlan plan_sort(int64_t n, int64_t limit, bool one_pass)
+{
+    SortPlan p;
+    p.n = n;
+    p.small = n <= kSortSmall;
+    const int bits = vec_bits(limit);
+    const int most = one_pass ? kSortBits : p.small ? kSortSmallBits : kSortBits;
+    p.passes = (int)vec_ceil(bits, most);
+    p.bits = (int)vec_ceil(bits, p.passes);
+    p.radix = 1 << p.bits;
+    if (p.small) {
+        p.blocks = p.tiles = 1;
+        return p;
+    }
+    const int64_t tiles = vec_ceil(n, kSortTile);
+    p.tiles = (int)vec_ceil(tiles, kSortMaxBlocks);
+    p.blocks = (int)vec_ceil(tiles, p.tiles);
+    return p;
+}
+
+// LDS words in which the one-block sort exchanges its pairs between passes:
+// the launch and the kernel lay the rest out behind them.
+constexpr int small_pair_words(const SortPlan& p, int items, int threads) { return p.passes > 1 ? 2 * items * threads : 0; }
+
+// Lanes that share a row of `dim` values, V values a lane: a power of two up
+// to a wave; wider rows are cut into slices of 64 * V columns or walked in steps.
+inline int vec_group(int64_t dim, int V) { return std::min(64, vec_pow2(vec_ceil(dim, V))); }
+
+// The embedding's gradient: the sort, then chunks of sorted positions.
+// Workspace: counts | pairs A | pairs B | partial sums (two rows a chunk).
+struct EmbedPlan {
+    SortPlan sort;
+    int chunk = 1;             // sorted positions a group of lanes sums
+    int64_t chunks = 0;
+    int64_t part_stride = 0;   // floats of a partial row
+    int64_t off_a = 0, off_b = 0, off_part = 0, bytes = 0;
+};
+
+constexpr int kEmbedChunk = 64;          // largest chunk
+constexpr int64_t kEmbedWaves = 4096;    // chunks are halved until this many waves run (16 a CU)
+
+inline EmbedPlan plan_embed(int64_t n, int64_t vocab, int64_t dim)
+{
+    EmbedPlan p;
+    p.sort = plan_sort(n, vocab, false);
+    // The narrowest lanes' values (4) decide, so that the plan and the
+    // workspace do not depend on the types.
+    const int64_t group = vec_group(dim, 4), slices = vec_ceil(dim, 64 * 4);
+    p.chunk = kEmbedChunk;
+    while (p.chunk > 4 && vec_ceil(n, p.chunk) * group * slices / 64 < kEmbedWaves) p.chunk /= 2;
+    p.chunks = vec_ceil(n, p.chunk);
+    p.part_stride = vec_up(dim, 4);
+    p.off_a = vec_up((int64_t)p.sort.blocks * p.sort.radix * 4, 256);
+    p.off_b = p.off_a + vec_up(n * 8, 256);
+    p.off_part = p.off_b + (p.sort.small ? 0 : vec_up(n * 8, 256));
+    p.bytes = p.off_part + vec_up(p.chunks * 2 * p.part_stride * 4, 256);
+    return p;
+}
+
+// The routing's sort: counts only.
+inline int64_t route_workspace(int64_t slots, int experts)
+{
+    const SortPlan p = plan_sort(slots, experts, true);
+    return p.small ? 0 : vec_up((int64_t)p.blocks * p.radix * 4, 256);
+}
+
+// The layer norm's parameter gradients: `parts` partial rows of dim floats,
+// twice (weight, bias).
+constexpr int kNormParts = 256;
+
+inline int norm_parts(int64_t rows) { return (int)std::min<int64_t>(kNormParts, std::max<int64_t>(1, vec_ceil(rows, 16))); }
+inline int64_t norm_workspace(int64_t rows, int64_t dim) { return vec_up((int64_t)norm_parts(rows) * dim * 2 * 4, 256); }
+
+}  // namespace hgb

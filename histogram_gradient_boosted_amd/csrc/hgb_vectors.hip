@@ -1,0 +1,505 @@
+// hgb: the vector verbs of the C ABI (see include/hgb.h for the contract):
+// token embedding, layer norm and rows sorted by expert, with their gradients.
+//
+// Host side: argument checks and launches.  The kernels live in
+// hgb_vector_kernels.h, the launch plans in hgb_vector_plan.h.  Nothing here
+// allocates or waits: a verb's scratch is its caller's workspace, so calls may
+// be captured into a graph.
+#include "hgb.h"
+#include "hgb_ctx.h"
+#include "hgb_vector_kernels.h"
+#include "hgb_vector_plan.h"
+
+#include <hip/hip_runtime.h>
+
+#include <cmath>
+
+using namespace hgb;
+
+namespace {
+
+int elem_size(int32_t type) { return type == HGB_F32 ? 4 : 2; }
+bool is_type(int32_t type) { return type == HGB_F32 || type == HGB_BF16 || type == HGB_F16; }
+
+// A matrix argument's pointer, type and row stride.
+hgb_status check_rows(hgb_ctx* c, const char* verb, const char* name, const void* p, int32_t type, int64_t rows,
+                      int64_t dim, int64_t stride)
+{
+    if (!is_type(type)) return fail(c, HGB_E_INVALID, "%s: %s has an unknown type %d", verb, name, type);
+    if (stride < dim) return fail(c, HGB_E_INVALID, "%s: %s's rows overlap (stride %lld below %lld values)", verb, name,
+                                  (long long)stride, (long long)dim);
+    if (stride > ((int64_t)1 << 40)) return fail(c, HGB_E_INVALID, "%s: %s's stride is too large", verb, name);
+    if (rows > 0 && !p) return fail(c, HGB_E_INVALID, "%s: %s is null", verb, name);
+    if ((uintptr_t)p % elem_size(type)) return fail(c, HGB_E_INVALID, "%s: %s is not aligned to its type", verb, name);
+    return HGB_OK;
+}
+
+// The bytes of a matrix argument, from its first element to past its last.
+struct Span {
+    const char* begin;
+    int64_t bytes;
+};
+
+Span span(const void* p, int32_t type, int64_t rows, int64_t dim, int64_t stride)
+{
+    return {(const char*)p, p && rows > 0 ? ((rows - 1) * stride + dim) * elem_size(type) : 0};
+}
+
+hgb_status check_apart(hgb_ctx* c, const char* verb, const Span& out, const Span& in)
+{
+    if (out.bytes > 0 && in.bytes > 0 && out.begin < in.begin + in.bytes && in.begin < out.begin + out.bytes)
+        return fail(c, HGB_E_INVALID, "%s: an output overlaps an input", verb);
+    return HGB_OK;
+}
+
+hgb_status check_dim(hgb_ctx* c, const char* verb, int64_t rows, int64_t dim)
+{
+    if (rows < 0 || rows > kVecMaxRows)
+        return fail(c, HGB_E_INVALID, "%s: %lld rows are outside [0, 2^31)", verb, (long long)rows);
+    if (dim < 1) return fail(c, HGB_E_INVALID, "%s: dim must be positive", verb);
+    if (dim > kVecMaxDim) return fail(c, HGB_E_UNSUPPORTED, "%s: dim is above %lld", verb, (long long)kVecMaxDim);
+    return HGB_OK;
+}
+
+hgb_status check_workspace(hgb_ctx* c, const char* verb, const void* p, int64_t have, int64_t need)
+{
+    if (need > 0 && (!p || have < need))
+        return fail(c, HGB_E_INVALID, "%s: the workspace holds %lld bytes, needs %lld", verb, (long long)(p ? have : 0),
+                    (long long)need);
+    if ((uintptr_t)p % 16) return fail(c, HGB_E_INVALID, "%s: the workspace is not aligned to 16 bytes", verb);
+    return HGB_OK;
+}
+
+#define HGB_TRY(expr)                      \
+    do {                                   \
+        hgb_status s_ = (expr);            \
+        if (s_ != HGB_OK) return s_;       \
+    } while (0)
+
+// Runs an entry point's body: no C++ exception leaves the library.
+template <typename F>
+hgb_status guarded(hgb_ctx* c, F&& body)
+{
+    if (!c) return HGB_E_INVALID;
+    try {
+        c->err.clear();
+        return body();
+    } catch (...) {
+        return HGB_E_DEVICE;
+    }
+}
+
+// f with a null pointer of the type's element, so that generic code names it.
+template <typename F>
+hgb_status by_type(int32_t type, F&& f)
+{
+    if (type == HGB_F32) return f((float*)nullptr);
+    if (type == HGB_BF16) return f((__bf16*)nullptr);
+    return f((_Float16*)nullptr);
+}
+
+// The pairs of a table's type and its vectors' type: the same, or 16 bits
+// beside a 32-bit table.
+bool is_pair(int32_t table, int32_t vec) { return table == vec || table == HGB_F32; }
+
+template <typename F>
+hgb_status by_pair(int32_t table, int32_t vec, F&& f)
+{
+    if (table == HGB_F32) return by_type(vec, [&](auto* v) { return f((float*)nullptr, v); });
+    return by_type(vec, [&](auto* v) { return f(v, v); });
+}
+
+int log2_of(int p) { return 31 - __builtin_clz((unsigned)p); }
+
+hgb_status raise_lds(hgb_ctx* c, const void* fn, size_t bytes)
+{
+    if (bytes <= 65536) return HGB_OK;
+    for (auto& e : c->lds_set)
+        if (e.first == fn) {
+            if (e.second >= bytes) return HGB_OK;
+            HGB_HIP(c, hipFuncSetAttribute(fn, hipFuncAttributeMaxDynamicSharedMemorySize, (int)bytes));
+            e.second = bytes;
+            return HGB_OK;
+        }
+    HGB_HIP(c, hipFuncSetAttribute(fn, hipFuncAttributeMaxDynamicSharedMemorySize, (int)bytes));
+    c->lds_set.emplace_back(fn, bytes);
+    return HGB_OK;
+}
+
+// Blocks for a zero fill of `bytes`: a wave's 16-byte stores 16 times over, at most two blocks a CU.
+int zero_blocks(const hgb_ctx* c, int64_t bytes, int threads)
+{
+    return (int)std::min<int64_t>(2 * c->n_cu, vec_ceil(bytes, (int64_t)threads * 16 * 16));
+}
+
+template <int ITEMS>
+hgb_status launch_sort_small(hgb_ctx* c, const SortIn& in, const SortOut& out, const SortPlan& p, const ZeroFill& z)
+{
+    const int threads = (int)std::max<int64_t>(std::max<int64_t>(64, p.radix), vec_up(vec_ceil(in.n, ITEMS), 64));
+    const size_t lds = 4 * ((size_t)small_pair_words(p, ITEMS, threads) + (size_t)(threads / 64) * p.radix + p.radix + 16);
+    HGB_TRY(raise_lds(c, (const void*)k_sort_small<ITEMS>, lds));
+    k_sort_small<ITEMS><<<1 + zero_blocks(c, z.rows * z.cols * z.elem, threads), threads, lds, c->stream>>>(in, out, p, z);
+    HGB_LAUNCHED(c, "k_sort_small");
+    return HGB_OK;
+}
+
+// The sort of in.tokens into `out` (out.to: into whichever of a and b the
+// last pass writes; returned in *sorted), and the zeros beside it.
+hgb_status launch_sort(hgb_ctx* c, SortIn in, SortOut out, const SortPlan& p, const ZeroFill& z, uint32_t* counts, uint2* a,
+                       uint2* b, const uint2** sorted)
+{
+    if (p.small) {
+        if (a) out.to = a;
+        if (sorted) *sorted = a;
+        if (in.n <= 1024) return launch_sort_small<1>(c, in, out, p, z);
+        if (in.n <= 4096) return launch_sort_small<4>(c, in, out, p, z);
+        return launch_sort_small<kSortItems>(c, in, out, p, z);
+    }
+    const size_t lds = 4 * ((size_t)(kSortThreads / 64) * p.radix + 2 * (size_t)p.radix + 16);
+    HGB_TRY(raise_lds(c, (const void*)k_sort_scatter<true>, lds));
+    HGB_TRY(raise_lds(c, (const void*)k_sort_scatter<false>, lds));
+    for (int pass = 0; pass < p.passes; ++pass) {
+        const int shift = pass * p.bits;
+        if (a) out.to = pass & 1 ? b : a;
+        if (pass == 0) {
+            k_sort_count<true><<<p.blocks + zero_blocks(c, z.rows * z.cols * z.elem, kSortThreads), kSortThreads, 4 * p.radix,
+                                 c->stream>>>(in, p, shift, counts, z);
+            k_sort_scatter<true><<<p.blocks, kSortThreads, lds, c->stream>>>(in, out, p, shift, counts);
+        } else {
+            in.from = pass & 1 ? a : b;
+            k_sort_count<false><<<p.blocks, kSortThreads, 4 * p.radix, c->stream>>>(in, p, shift, counts, ZeroFill{});
+            k_sort_scatter<false><<<p.blocks, kSortThreads, lds, c->stream>>>(in, out, p, shift, counts);
+        }
+        HGB_LAUNCHED(c, "k_sort_scatter");
+    }
+    if (sorted) *sorted = out.to;
+    return HGB_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+hgb_status hgb_embed(hgb_ctx* c, const void* table, int32_t table_type, int64_t table_stride, int64_t vocab, int64_t dim,
+                     const int32_t* tokens, int64_t n_tokens, int32_t pad, float scale, void* out, int32_t out_type,
+                     int64_t out_stride)
+{
+    return guarded(c, [&]() -> hgb_status {
+        HGB_TRY(check_dim(c, "embed", n_tokens, dim));
+        if (vocab < 1 || vocab > kVecMaxVocab) return fail(c, HGB_E_INVALID, "embed: vocab is outside [1, 2^31 - 2]");
+        HGB_TRY(check_rows(c, "embed", "table", table, table_type, vocab, dim, table_stride));
+        HGB_TRY(check_rows(c, "embed", "out", out, out_type, n_tokens, dim, out_stride));
+        if (!is_pair(table_type, out_type))
+            return fail(c, HGB_E_UNSUPPORTED, "embed: out has the table's type, or 16 bits beside a 32-bit table");
+        if (n_tokens > 0 && !tokens) return fail(c, HGB_E_INVALID, "embed: tokens is null");
+        HGB_TRY(check_apart(c, "embed", span(out, out_type, n_tokens, dim, out_stride),
+                            span(table, table_type, vocab, dim, table_stride)));
+        if (n_tokens == 0) return HGB_OK;
+        HGB_HIP(c, hipSetDevice(c->device));
+        ProfScope ps(c, HGB_KERNEL_EMBED);
+        return by_pair(table_type, out_type, [&](auto* t, auto* u) -> hgb_status {
+            using T = std::remove_pointer_t<decltype(t)>;
+            using U = std::remove_pointer_t<decltype(u)>;
+            const int lg = log2_of(vec_group(dim, kVals<T, U>));
+            const int64_t groups = 256 >> lg;
+            // four rows a group keep four loads in flight, where the tokens still give every CU a few blocks
+            if (n_tokens >= groups * 4 * 8 * c->n_cu) {
+                k_embed<T, U, 4><<<(unsigned)vec_ceil(n_tokens, groups * 4), 256, 0, c->stream>>>(
+                    (const T*)table, table_stride, vocab, dim, tokens, n_tokens, pad, scale, (U*)out, out_stride, lg,
+                    c->dev_words + kWordVectors);
+            } else {
+                k_embed<T, U, 1><<<(unsigned)vec_ceil(n_tokens, groups), 256, 0, c->stream>>>(
+                    (const T*)table, table_stride, vocab, dim, tokens, n_tokens, pad, scale, (U*)out, out_stride, lg,
+                    c->dev_words + kWordVectors);
+            }
+            HGB_LAUNCHED(c, "k_embed");
+            return HGB_OK;
+        });
+    });
+}
+
+int64_t hgb_embed_backward_workspace(int64_t n_tokens, int64_t vocab, int64_t dim)
+{
+    if (n_tokens < 0 || n_tokens > kVecMaxRows || vocab < 1 || vocab > kVecMaxVocab || dim < 1 || dim > kVecMaxDim) return -1;
+    return n_tokens == 0 ? 0 : plan_embed(n_tokens, vocab, dim).bytes;
+}
+
+hgb_status hgb_embed_backward(hgb_ctx* c, const void* grad, int32_t grad_type, int64_t grad_stride, int64_t n_tokens,
+                              int64_t dim, const int32_t* tokens, int32_t pad, float scale, int64_t vocab, void* out,
+                              int32_t out_type, int64_t out_stride, void* workspace, int64_t workspace_bytes)
+{
+    return guarded(c, [&]() -> hgb_status {
+        HGB_TRY(check_dim(c, "embed_backward", n_tokens, dim));
+        if (vocab < 1 || vocab > kVecMaxVocab)
+            return fail(c, HGB_E_INVALID, "embed_backward: vocab is outside [1, 2^31 - 2]");
+        HGB_TRY(check_rows(c, "embed_backward", "grad", grad, grad_type, n_tokens, dim, grad_stride));
+        HGB_TRY(check_rows(c, "embed_backward", "out", out, out_type, vocab, dim, out_stride));
+        if (!is_pair(out_type, grad_type))
+            return fail(c, HGB_E_UNSUPPORTED, "embed_backward: grad has out's type, or 16 bits beside a 32-bit out");
+        if (n_tokens > 0 && !tokens) return fail(c, HGB_E_INVALID, "embed_backward: tokens is null");
+        HGB_TRY(check_apart(c, "embed_backward", span(out, out_type, vocab, dim, out_stride),
+                            span(grad, grad_type, n_tokens, dim, grad_stride)));
+        const EmbedPlan p = plan_embed(n_tokens, vocab, dim);
+        if (n_tokens > 0) HGB_TRY(check_workspace(c, "embed_backward", workspace, workspace_bytes, p.bytes));
+        HGB_HIP(c, hipSetDevice(c->device));
+        ProfScope ps(c, HGB_KERNEL_EMBED);
+        ZeroFill z;
+        z.out = out;
+        z.rows = vocab;
+        z.cols = dim;
+        z.stride = out_stride;
+        z.elem = elem_size(out_type);
+        if (n_tokens == 0) {
+            k_zero_rows<<<(unsigned)std::min<int64_t>(vec_ceil(vocab * dim * z.elem, 4096 * 4), 8 * c->n_cu), 256, 0,
+                          c->stream>>>(z);
+            HGB_LAUNCHED(c, "k_zero_rows");
+            return HGB_OK;
+        }
+        char* ws = (char*)workspace;
+        SortIn in{tokens, nullptr, n_tokens, vocab, pad, kVecErrToken, c->dev_words + kWordVectors};
+        const uint2* pairs = nullptr;
+        HGB_TRY(launch_sort(c, in, SortOut{}, p.sort, z, (uint32_t*)ws, (uint2*)(ws + p.off_a), (uint2*)(ws + p.off_b), &pairs));
+        return by_pair(out_type, grad_type, [&](auto* u, auto* t) -> hgb_status {
+            using U = std::remove_pointer_t<decltype(u)>;
+            using T = std::remove_pointer_t<decltype(t)>;
+            float* part = (float*)(ws + p.off_part);
+            constexpr int V = kVals<T, U>;
+            const int lg = log2_of(vec_group(dim, V));
+            const dim3 grid((unsigned)vec_ceil(p.chunks, 256 >> lg), (unsigned)vec_ceil(dim, (int64_t)V << lg));
+            k_embed_sum<T, U><<<grid, 256, 0, c->stream>>>(pairs, n_tokens, (const T*)grad, grad_stride, dim, vocab, scale,
+                                                           (U*)out, out_stride, part, p.part_stride, p.chunk, lg);
+            HGB_LAUNCHED(c, "k_embed_sum");
+            if (p.chunks > 1) {
+                const dim3 jgrid((unsigned)vec_ceil(p.chunks, kJoinChunks), (unsigned)vec_ceil(dim, 64));
+                k_embed_join<U><<<jgrid, 256, 0, c->stream>>>(pairs, n_tokens, dim, vocab, scale, (U*)out, out_stride, part,
+                                                              p.part_stride, p.chunk, p.chunks);
+                HGB_LAUNCHED(c, "k_embed_join");
+            }
+            return HGB_OK;
+        });
+    });
+}
+
+hgb_status hgb_layer_norm(hgb_ctx* c, const void* x, int32_t type, int64_t x_stride, int64_t n_rows, int64_t dim,
+                          const void* weight, const void* bias, int32_t param_type, float eps, void* y, int64_t y_stride,
+                          float* mean, float* rstd)
+{
+    return guarded(c, [&]() -> hgb_status {
+        HGB_TRY(check_dim(c, "layer_norm", n_rows, dim));
+        HGB_TRY(check_rows(c, "layer_norm", "x", x, type, n_rows, dim, x_stride));
+        HGB_TRY(check_rows(c, "layer_norm", "y", y, type, n_rows, dim, y_stride));
+        HGB_TRY(check_rows(c, "layer_norm", "weight", weight, param_type, 0, dim, dim));
+        HGB_TRY(check_rows(c, "layer_norm", "bias", bias, param_type, 0, dim, dim));
+        if (param_type != type && param_type != HGB_F32)
+            return fail(c, HGB_E_UNSUPPORTED, "layer_norm: the parameters have x's type, or 32 bits");
+        if (!(eps >= 0.0f) || std::isinf(eps)) return fail(c, HGB_E_INVALID, "layer_norm: eps must be finite and not negative");
+        if (n_rows == 0) return HGB_OK;
+        if (!mean || !rstd) return fail(c, HGB_E_INVALID, "layer_norm: mean or rstd is null");
+        HGB_TRY(check_apart(c, "layer_norm", span(y, type, n_rows, dim, y_stride), span(x, type, n_rows, dim, x_stride)));
+        HGB_HIP(c, hipSetDevice(c->device));
+        ProfScope ps(c, HGB_KERNEL_NORM);
+        return by_type(type, [&](auto* t) -> hgb_status {
+            using T = std::remove_pointer_t<decltype(t)>;
+            k_norm<T><<<(unsigned)std::min<int64_t>(n_rows, 65536), 256, 0, c->stream>>>(
+                (const T*)x, x_stride, n_rows, dim, weight, bias, param_type, eps, (T*)y, y_stride, mean, rstd);
+            HGB_LAUNCHED(c, "k_norm");
+            return HGB_OK;
+        });
+    });
+}
+
+int64_t hgb_layer_norm_backward_workspace(int64_t n_rows, int64_t dim)
+{
+    if (n_rows < 0 || n_rows > kVecMaxRows || dim < 1 || dim > kVecMaxDim) return -1;
+    return norm_workspace(n_rows, dim);
+}
+
+hgb_status hgb_layer_norm_backward(hgb_ctx* c, const void* grad, int64_t grad_stride, const void* x, int64_t x_stride,
+                                   int32_t type, int64_t n_rows, int64_t dim, const float* mean, const float* rstd,
+                                   const void* weight, int32_t param_type, void* dx, int64_t dx_stride, void* dweight,
+                                   void* dbias, void* workspace, int64_t workspace_bytes)
+{
+    return guarded(c, [&]() -> hgb_status {
+        const char* verb = "layer_norm_backward";
+        HGB_TRY(check_dim(c, verb, n_rows, dim));
+        HGB_TRY(check_rows(c, verb, "grad", grad, type, n_rows, dim, grad_stride));
+        HGB_TRY(check_rows(c, verb, "x", x, type, n_rows, dim, x_stride));
+        HGB_TRY(check_rows(c, verb, "dx", dx, type, n_rows, dim, dx_stride));
+        HGB_TRY(check_rows(c, verb, "weight", weight, param_type, 0, dim, dim));
+        HGB_TRY(check_rows(c, verb, "dweight", dweight, param_type, 0, dim, dim));
+        HGB_TRY(check_rows(c, verb, "dbias", dbias, param_type, 0, dim, dim));
+        if (param_type != type && param_type != HGB_F32)
+            return fail(c, HGB_E_UNSUPPORTED, "%s: the parameters have x's type, or 32 bits", verb);
+        if (n_rows > 0 && (!mean || !rstd)) return fail(c, HGB_E_INVALID, "%s: mean or rstd is null", verb);
+        HGB_TRY(check_apart(c, verb, span(dx, type, n_rows, dim, dx_stride), span(x, type, n_rows, dim, x_stride)));
+        HGB_TRY(check_apart(c, verb, span(dx, type, n_rows, dim, dx_stride), span(grad, type, n_rows, dim, grad_stride)));
+        const bool params = dweight || dbias;
+        if (params) HGB_TRY(check_workspace(c, verb, workspace, workspace_bytes, norm_workspace(n_rows, dim)));
+        HGB_HIP(c, hipSetDevice(c->device));
+        ProfScope ps(c, HGB_KERNEL_NORM);
+        const int parts = norm_parts(n_rows);
+        const unsigned tiles = (unsigned)vec_ceil(dim, 256);
+        HGB_TRY(by_type(type, [&](auto* t) -> hgb_status {
+            using T = std::remove_pointer_t<decltype(t)>;
+            if (n_rows > 0) {
+                k_norm_dx<T><<<(unsigned)std::min<int64_t>(n_rows, 65536), 256, 0, c->stream>>>(
+                    (const T*)grad, grad_stride, (const T*)x, x_stride, n_rows, dim, mean, rstd, weight, param_type, (T*)dx,
+                    dx_stride);
+                HGB_LAUNCHED(c, "k_norm_dx");
+            }
+            if (params) {
+                k_norm_params<T><<<dim3(tiles, (unsigned)parts), 256, 0, c->stream>>>(
+                    (const T*)grad, grad_stride, (const T*)x, x_stride, n_rows, dim, mean, rstd, (float*)workspace);
+                HGB_LAUNCHED(c, "k_norm_params");
+            }
+            return HGB_OK;
+        }));
+        if (params) {
+            k_norm_join<<<dim3(tiles, 2), 256, 0, c->stream>>>((const float*)workspace, parts, dim, dweight, dbias, param_type);
+            HGB_LAUNCHED(c, "k_norm_join");
+        }
+        return HGB_OK;
+    });
+}
+
+// The shape of a routing, as every routing verb takes it.
+static hgb_status check_route(hgb_ctx* c, const char* verb, int64_t n_rows, int32_t top, const int32_t* position)
+{
+    if (n_rows < 0 || n_rows > kVecMaxRows)
+        return fail(c, HGB_E_INVALID, "%s: %lld rows are outside [0, 2^31)", verb, (long long)n_rows);
+    if (top < 1) return fail(c, HGB_E_INVALID, "%s: top must be positive", verb);
+    if (top > kRouteMaxTop) return fail(c, HGB_E_UNSUPPORTED, "%s: top is above %d", verb, kRouteMaxTop);
+    if (n_rows * top > kVecMaxRows) return fail(c, HGB_E_INVALID, "%s: the slots do not fit 31 bits", verb);
+    if (n_rows > 0 && !position) return fail(c, HGB_E_INVALID, "%s: position is null", verb);
+    return HGB_OK;
+}
+
+static hgb_status check_experts(hgb_ctx* c, const char* verb, int32_t n_experts)
+{
+    if (n_experts < 1) return fail(c, HGB_E_INVALID, "%s: n_experts must be positive", verb);
+    if (n_experts > kRouteMaxExperts) return fail(c, HGB_E_UNSUPPORTED, "%s: n_experts is above %d", verb, kRouteMaxExperts);
+    return HGB_OK;
+}
+
+int64_t hgb_route_workspace(int64_t n_rows, int32_t top, int32_t n_experts)
+{
+    if (n_rows < 0 || n_rows > kVecMaxRows || top < 1 || top > kRouteMaxTop || n_rows * top > kVecMaxRows || n_experts < 1 ||
+        n_experts > kRouteMaxExperts)
+        return -1;
+    return route_workspace(n_rows * top, n_experts);
+}
+
+hgb_status hgb_route(hgb_ctx* c, const int32_t* experts, int64_t n_rows, int32_t top, int32_t n_experts, int32_t* order,
+                     int32_t* position, int32_t* offsets, void* workspace, int64_t workspace_bytes)
+{
+    return guarded(c, [&]() -> hgb_status {
+        HGB_TRY(check_route(c, "route", n_rows, top, position));
+        HGB_TRY(check_experts(c, "route", n_experts));
+        if (n_rows > 0 && (!experts || !order)) return fail(c, HGB_E_INVALID, "route: experts or order is null");
+        if (!offsets) return fail(c, HGB_E_INVALID, "route: offsets is null");
+        const int64_t n = n_rows * top;
+        HGB_TRY(check_workspace(c, "route", workspace, workspace_bytes, route_workspace(n, n_experts)));
+        HGB_HIP(c, hipSetDevice(c->device));
+        ProfScope ps(c, HGB_KERNEL_ROUTE);
+        SortIn in{experts, nullptr, n, n_experts, -1, kVecErrExpert, c->dev_words + kWordVectors};
+        SortOut out{nullptr, order, position, offsets};
+        return launch_sort(c, in, out, plan_sort(n, n_experts, true), ZeroFill{}, (uint32_t*)workspace, nullptr, nullptr, nullptr);
+    });
+}
+
+hgb_status hgb_route_gather(hgb_ctx* c, const void* x, int32_t type, int64_t x_stride, int64_t n_rows, int32_t top, int64_t dim,
+                            const int32_t* position, const int32_t* offsets, int32_t n_experts, void* out, int64_t out_stride)
+{
+    return guarded(c, [&]() -> hgb_status {
+        HGB_TRY(check_dim(c, "route_gather", n_rows, dim));
+        HGB_TRY(check_route(c, "route_gather", n_rows, top, position));
+        HGB_TRY(check_experts(c, "route_gather", n_experts));
+        HGB_TRY(check_rows(c, "route_gather", "x", x, type, n_rows, dim, x_stride));
+        HGB_TRY(check_rows(c, "route_gather", "out", out, type, n_rows, dim, out_stride));
+        if (n_rows == 0) return HGB_OK;
+        if (!offsets) return fail(c, HGB_E_INVALID, "route_gather: offsets is null");
+        HGB_TRY(check_apart(c, "route_gather", span(out, type, n_rows * top, dim, out_stride),
+                            span(x, type, n_rows, dim, x_stride)));
+        HGB_HIP(c, hipSetDevice(c->device));
+        ProfScope ps(c, HGB_KERNEL_ROUTE);
+        return by_type(type, [&](auto* t) -> hgb_status {
+            using T = std::remove_pointer_t<decltype(t)>;
+            const int lg = log2_of(vec_group(dim, kVals<T>));
+            k_route_gather<T><<<(unsigned)vec_ceil(n_rows, 256 >> lg), 256, 0, c->stream>>>(
+                (const T*)x, x_stride, n_rows, top, dim, position, offsets + n_experts, (T*)out, out_stride, lg);
+            HGB_LAUNCHED(c, "k_route_gather");
+            return HGB_OK;
+        });
+    });
+}
+
+static hgb_status combine(hgb_ctx* c, const char* verb, const void* y, int32_t type, int64_t y_stride, int64_t n_rows,
+                          int32_t top, int64_t dim, const int32_t* position, const float* weight, void* out,
+                          int64_t out_stride)
+{
+    HGB_TRY(check_dim(c, verb, n_rows, dim));
+    HGB_TRY(check_route(c, verb, n_rows, top, position));
+    HGB_TRY(check_rows(c, verb, "the sorted rows", y, type, n_rows, dim, y_stride));
+    HGB_TRY(check_rows(c, verb, "out", out, type, n_rows, dim, out_stride));
+    if (n_rows == 0) return HGB_OK;
+    HGB_TRY(check_apart(c, verb, span(out, type, n_rows, dim, out_stride), span(y, type, n_rows * top, dim, y_stride)));
+    HGB_HIP(c, hipSetDevice(c->device));
+    ProfScope ps(c, HGB_KERNEL_ROUTE);
+    return by_type(type, [&](auto* t) -> hgb_status {
+        using T = std::remove_pointer_t<decltype(t)>;
+        const int lg = log2_of(vec_group(dim, kVals<T>));
+        k_route_combine<T><<<(unsigned)vec_ceil(n_rows, 256 >> lg), 256, 0, c->stream>>>(
+            (const T*)y, y_stride, n_rows, top, dim, position, weight, (T*)out, out_stride, lg);
+        HGB_LAUNCHED(c, "k_route_combine");
+        return HGB_OK;
+    });
+}
+
+hgb_status hgb_route_combine(hgb_ctx* c, const void* y, int32_t type, int64_t y_stride, int64_t n_rows, int32_t top,
+                             int64_t dim, const int32_t* position, const float* weight, void* out, int64_t out_stride)
+{
+    return guarded(c, [&]() -> hgb_status {
+        return combine(c, "route_combine", y, type, y_stride, n_rows, top, dim, position, weight, out, out_stride);
+    });
+}
+
+hgb_status hgb_route_gather_backward(hgb_ctx* c, const void* grad, int32_t type, int64_t grad_stride, int64_t n_rows,
+                                     int32_t top, int64_t dim, const int32_t* position, void* dx, int64_t dx_stride)
+{
+    return guarded(c, [&]() -> hgb_status {
+        return combine(c, "route_gather_backward", grad, type, grad_stride, n_rows, top, dim, position, nullptr, dx, dx_stride);
+    });
+}
+
+hgb_status hgb_route_combine_backward(hgb_ctx* c, const void* grad, int32_t type, int64_t grad_stride, const void* y,
+                                      int64_t y_stride, int64_t n_rows, int32_t top, int64_t dim, const int32_t* position,
+                                      const int32_t* offsets, int32_t n_experts, const float* weight, void* dy,
+                                      int64_t dy_stride, float* dweight)
+{
+    return guarded(c, [&]() -> hgb_status {
+        const char* verb = "route_combine_backward";
+        HGB_TRY(check_dim(c, verb, n_rows, dim));
+        HGB_TRY(check_route(c, verb, n_rows, top, position));
+        HGB_TRY(check_experts(c, verb, n_experts));
+        HGB_TRY(check_rows(c, verb, "grad", grad, type, n_rows, dim, grad_stride));
+        HGB_TRY(check_rows(c, verb, "the sorted rows", y, type, dweight ? n_rows : 0, dim, y_stride));
+        HGB_TRY(check_rows(c, verb, "their gradient", dy, type, n_rows, dim, dy_stride));
+        if (n_rows == 0) return HGB_OK;
+        if (!offsets) return fail(c, HGB_E_INVALID, "%s: offsets is null", verb);
+        const Span to = span(dy, type, n_rows * top, dim, dy_stride);
+        HGB_TRY(check_apart(c, verb, to, span(grad, type, n_rows, dim, grad_stride)));
+        if (dweight) HGB_TRY(check_apart(c, verb, to, span(y, type, n_rows * top, dim, y_stride)));
+        HGB_HIP(c, hipSetDevice(c->device));
+        ProfScope ps(c, HGB_KERNEL_ROUTE);
+        return by_type(type, [&](auto* t) -> hgb_status {
+            using T = std::remove_pointer_t<decltype(t)>;
+            k_route_combine_grad<T><<<(unsigned)vec_ceil(n_rows, 4), 256, 0, c->stream>>>(
+                (const T*)grad, grad_stride, (const T*)y, y_stride, n_rows, top, dim, position, offsets + n_experts, weight,
+                (T*)dy, dy_stride, dweight);
+            HGB_LAUNCHED(c, "k_route_combine_grad");
+            return HGB_OK;
+        });
+    });
+}
+
+}  // extern "C"

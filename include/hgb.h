@@ -100,8 +100,9 @@ const char* hgb_last_error(const hgb_ctx* ctx);
  * context lifecycle": the host reads results once the level's work is done).
  * Returns HGB_E_NONFINITE if a tree started asynchronously since the previous
  * hgb_sync had a non-finite value (hgb_set_async_begin), else HGB_E_INVALID
- * if a kernel met a row index outside [0, n) since the previous hgb_sync
- * (those entries were skipped), HGB_E_DEVICE on a runtime error, else HGB_OK. */
+ * if a kernel met a row index outside [0, n), or a vector verb a token or
+ * expert out of range, since the previous hgb_sync (those entries were
+ * skipped), HGB_E_DEVICE on a runtime error, else HGB_OK. */
 hgb_status hgb_sync(hgb_ctx* ctx);
 
 /*
@@ -456,6 +457,164 @@ hgb_status hgb_grow_level(hgb_ctx* ctx, const int64_t* parent_hist_dev, const hg
                           int32_t oblivious);
 
 /*
+ * The vector verbs: learned vectors beside the trees.  A binned row is a list
+ * of tokens (a bin of a feature, or the leaf a tree sends the row to); a model
+ * on top of them looks up a vector for each token (hgb_embed), normalises the
+ * rows (hgb_layer_norm) and sends each row to some of its experts, a tree's
+ * leaves for instance, and back (hgb_route and the verbs after it).  Each has
+ * its gradient.  No page describes them; the definitions stand here.
+ *
+ * Conventions, besides those at the top:
+ *   - A context needs no upload_bins or begin_tree for them.
+ *   - Vectors are rows of `dim` values of an hgb_dtype, 1 <= dim <= 2^20, whose
+ *     starts lie `stride` elements apart (stride >= dim).  Buffers need only
+ *     their element's alignment.  Element offsets are 64-bit.
+ *   - Sums, means and variances are 32-bit floats; a result of fewer bits is
+ *     rounded once, to nearest even, when it is stored.  Sums run in a fixed
+ *     order: the same call gives the same bits.
+ *   - Scratch is the caller's: `workspace` (device, 16-byte aligned, at least
+ *     what the verb's _workspace function returns, which is -1 for sizes the
+ *     verb refuses).  Its contents mean nothing before and after the call, and
+ *     calls that may overlap need one each.  The verbs allocate nothing and
+ *     wait for nothing, so they can be captured into a graph.
+ *   - An output that overlaps an input is refused (HGB_E_INVALID); outputs may
+ *     not overlap each other.
+ *   - Zero rows or tokens are valid and leave only what the verb defines for
+ *     them.
+ */
+typedef enum {
+    HGB_F32 = 0,
+    HGB_BF16 = 1,
+    HGB_F16 = 2
+} hgb_dtype;
+
+/*
+ * out[i] = scale * table[tokens[i]] for i in [0, n_tokens).
+ *
+ * table_dev:  [vocab][dim], rows table_stride apart, type table_type.
+ * tokens_dev: int32 [n_tokens].  The token `pad` gives a row of zeros (the
+ *             table's row is not read); so does any other token outside
+ *             [0, vocab), which the next hgb_sync reports (HGB_E_INVALID).
+ * out_dev:    [n_tokens][dim], rows out_stride apart, type out_type: the
+ *             table's type, or a 16-bit type beside a 32-bit table.
+ * Errors: HGB_E_INVALID for null or misaligned pointers, vocab outside
+ *         [1, 2^31 - 2], n_tokens outside [0, 2^31), strides below dim;
+ *         HGB_E_UNSUPPORTED for dim above 2^20 or another pair of types.
+ */
+hgb_status hgb_embed(hgb_ctx* ctx, const void* table_dev, int32_t table_type, int64_t table_stride, int64_t vocab,
+                     int64_t dim, const int32_t* tokens_dev, int64_t n_tokens, int32_t pad, float scale, void* out_dev,
+                     int32_t out_type, int64_t out_stride);
+
+/*
+ * The table's gradient: out[v] = scale * the sum of grad[i] over the i with
+ * tokens[i] = v, for every v in [0, vocab): all of out is written, zeros for a
+ * token that does not occur.  The tokens are sorted (a stable sort, so a
+ * token's rows are added in an order that depends on the tokens alone).
+ * `pad` and tokens out of range contribute nothing; the latter are reported as
+ * by hgb_embed.
+ *
+ * grad_dev: [n_tokens][dim], type grad_type.  out_dev: [vocab][dim], type
+ * out_type: grad_type, or 32 bits beside 16-bit gradients.
+ * Errors: as for hgb_embed, and HGB_E_INVALID for a workspace too small.
+ */
+hgb_status hgb_embed_backward(hgb_ctx* ctx, const void* grad_dev, int32_t grad_type, int64_t grad_stride,
+                              int64_t n_tokens, int64_t dim, const int32_t* tokens_dev, int32_t pad, float scale,
+                              int64_t vocab, void* out_dev, int32_t out_type, int64_t out_stride, void* workspace_dev,
+                              int64_t workspace_bytes);
+int64_t hgb_embed_backward_workspace(int64_t n_tokens, int64_t vocab, int64_t dim);
+
+/*
+ * y = (x - mean) * rstd * weight + bias by rows, with mean = the row's mean,
+ * rstd = 1 / sqrt(the mean of (x - mean)^2 + eps).
+ *
+ * weight_dev, bias_dev: [dim] of type param_type (x's type, or HGB_F32), or
+ *                       NULL for ones and zeros.
+ * mean_dev, rstd_dev:   float [n_rows]; written, for the gradient.
+ * Errors: HGB_E_INVALID for null or misaligned pointers, n_rows outside
+ *         [0, 2^31), strides below dim, an eps that is negative or not finite;
+ *         HGB_E_UNSUPPORTED for dim above 2^20 or another param_type.
+ */
+hgb_status hgb_layer_norm(hgb_ctx* ctx, const void* x_dev, int32_t type, int64_t x_stride, int64_t n_rows, int64_t dim,
+                          const void* weight_dev, const void* bias_dev, int32_t param_type, float eps, void* y_dev,
+                          int64_t y_stride, float* mean_dev, float* rstd_dev);
+
+/*
+ * Gradients of hgb_layer_norm, with h = (x - mean) * rstd and
+ * a = grad * weight:
+ *   dx = rstd * (a - mean of a - h * mean of (a * h))   (means over the row)
+ *   dweight = the sum of grad * h, dbias = the sum of grad, over the rows
+ * (zeros for no rows).
+ *
+ * mean_dev, rstd_dev: as hgb_layer_norm wrote them.
+ * weight_dev:         as given to hgb_layer_norm, NULL for ones.
+ * dweight_dev, dbias_dev: [dim] of type param_type, or NULL when not wanted.
+ * Errors: as for hgb_layer_norm, and HGB_E_INVALID for a workspace too small
+ *         (none is needed when neither dweight nor dbias is wanted).
+ */
+hgb_status hgb_layer_norm_backward(hgb_ctx* ctx, const void* grad_dev, int64_t grad_stride, const void* x_dev,
+                                   int64_t x_stride, int32_t type, int64_t n_rows, int64_t dim, const float* mean_dev,
+                                   const float* rstd_dev, const void* weight_dev, int32_t param_type, void* dx_dev,
+                                   int64_t dx_stride, void* dweight_dev, void* dbias_dev, void* workspace_dev,
+                                   int64_t workspace_bytes);
+int64_t hgb_layer_norm_backward_workspace(int64_t n_rows, int64_t dim);
+
+/*
+ * Sort the slots of a batch by expert.  Row r asks `top` experts: slot
+ * s = r * top + k goes to experts[s].  The slots are ordered by expert, those
+ * of one expert by slot (a stable sort).  A slot whose expert is -1 is
+ * dropped; so is one with any other value outside [0, n_experts), which the
+ * next hgb_sync reports.
+ *
+ * experts_dev:  int32 [n_rows][top].
+ * order_dev:    int32 [n_rows * top]; the slot at each place, -1 past the last
+ *               routed one.
+ * position_dev: int32 [n_rows][top]; the place of each slot, -1 when dropped.
+ * offsets_dev:  int32 [n_experts + 1]; expert e's places are
+ *               [offsets[e], offsets[e + 1]).
+ * Errors: HGB_E_INVALID for null pointers, sizes below one (n_rows below
+ *         zero), n_rows * top above 2^31 - 1, a workspace too small;
+ *         HGB_E_UNSUPPORTED for n_experts above 1,023 or top above 64.
+ */
+hgb_status hgb_route(hgb_ctx* ctx, const int32_t* experts_dev, int64_t n_rows, int32_t top, int32_t n_experts,
+                     int32_t* order_dev, int32_t* position_dev, int32_t* offsets_dev, void* workspace_dev,
+                     int64_t workspace_bytes);
+int64_t hgb_route_workspace(int64_t n_rows, int32_t top, int32_t n_experts);
+
+/*
+ * The rows in the experts' order: out[position[r][k]] = x[r], and zeros at the
+ * places from offsets[n_experts] on, so that all n_rows * top rows of out are
+ * written.  x_dev: [n_rows][dim]; out_dev: [n_rows * top][dim], the same type.
+ * A position outside [0, n_rows * top) is taken as dropped, here and below.
+ * Errors: as for hgb_route and hgb_layer_norm.
+ */
+hgb_status hgb_route_gather(hgb_ctx* ctx, const void* x_dev, int32_t type, int64_t x_stride, int64_t n_rows, int32_t top,
+                            int64_t dim, const int32_t* position_dev, const int32_t* offsets_dev, int32_t n_experts,
+                            void* out_dev, int64_t out_stride);
+
+/* Its gradient: dx[r] = the sum over k of grad[position[r][k]], dropped slots
+ * left out (zeros when all are).  grad_dev: [n_rows * top][dim]. */
+hgb_status hgb_route_gather_backward(hgb_ctx* ctx, const void* grad_dev, int32_t type, int64_t grad_stride, int64_t n_rows,
+                                     int32_t top, int64_t dim, const int32_t* position_dev, void* dx_dev,
+                                     int64_t dx_stride);
+
+/* The experts' answers back in the rows' order, with weights applied:
+ * out[r] = the sum over k of weight[r][k] * y[position[r][k]], dropped slots
+ * left out.  y_dev: [n_rows * top][dim]; weight_dev: float [n_rows][top], or
+ * NULL for ones; out_dev: [n_rows][dim]. */
+hgb_status hgb_route_combine(hgb_ctx* ctx, const void* y_dev, int32_t type, int64_t y_stride, int64_t n_rows, int32_t top,
+                             int64_t dim, const int32_t* position_dev, const float* weight_dev, void* out_dev,
+                             int64_t out_stride);
+
+/* Its gradients: dy[position[r][k]] = weight[r][k] * grad[r], zeros at the
+ * places from offsets[n_experts] on, and dweight[r][k] = the product
+ * <grad[r], y[position[r][k]]>, 0 for a dropped slot.  dweight_dev may be NULL
+ * when not wanted (y_dev is not read then). */
+hgb_status hgb_route_combine_backward(hgb_ctx* ctx, const void* grad_dev, int32_t type, int64_t grad_stride,
+                                      const void* y_dev, int64_t y_stride, int64_t n_rows, int32_t top, int64_t dim,
+                                      const int32_t* position_dev, const int32_t* offsets_dev, int32_t n_experts,
+                                      const float* weight_dev, void* dy_dev, int64_t dy_stride, float* dweight_dev);
+
+/*
  * Per-kernel device timing ([bonsai-10] "The kernel": the pages' backend
  * prints an upload / gpu / unpack breakdown when asked).  When enabled, every
  * launch is bracketed by HIP events on the context's stream.
@@ -472,7 +631,10 @@ typedef enum {
     HGB_KERNEL_FILL_ROOT = 7,  /* the root's fill launches */
     HGB_KERNEL_FILL_LEVEL = 8, /* the fill launch of a level below the root */
     HGB_KERNEL_MERGE = 9,      /* merges of nodes' partial histograms */
-    HGB_KERNEL_COUNT = 10
+    HGB_KERNEL_EMBED = 10,     /* embed and embed_backward, each call */
+    HGB_KERNEL_NORM = 11,      /* layer_norm and layer_norm_backward, each call */
+    HGB_KERNEL_ROUTE = 12,     /* the route verbs, each call */
+    HGB_KERNEL_COUNT = 13
 } hgb_kernel;
 
 /* Turn timing on (nonzero) or off, and reset the counters. */
