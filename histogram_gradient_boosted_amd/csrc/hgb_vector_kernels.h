@@ -25,16 +25,24 @@ struct Vals {
 };
 
 template <int V, typename T>
-__device__ inline void load_vals(float (&r)[V], const T* p, int64_t left)
+__device__ inline typename Vals<T, V>::type load_raw(const T* p, int64_t left)
 {
+    typename Vals<T, V>::type v;
     if (left >= V) {
-        const typename Vals<T, V>::type v = *(const typename Vals<T, V>::type*)p;
-#pragma unroll
-        for (int k = 0; k < V; ++k) r[k] = (float)v[k];
+        v = *(const typename Vals<T, V>::type*)p;
     } else {
 #pragma unroll
-        for (int k = 0; k < V; ++k) r[k] = k < left ? (float)p[k] : 0.0f;
+        for (int k = 0; k < V; ++k) v[k] = k < left ? p[k] : (T)0.0f;
     }
+    return v;
+}
+
+template <int V, typename T>
+__device__ inline void load_vals(float (&r)[V], const T* p, int64_t left)
+{
+    const typename Vals<T, V>::type v = load_raw<V>(p, left);
+#pragma unroll
+    for (int k = 0; k < V; ++k) r[k] = (float)v[k];
 }
 
 template <int V, typename T>
@@ -50,6 +58,35 @@ __device__ inline void store_vals(const float (&r)[V], T* p, int64_t left)
         for (int k = 0; k < V; ++k)
             if (k < left) p[k] = (T)r[k];
     }
+}
+
+// x plus the value of the lane that CTRL names in its row of 16.
+template <int CTRL>
+__device__ inline float dpp_add(float x)
+{
+    return x + __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(x), CTRL, 0xf, 0xf, true));
+}
+
+// Sums over aligned groups of 2^log_group lanes; every lane of a group gets
+// its sum, the same bits.  Moves between lanes in the vector unit: no trip
+// through LDS as a shuffle makes.
+__device__ inline float group_sum(float x, int log_group)
+{
+    if (log_group > 0) x = dpp_add<0xb1>(x);    // lanes 1, 0, 3, 2 of a quad
+    if (log_group > 1) x = dpp_add<0x4e>(x);    // lanes 2, 3, 0, 1
+    if (log_group > 2) x = dpp_add<0x141>(x);   // the other quad of eight, mirrored
+    if (log_group > 3) x = dpp_add<0x140>(x);   // the other eight of sixteen
+    if (log_group > 4) {
+        const uint32_t u = __float_as_uint(x);
+        const auto v = __builtin_amdgcn_permlane16_swap(u, u, false, false);
+        x = __uint_as_float(v[0]) + __uint_as_float(v[1]);
+    }
+    if (log_group > 5) {
+        const uint32_t u = __float_as_uint(x);
+        const auto v = __builtin_amdgcn_permlane32_swap(u, u, false, false);
+        x = __uint_as_float(v[0]) + __uint_as_float(v[1]);
+    }
+    return x;
 }
 
 // ---------------------------------------------------------------------------
@@ -547,12 +584,7 @@ __device__ inline void set_param(void* p, int type, int64_t c, float v)
     else ((_Float16*)p)[c] = (_Float16)v;
 }
 
-__device__ inline float wave_sum(float x)
-{
-#pragma unroll
-    for (int d = 1; d < 64; d *= 2) x += __shfl_xor(x, d, 64);
-    return x;
-}
+__device__ inline float wave_sum(float x) { return group_sum(x, 6); }
 
 __device__ inline float block_sum(float x, float* tmp)   // 256 threads; tmp: four floats
 {
@@ -563,12 +595,291 @@ __device__ inline float block_sum(float x, float* tmp)   // 256 threads; tmp: fo
     return tmp[0] + tmp[1] + (tmp[2] + tmp[3]);
 }
 
-// One row a block, read again for each of its three sums (from the cache).
+// The columns of a row that a lane holds: K runs of V values, c(k) =
+// (k * span + lane) * V, where `span` lanes share the row: a part of a wave, a
+// wave (WPR = 1), or WPR waves, which are the whole block then.  With more than
+// 8 values a lane a row is longer than half of its columns (plan_norm), so that
+// only the upper half of the runs can pass its end.
+template <typename T, int NV, int WPR>
+struct NormShape {
+    static constexpr int V = kVals<T>, K = NV / V, kThreads = norm_threads(WPR);
+    static constexpr int kFull = NV > 8 ? K / 2 : 0;   // runs that lie in every row
+    static_assert(NV % V == 0, "whole vectors");
+};
+
+// How many of the values from column c on, of run k, lie in the row.
+template <typename S>
+__device__ inline int norm_left(int k, int c, int dim)
+{
+    return k < S::kFull ? S::V : dim - c;
+}
+
+// The row of a lane's span: the same for the whole wave unless several rows
+// share one (8 values a lane), and known to be, so that it stays in scalar
+// registers and the loads take a scalar base.
+template <int NV>
+__device__ inline int64_t norm_row(int64_t first, int span_index)
+{
+    return first + (NV > 8 ? __builtin_amdgcn_readfirstlane(span_index) : span_index);
+}
+
+// v, as a value of which the compiler knows nothing: what was computed from
+// it before does not stay in registers.
+template <typename R>
+__device__ inline R anew(R v)
+{
+    typedef uint32_t Words __attribute__((ext_vector_type(sizeof(R) / 4)));
+    Words u = __builtin_bit_cast(Words, v);
+    asm volatile("" : "+v"(u));
+    return __builtin_bit_cast(R, u);
+}
+
+// Sums of N values over the lanes that share a row; every lane gets them.
+// `tmp` ([2][N][WPR] floats) is used by turns, so that one barrier a sum is
+// enough.
+template <int N, int WPR>
+__device__ inline void row_sums(float (&x)[N], int log_group, float* tmp, int& turn)
+{
+#pragma unroll
+    for (int i = 0; i < N; ++i) x[i] = group_sum(x[i], log_group);
+    if (WPR > 1) {
+        float* t = tmp + turn * N * WPR;
+        turn ^= 1;
+        if ((threadIdx.x & 63) == 0)
+#pragma unroll
+            for (int i = 0; i < N; ++i) t[i * WPR + (threadIdx.x >> 6)] = x[i];
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            x[i] = 0.0f;
+#pragma unroll
+            for (int k = 0; k < WPR; ++k) x[i] += t[i * WPR + k];
+        }
+    }
+}
+
+// V values of a parameter from column c on; `other` where there is none.
+template <int V>
+__device__ inline void load_param(float (&r)[V], const void* p, int type, int64_t c, int64_t left, float other)
+{
+    if (!p || left <= 0) {
+#pragma unroll
+        for (int k = 0; k < V; ++k) r[k] = other;
+    } else if (type == 0) {
+        load_vals<V>(r, (const float*)p + c, left);
+    } else if (type == 1) {
+        load_vals<V>(r, (const __bf16*)p + c, left);
+    } else {
+        load_vals<V>(r, (const _Float16*)p + c, left);
+    }
+}
+
+// mean = sum x / dim, rstd = 1 / sqrt(sum (x - mean)^2 / dim + eps), y = (x -
+// mean) rstd weight + bias.  Bound by bytes: the row stays in registers between
+// its three uses, so x is read once, and the parameters stay there from row to
+// row.  A wave takes a row of up to 2,048 values: its sums need no barrier.
+// 32,768 rows of 1,792 bf16 values: 42.5 us, 5.5 TB/s (a large copy: 4.9); a
+// block a row that read the row three times took 235 us.
+template <typename T, int NV, int WPR>
+__global__ __launch_bounds__(norm_threads(WPR)) void k_norm(
+    const T* __restrict__ x, int64_t x_stride, int64_t rows, int dim, const void* __restrict__ weight,
+    const void* __restrict__ bias, int wtype, float eps, T* __restrict__ y, int64_t y_stride, float* __restrict__ mean,
+    float* __restrict__ rstd, int log_group)
+{
+    using S = NormShape<T, NV, WPR>;
+    constexpr int V = S::V, K = S::K;
+    __shared__ float tmp[2 * WPR];
+    int turn = 0;
+    const int span = WPR > 1 ? S::kThreads : 1 << log_group, lane = threadIdx.x & (span - 1);
+    const int per = S::kThreads / span;   // rows a block takes at a time
+    float w[K][V], b[K][V];
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+        const int c = (k * span + lane) * V;
+        load_param<V>(w[k], weight, wtype, c, dim - c, 1.0f);
+        load_param<V>(b[k], bias, wtype, c, dim - c, 0.0f);
+    }
+    for (int64_t r = norm_row<NV>((int64_t)blockIdx.x * per, threadIdx.x / span); r < rows; r += (int64_t)gridDim.x * per) {
+        const T* p = x + r * x_stride;
+        float v[K][V], s[1] = {0.0f};
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            const int c = (k * span + lane) * V;
+            load_vals<V>(v[k], p + c, norm_left<S>(k, c, dim));
+        }
+#pragma unroll
+        for (int k = 0; k < K; ++k)
+#pragma unroll
+            for (int i = 0; i < V; ++i) s[0] += v[k][i];
+        row_sums<1, WPR>(s, log_group, tmp, turn);
+        const float m = s[0] / (float)dim;
+        s[0] = 0.0f;
+#pragma unroll
+        for (int k = 0; k < K; ++k)
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                v[k][i] -= m;
+                if (k < S::kFull || (k * span + lane) * V + i < dim) s[0] = fmaf(v[k][i], v[k][i], s[0]);
+            }
+        row_sums<1, WPR>(s, log_group, tmp, turn);
+        const float q = 1.0f / sqrtf(s[0] / (float)dim + eps);
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            const int c = (k * span + lane) * V;
+#pragma unroll
+            for (int i = 0; i < V; ++i) v[k][i] = fmaf(v[k][i] * q, w[k][i], b[k][i]);
+            store_vals<V>(v[k], y + r * y_stride + c, norm_left<S>(k, c, dim));
+        }
+        if (lane == 0) {
+            mean[r] = m;
+            rstd[r] = q;
+        }
+    }
+}
+
+// dx by rows, and the parameters' gradients over the block's rows in the same
+// pass: a lane keeps the sums of its columns in registers, the block's waves
+// join theirs through LDS at the end (a fixed tree), and part
+// [blocks][2][dim] holds the blocks' sums for k_norm_join.  Bound by bytes,
+// each read and written once.  32,768 rows of 1,792 bf16 values: 78 us, 4.5
+// TB/s, and 5 us for k_norm_join; 120 us without the row ahead, 94 us with both
+// forms of the row in registers (which spill), 298 us as passes of their own
+// for dx and for the sums.
+template <typename T, int NV, int WPR>
+__global__ __launch_bounds__(norm_threads(WPR)) void k_norm_grad(
+    const T* __restrict__ grad, int64_t grad_stride, const T* __restrict__ x, int64_t x_stride, int64_t rows, int dim,
+    const float* __restrict__ mean, const float* __restrict__ rstd, const void* __restrict__ weight, int wtype,
+    T* __restrict__ dx, int64_t dx_stride, float* __restrict__ part, int log_group)
+{
+    using S = NormShape<T, NV, WPR>;
+    constexpr int V = S::V, K = S::K, WAVES = S::kThreads / 64;
+    __shared__ float tmp[2 * 2 * WPR];
+    __shared__ float sums[WPR > 1 ? 1 : WAVES / 2][WPR > 1 ? 1 : 64 * NV];
+    int turn = 0;
+    const int span = WPR > 1 ? S::kThreads : 1 << log_group, lane = threadIdx.x & (span - 1);
+    const int per = S::kThreads / span;
+    float w[K][V], dw[K][V], db[K][V];
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+        const int c = (k * span + lane) * V;
+        load_param<V>(w[k], weight, wtype, c, dim - c, 1.0f);
+#pragma unroll
+        for (int i = 0; i < V; ++i) dw[k][i] = db[k][i] = 0.0f;
+    }
+    // The next row is on its way while a row is summed: with two waves on a
+    // SIMD (the sums take the registers) nothing else hides its latency.  A row
+    // is held as it was loaded and converted twice, for the same reason.  Where
+    // the registers do not reach for that (32 values of 32 bits; the 128 a lane
+    // of a block of 16 waves), rows come one at a time, to more waves.
+    constexpr bool AHEAD = WPR < 16 && (sizeof(T) < 4 || NV < 32);
+    using Raw = typename Vals<T, V>::type;
+    Raw next_g[K], next_x[K];
+    float next_m, next_q;
+    auto fetch = [&](int64_t r) {
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            const int c = (k * span + lane) * V;
+            const int left = norm_left<S>(k, c, dim);
+            next_g[k] = load_raw<V>(grad + r * grad_stride + c, left);
+            next_x[k] = load_raw<V>(x + r * x_stride + c, left);
+        }
+        next_m = mean[r];
+        next_q = rstd[r];
+    };
+    const int64_t step = (int64_t)gridDim.x * per;
+    int64_t r = norm_row<NV>((int64_t)blockIdx.x * per, threadIdx.x / span);
+    if (AHEAD && r < rows) fetch(r);
+    for (; r < rows; r += step) {
+        if (!AHEAD) fetch(r);
+        Raw g[K], p[K];
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            g[k] = next_g[k];
+            p[k] = next_x[k];
+        }
+        const float m = next_m, q = next_q;
+        if (AHEAD && r + step < rows) fetch(r + step);
+        float s[2] = {0.0f, 0.0f};
+#pragma unroll
+        for (int k = 0; k < K; ++k)
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                float h = ((float)p[k][i] - m) * q;
+                // past the row's end g is 0, and h too: not a mean or rstd that may be infinite
+                if (k >= S::kFull && (k * span + lane) * V + i >= dim) h = 0.0f;
+                const float u = (float)g[k][i], v = u * w[k][i];
+                dw[k][i] = fmaf(u, h, dw[k][i]);
+                db[k][i] += u;
+                s[0] += v;
+                s[1] = fmaf(v, h, s[1]);
+            }
+        row_sums<2, WPR>(s, log_group, tmp, turn);
+        const float a = s[0] / (float)dim, b = s[1] / (float)dim;
+        if (sizeof(T) < 4) {
+            // the row's values are converted anew from here on
+#pragma unroll
+            for (int k = 0; k < K; ++k) {
+                g[k] = anew(g[k]);
+                p[k] = anew(p[k]);
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            const int c = (k * span + lane) * V;
+            float v[V];
+#pragma unroll
+            for (int i = 0; i < V; ++i) v[i] = q * fmaf(((float)p[k][i] - m) * q, -b, (float)g[k][i] * w[k][i] - a);
+            store_vals<V>(v, dx + r * dx_stride + c, norm_left<S>(k, c, dim));
+        }
+    }
+    if (!part) return;
+    if (WPR == 1) {
+        const int wave = threadIdx.x >> 6, l = threadIdx.x & 63;
+        for (int d = span; d < 64; d *= 2)
+#pragma unroll
+            for (int k = 0; k < K; ++k)
+#pragma unroll
+                for (int i = 0; i < V; ++i) {
+                    dw[k][i] += __shfl_xor(dw[k][i], d, 64);
+                    db[k][i] += __shfl_xor(db[k][i], d, 64);
+                }
+        auto join = [&](float (&v)[K][V], int half) {
+            if (wave >= half && wave < 2 * half)
+#pragma unroll
+                for (int k = 0; k < K; ++k)
+#pragma unroll
+                    for (int i = 0; i < V; ++i) sums[wave - half][(k * V + i) * 64 + l] = v[k][i];
+            __syncthreads();
+            if (wave < half)
+#pragma unroll
+                for (int k = 0; k < K; ++k)
+#pragma unroll
+                    for (int i = 0; i < V; ++i) v[k][i] += sums[wave][(k * V + i) * 64 + l];
+            __syncthreads();
+        };
+#pragma unroll
+        for (int half = WAVES / 2; half > 0; half /= 2) {
+            join(dw, half);
+            join(db, half);
+        }
+        if ((int)threadIdx.x >= span) return;
+    }
+    float* to = part + (int64_t)blockIdx.x * 2 * dim;
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+        const int c = (k * span + lane) * V;
+        store_vals<V>(dw[k], to + c, dim - c);
+        store_vals<V>(db[k], to + dim + c, dim - c);
+    }
+}
+
+// Rows that registers do not hold (dim above kNormMaxDim): one row a block,
+// read again for each of its sums (from the cache).
 template <typename T>
-__global__ __launch_bounds__(256) void k_norm(const T* __restrict__ x, int64_t x_stride, int64_t rows, int64_t dim,
-                                              const void* __restrict__ weight, const void* __restrict__ bias, int wtype,
-                                              float eps, T* __restrict__ y, int64_t y_stride, float* __restrict__ mean,
-                                              float* __restrict__ rstd)
+__global__ __launch_bounds__(256) void k_norm_wide(const T* __restrict__ x, int64_t x_stride, int64_t rows, int64_t dim,
+                                                   const void* __restrict__ weight, const void* __restrict__ bias,
+                                                   int wtype, float eps, T* __restrict__ y, int64_t y_stride,
+                                                   float* __restrict__ mean, float* __restrict__ rstd)
 {
     __shared__ float tmp[4];
     for (int64_t r = blockIdx.x; r < rows; r += gridDim.x) {
@@ -596,11 +907,11 @@ __global__ __launch_bounds__(256) void k_norm(const T* __restrict__ x, int64_t x
 }
 
 template <typename T>
-__global__ __launch_bounds__(256) void k_norm_dx(const T* __restrict__ grad, int64_t grad_stride, const T* __restrict__ x,
-                                                 int64_t x_stride, int64_t rows, int64_t dim,
-                                                 const float* __restrict__ mean, const float* __restrict__ rstd,
-                                                 const void* __restrict__ weight, int wtype, T* __restrict__ dx,
-                                                 int64_t dx_stride)
+__global__ __launch_bounds__(256) void k_norm_wide_dx(const T* __restrict__ grad, int64_t grad_stride,
+                                                      const T* __restrict__ x, int64_t x_stride, int64_t rows,
+                                                      int64_t dim, const float* __restrict__ mean,
+                                                      const float* __restrict__ rstd, const void* __restrict__ weight,
+                                                      int wtype, T* __restrict__ dx, int64_t dx_stride)
 {
     __shared__ float tmp[4];
     for (int64_t r = blockIdx.x; r < rows; r += gridDim.x) {
@@ -625,10 +936,10 @@ __global__ __launch_bounds__(256) void k_norm_dx(const T* __restrict__ grad, int
 // Partial sums of the parameters' gradients over one share of the rows: part
 // [parts][2][dim].
 template <typename T>
-__global__ __launch_bounds__(256) void k_norm_params(const T* __restrict__ grad, int64_t grad_stride,
-                                                     const T* __restrict__ x, int64_t x_stride, int64_t rows, int64_t dim,
-                                                     const float* __restrict__ mean, const float* __restrict__ rstd,
-                                                     float* __restrict__ part)
+__global__ __launch_bounds__(256) void k_norm_wide_params(const T* __restrict__ grad, int64_t grad_stride,
+                                                          const T* __restrict__ x, int64_t x_stride, int64_t rows,
+                                                          int64_t dim, const float* __restrict__ mean,
+                                                          const float* __restrict__ rstd, float* __restrict__ part)
 {
     const int64_t c = (int64_t)blockIdx.x * 256 + threadIdx.x;
     if (c >= dim) return;
@@ -642,16 +953,28 @@ __global__ __launch_bounds__(256) void k_norm_params(const T* __restrict__ grad,
     part[((int64_t)blockIdx.y * 2 + 1) * dim + c] = b;
 }
 
+// The parameters' gradients from the blocks' sums: 16 columns a block, 16
+// threads a column, each over every 16th part, joined by a fixed tree.
 __global__ __launch_bounds__(256) void k_norm_join(const float* __restrict__ part, int parts, int64_t dim,
                                                    void* __restrict__ dweight, void* __restrict__ dbias, int wtype)
 {
-    const int64_t c = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    if (c >= dim) return;
+    __shared__ float sums[16][17];
+    const int col = threadIdx.x & 15, row = threadIdx.x >> 4;
+    const int64_t c = (int64_t)blockIdx.x * 16 + col;
     void* out = blockIdx.y == 0 ? dweight : dbias;
     if (!out) return;
     float s = 0.0f;
-    for (int k = 0; k < parts; ++k) s += part[((int64_t)k * 2 + blockIdx.y) * dim + c];
-    set_param(out, wtype, c, s);
+    if (c < dim) {
+#pragma unroll 8
+        for (int k = row; k < parts; k += 16) s += part[((int64_t)k * 2 + blockIdx.y) * dim + c];
+    }
+    sums[row][col] = s;
+    __syncthreads();
+    for (int half = 8; half > 0; half /= 2) {
+        if (row < half) sums[row][col] += sums[row + half][col];
+        __syncthreads();
+    }
+    if (row == 0 && c < dim) set_param(out, wtype, c, sums[0][col]);
 }
 
 // ---------------------------------------------------------------------------

@@ -117,11 +117,47 @@ inline int64_t route_workspace(int64_t slots, int experts)
     return p.small ? 0 : vec_up((int64_t)p.blocks * p.radix * 4, 256);
 }
 
-// The layer norm's parameter gradients: `parts` partial rows of dim floats,
-// twice (weight, bias).
-constexpr int kNormParts = 256;
+// The layer norm's launch: `values` of a row in each lane's registers, a row
+// over 2^log_group lanes of a wave (waves = 1) or over all `waves` of a block.
+// `values` = 0: the row is too wide for registers and is read again.
+constexpr int kNormThreads = 512;      // of a block whose waves take a row each
+constexpr int kNormMaxDim = 16384;     // 16 values a lane, 16 waves (32 spill: a block of 16 waves has 128 registers a lane)
+constexpr int kNormParts = 256;        // blocks of the backward pass: one a CU
+constexpr int norm_threads(int waves) { return waves > 1 ? 64 * waves : kNormThreads; }
 
+struct NormPlan {
+    int values = 0;
+    int waves = 1;
+    int log_group = 6;
+    int per_block = 1;   // rows of a block at a time
+};
+
+inline NormPlan plan_norm(int64_t dim)
+{
+    NormPlan p;
+    if (dim > kNormMaxDim) return p;
+    p.waves = dim <= 2048 ? 1 : dim <= 8192 ? 4 : 16;
+    const int64_t lane = vec_ceil(dim, 64 * p.waves);   // values a lane
+    p.values = lane <= 8 ? 8 : lane <= 16 ? 16 : 32;
+    if (dim <= 512) {
+        p.log_group = 0;
+        while ((8 << p.log_group) < dim) ++p.log_group;
+    }
+    p.per_block = p.waves > 1 ? 1 : kNormThreads >> p.log_group;
+    return p;
+}
+
+// Partial rows of the parameters' gradients, [2][dim] floats each: of the wide
+// rows' kernel (shares of 16 rows and more), and the register kernel's blocks.
 inline int norm_parts(int64_t rows) { return (int)std::min<int64_t>(kNormParts, std::max<int64_t>(1, vec_ceil(rows, 16))); }
-inline int64_t norm_workspace(int64_t rows, int64_t dim) { return vec_up((int64_t)norm_parts(rows) * dim * 2 * 4, 256); }
+inline int norm_blocks(int64_t rows, const NormPlan& p)
+{
+    const int64_t most = p.waves == 4 ? 2 * kNormParts : kNormParts;   // blocks of four waves: two a CU
+    return (int)std::min<int64_t>(most, std::max<int64_t>(1, vec_ceil(rows, p.per_block)));
+}
+inline int64_t norm_workspace(int64_t rows, int64_t dim)
+{
+    return vec_up((int64_t)std::max(norm_parts(rows), norm_blocks(rows, plan_norm(dim))) * dim * 2 * 4, 256);
+}
 
 }  // namespace hgb

@@ -13,6 +13,7 @@
 #include <hip/hip_runtime.h>
 
 #include <cmath>
+#include <type_traits>
 
 using namespace hgb;
 
@@ -107,6 +108,20 @@ hgb_status by_pair(int32_t table, int32_t vec, F&& f)
 {
     if (table == HGB_F32) return by_type(vec, [&](auto* v) { return f((float*)nullptr, v); });
     return by_type(vec, [&](auto* v) { return f(v, v); });
+}
+
+// f with the plan's values a lane and waves a row as types.
+template <typename F>
+void by_shape(const NormPlan& p, F&& f)
+{
+    auto with = [&](auto values) {
+        if (p.waves == 4) f(values, std::integral_constant<int, 4>());
+        else f(values, std::integral_constant<int, 1>());
+    };
+    if (p.waves == 16) f(std::integral_constant<int, 16>(), std::integral_constant<int, 16>());
+    else if (p.values == 8) f(std::integral_constant<int, 8>(), std::integral_constant<int, 1>());
+    else if (p.values == 16) with(std::integral_constant<int, 16>());
+    else with(std::integral_constant<int, 32>());
 }
 
 int log2_of(int p) { return 31 - __builtin_clz((unsigned)p); }
@@ -300,8 +315,19 @@ hgb_status hgb_layer_norm(hgb_ctx* c, const void* x, int32_t type, int64_t x_str
         ProfScope ps(c, HGB_KERNEL_NORM);
         return by_type(type, [&](auto* t) -> hgb_status {
             using T = std::remove_pointer_t<decltype(t)>;
-            k_norm<T><<<(unsigned)std::min<int64_t>(n_rows, 65536), 256, 0, c->stream>>>(
-                (const T*)x, x_stride, n_rows, dim, weight, bias, param_type, eps, (T*)y, y_stride, mean, rstd);
+            const NormPlan p = plan_norm(dim);
+            if (!p.values) {
+                k_norm_wide<T><<<(unsigned)std::min<int64_t>(n_rows, 65536), 256, 0, c->stream>>>(
+                    (const T*)x, x_stride, n_rows, dim, weight, bias, param_type, eps, (T*)y, y_stride, mean, rstd);
+            } else {
+                by_shape(p, [&](auto values, auto waves) {
+                    constexpr int NV = decltype(values)::value, WPR = decltype(waves)::value, THREADS = norm_threads(WPR);
+                    const unsigned blocks =
+                        (unsigned)std::min<int64_t>(vec_ceil(n_rows, p.per_block), (int64_t)c->n_cu * 2048 / THREADS);
+                    k_norm<T, NV, WPR><<<blocks, THREADS, 0, c->stream>>>((const T*)x, x_stride, n_rows, (int)dim, weight, bias,
+                                                                          param_type, eps, (T*)y, y_stride, mean, rstd, p.log_group);
+                });
+            }
             HGB_LAUNCHED(c, "k_norm");
             return HGB_OK;
         });
@@ -337,25 +363,36 @@ hgb_status hgb_layer_norm_backward(hgb_ctx* c, const void* grad, int64_t grad_st
         if (params) HGB_TRY(check_workspace(c, verb, workspace, workspace_bytes, norm_workspace(n_rows, dim)));
         HGB_HIP(c, hipSetDevice(c->device));
         ProfScope ps(c, HGB_KERNEL_NORM);
-        const int parts = norm_parts(n_rows);
-        const unsigned tiles = (unsigned)vec_ceil(dim, 256);
+        const NormPlan p = plan_norm(dim);
+        const int parts = p.values ? norm_blocks(n_rows, p) : norm_parts(n_rows);
         HGB_TRY(by_type(type, [&](auto* t) -> hgb_status {
             using T = std::remove_pointer_t<decltype(t)>;
-            if (n_rows > 0) {
-                k_norm_dx<T><<<(unsigned)std::min<int64_t>(n_rows, 65536), 256, 0, c->stream>>>(
-                    (const T*)grad, grad_stride, (const T*)x, x_stride, n_rows, dim, mean, rstd, weight, param_type, (T*)dx,
-                    dx_stride);
-                HGB_LAUNCHED(c, "k_norm_dx");
-            }
-            if (params) {
-                k_norm_params<T><<<dim3(tiles, (unsigned)parts), 256, 0, c->stream>>>(
-                    (const T*)grad, grad_stride, (const T*)x, x_stride, n_rows, dim, mean, rstd, (float*)workspace);
-                HGB_LAUNCHED(c, "k_norm_params");
+            const T* g = (const T*)grad;
+            if (!p.values) {
+                if (n_rows > 0) {
+                    k_norm_wide_dx<T><<<(unsigned)std::min<int64_t>(n_rows, 65536), 256, 0, c->stream>>>(
+                        g, grad_stride, (const T*)x, x_stride, n_rows, dim, mean, rstd, weight, param_type, (T*)dx, dx_stride);
+                    HGB_LAUNCHED(c, "k_norm_wide_dx");
+                }
+                if (params) {
+                    k_norm_wide_params<T><<<dim3((unsigned)vec_ceil(dim, 256), (unsigned)parts), 256, 0, c->stream>>>(
+                        g, grad_stride, (const T*)x, x_stride, n_rows, dim, mean, rstd, (float*)workspace);
+                    HGB_LAUNCHED(c, "k_norm_wide_params");
+                }
+            } else if (n_rows > 0 || params) {
+                by_shape(p, [&](auto values, auto waves) {
+                    constexpr int NV = decltype(values)::value, WPR = decltype(waves)::value;
+                    k_norm_grad<T, NV, WPR><<<(unsigned)parts, norm_threads(WPR), 0, c->stream>>>(
+                        g, grad_stride, (const T*)x, x_stride, n_rows, (int)dim, mean, rstd, weight, param_type, (T*)dx,
+                        dx_stride, params ? (float*)workspace : nullptr, p.log_group);
+                });
+                HGB_LAUNCHED(c, "k_norm_grad");
             }
             return HGB_OK;
         }));
         if (params) {
-            k_norm_join<<<dim3(tiles, 2), 256, 0, c->stream>>>((const float*)workspace, parts, dim, dweight, dbias, param_type);
+            k_norm_join<<<dim3((unsigned)vec_ceil(dim, 16), 2), 256, 0, c->stream>>>((const float*)workspace, parts, dim, dweight,
+                                                                                    dbias, param_type);
             HGB_LAUNCHED(c, "k_norm_join");
         }
         return HGB_OK;

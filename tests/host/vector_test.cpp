@@ -61,6 +61,21 @@ static void plans()
             CHECK(norm_workspace(n, dim) >= norm_parts(n) * dim * 8);
         }
     CHECK(norm_parts(0) == 1);
+    for (int64_t dim = 1; dim <= 20000; ++dim) {
+        const NormPlan p = plan_norm(dim);
+        CHECK((p.values > 0) == (dim <= kNormMaxDim));
+        if (!p.values) continue;
+        const int64_t span = p.waves > 1 ? 64 * p.waves : 1 << p.log_group, columns = span * p.values;
+        CHECK(columns >= dim && p.log_group <= 6 && (p.waves == 1 || p.log_group == 6));
+        // with more than 8 values a lane the kernels take the lower half of the columns to be in the row
+        CHECK(p.values == 8 || 2 * dim > columns);
+        CHECK(p.values > 8 || p.waves == 1);
+        CHECK(p.per_block * span == norm_threads(p.waves));
+        for (int64_t n : ns) {
+            CHECK(norm_blocks(n, p) >= 1 && norm_blocks(n, p) <= 2 * kNormParts);
+            CHECK(norm_workspace(n, dim) >= (int64_t)norm_blocks(n, p) * dim * 8);
+        }
+    }
     for (int V : {4, 8})
         for (int64_t dim = 1; dim < 700; ++dim) {
             const int g = vec_group(dim, V);

@@ -335,6 +335,17 @@ def test_layer_norm_and_its_gradient(torch, ctx, rows, dim, kind, pk, extra, shi
     assert all(p is q is None or torch.equal(p, q) for p, q in zip((dx, dw, db), again)), "the same call, the same bits"
 
 
+# the widths at which the launch changes its shape, and rows enough for several to a wave
+NORM_SHAPES = [(40000, 20, "bf16"), (4500, 512, "f16"), (4300, 513, "f32"), (4300, 1024, "bf16"), (4300, 1025, "f16"),
+               (2300, 1500, "f32"), (2300, 2048, "bf16"), (1100, 2050, "f16"), (1100, 4096, "f32"), (1100, 4097, "bf16"),
+               (1100, 6000, "f32"), (600, 8192, "f16"), (600, 8193, "bf16"), (600, 16384, "f32"), (300, 16385, "bf16")]
+
+
+@pytest.mark.parametrize("rows,dim,kind", NORM_SHAPES)
+def test_layer_norm_over_many_rows(torch, ctx, rows, dim, kind):
+    test_layer_norm_and_its_gradient(torch, ctx, rows, dim, kind, "f32", 0, 0, "both")
+
+
 def test_layer_norm_gradient_against_differences(torch, ctx):
     """<grad, norm(x + t d) - norm(x - t d)> / 2t in 64 bits against <dx, d> and <dweight, e>."""
     g = gen(torch, 12)
