@@ -183,6 +183,8 @@ class Context:
         if stream is None:
             stream = torch.cuda.current_stream(self.device)
         self.stream = stream
+        self._stream_id = stream.cuda_stream
+        self._current_stream_id = torch._C._cuda_getCurrentRawStream   # of a device; no Stream object made
         h = ctypes.c_void_p()
         st = self._lib.hgb_create(self.device, ctypes.c_void_p(stream.cuda_stream), ctypes.byref(h))
         if st != HGB_OK:
@@ -453,26 +455,34 @@ class Context:
     # Tensors must be on the context's device.  A call whose tensors were made
     # on another stream than the context's is ordered after that (the current)
     # stream's work, and the current stream after the call.
+    # A small call's time is the host's: what a verb makes itself is not checked
+    # again, and the checks take few calls.
+    def _here(self, t, name):
+        if not isinstance(t, self._torch.Tensor) or not t.is_cuda or t.get_device() != self.device:
+            raise ValueError(f"{name} must be a CUDA tensor on device {self.device}")
+
     def _rows(self, t, name, dim=None, rows=None, dtype=None):
         """A [..., dim] vector argument as (pointer, type code, rows, dim, row stride)."""
-        torch = self._torch
-        if not isinstance(t, torch.Tensor) or t.device.type != "cuda" or t.device.index != self.device:
-            raise ValueError(f"{name} must be a CUDA tensor on device {self.device}")
-        if t.dtype not in self._types:
-            raise ValueError(f"{name} must be float32, bfloat16 or float16, got {t.dtype}")
-        if dtype is not None and t.dtype != dtype:
-            raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
-        if t.dim() == 0:
-            raise ValueError(f"{name} must have a last dimension")
-        d = t.shape[-1]
-        n = t.numel() // d if d else 0
-        if t.dim() == 2:
-            n = t.shape[0]
-            stride = t.stride(0) if n > 1 else d
-            if (d > 1 and t.stride(1) != 1) or stride < d:
+        self._here(t, name)
+        kind = t.dtype
+        code = self._types.get(kind)
+        if code is None:
+            raise ValueError(f"{name} must be float32, bfloat16 or float16, got {kind}")
+        if dtype is not None and kind != dtype:
+            raise ValueError(f"{name} must be {dtype}, got {kind}")
+        shape = t.shape
+        if len(shape) == 2:
+            n, d = shape
+            stride, step = t.stride()
+            if n < 2:
+                stride = d
+            if stride < d or (step != 1 and d > 1):
                 raise ValueError(f"{name}'s rows must be contiguous and apart")
+        elif len(shape) == 0:
+            raise ValueError(f"{name} must have a last dimension")
         else:
-            stride = d
+            stride = d = shape[-1]
+            n = t.numel() // d if d else 0
             if not t.is_contiguous():
                 raise ValueError(f"{name} must be contiguous, or two-dimensional with contiguous rows")
         if d < 1:
@@ -481,35 +491,54 @@ class Context:
             raise ValueError(f"{name} has rows of {d} values, needs {dim}")
         if rows is not None and n != rows:
             raise ValueError(f"{name} holds {n} rows, needs {rows}")
-        return t.data_ptr(), self._types[t.dtype], n, d, stride
+        return t.data_ptr(), code, n, d, stride
+
+    def _out(self, out, shape, dtype, dim, rows):
+        """The output tensor, given or made: (tensor, pointer, type code, row stride)."""
+        if out is None:
+            code = self._types.get(dtype)
+            if code is None:
+                raise ValueError(f"dtype must be float32, bfloat16 or float16, got {dtype}")
+            out = self._torch.empty(shape, dtype=dtype, device=self._torch_device)
+            return out, out.data_ptr(), code, dim
+        p, code, _, _, stride = self._rows(out, "out", dim, rows, dtype)
+        return out, p, code, stride
 
     def _param(self, t, name, dim, x_dtype):
         """A [dim] parameter (x's type or float32), or None."""
-        torch = self._torch
         if t is None:
             return None
-        self._dev(t, name)
-        if t.dtype != torch.float32 and t.dtype != x_dtype:
-            raise ValueError(f"{name} must be float32 or {x_dtype}, got {t.dtype}")
-        if t.dim() != 1 or t.shape[0] != dim:
+        self._here(t, name)
+        kind = t.dtype
+        if kind != x_dtype and kind != self._torch.float32:
+            raise ValueError(f"{name} must be float32 or {x_dtype}, got {kind}")
+        if t.shape != (dim,):
             raise ValueError(f"{name} must have shape [{dim}]")
+        if not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
         return t.data_ptr()
 
-    def _ints(self, t, name, shape=None):
-        torch = self._torch
-        p = self._dev(t, name, torch.int32)
-        if shape is not None and tuple(t.shape) != tuple(shape):
+    def _plain(self, t, name, dtype, shape=None):
+        """A contiguous tensor of one type (and shape), as its pointer."""
+        self._here(t, name)
+        if t.dtype != dtype:
+            raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+        if not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
+        if shape is not None and t.shape != shape:
             raise ValueError(f"{name} has shape {tuple(t.shape)}, needs {tuple(shape)}")
-        return p
+        return t.data_ptr()
+
+    def _ints(self, t, name):
+        return self._plain(t, name, self._torch.int32)
 
     def _vec(self, what, fn, tensors, *args):
         """One vector verb: fn(ctx, *args), ordered between the current stream's
         work before and after it when that is not the context's stream."""
-        torch = self._torch
-        cur = torch.cuda.current_stream(self.device)
-        if cur.cuda_stream == self.stream.cuda_stream:
+        if self._current_stream_id(self.device) == self._stream_id:
             st = fn(self._h, *args)
         else:
+            cur = self._torch.cuda.current_stream(self.device)
             self.stream.wait_stream(cur)
             st = fn(self._h, *args)
             for t in tensors:
@@ -529,15 +558,14 @@ class Context:
         """scale * table[tokens]: [*tokens.shape, dim] of `dtype` (the table's
         type, or a 16-bit one beside a float32 table).  The token `pad` gives
         zeros; so does one out of range, which the next sync() reports."""
-        torch = self._torch
         tp, tt, vocab, dim, ts = self._rows(table, "table")
         if table.dim() != 2:
             raise ValueError("table must be two-dimensional")
         ip = self._ints(tokens, "tokens")
         n = tokens.numel()
-        if out is None:
-            out = torch.empty((*tokens.shape, dim), dtype=dtype or table.dtype, device=table.device)
-        op, ot, _, _, os_ = self._rows(out, "out", dim, n, dtype)
+        if out is None and dtype is None:
+            dtype = table.dtype
+        out, op, ot, os_ = self._out(out, (*tokens.shape, dim), dtype, dim, n)
         self._vec("embed", self._lib.hgb_embed, (table, tokens, out), tp, tt, ts, vocab, dim, ip, n, int(pad),
                   float(scale), op, ot, os_)
         return out
@@ -545,15 +573,14 @@ class Context:
     def embed_backward(self, grad, tokens, vocab: int, scale: float = 1.0, pad: int = -1, dtype=None, out=None):
         """The gradient of embed's table: [vocab, dim] of `dtype` (grad's type, or
         float32 beside a 16-bit one), zeros for tokens that do not occur."""
-        torch = self._torch
         gp, gt, n, dim, gs = self._rows(grad, "grad")
         ip = self._ints(tokens, "tokens")
         if tokens.numel() != n:
             raise ValueError(f"grad holds {n} rows for {tokens.numel()} tokens")
         vocab = int(vocab)
-        if out is None:
-            out = torch.empty((max(vocab, 0), dim), dtype=dtype or grad.dtype, device=grad.device)
-        op, ot, _, _, os_ = self._rows(out, "out", dim, vocab, dtype)
+        if out is None and dtype is None:
+            dtype = grad.dtype
+        out, op, ot, os_ = self._out(out, (max(vocab, 0), dim), dtype, dim, vocab)
         nbytes = self._lib.hgb_embed_backward_workspace(n, vocab, dim)
         ws = self._workspace(nbytes)
         self._vec("embed_backward", self._lib.hgb_embed_backward, (grad, tokens, out, ws), gp, gt, gs, n, dim, ip,
@@ -568,20 +595,20 @@ class Context:
         xp, xt, n, dim, xs = self._rows(x, "x")
         wp, bp = self._param(weight, "weight", dim, x.dtype), self._param(bias, "bias", dim, x.dtype)
         pt = self._param_type(weight, bias)
-        if out is None:
-            out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-        yp, _, _, _, ys = self._rows(out, "out", dim, n, x.dtype)
-        mean = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
-        rstd = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
+        shape = x.shape
+        out, yp, _, ys = self._out(out, shape, x.dtype, dim, n)
+        mean = torch.empty(shape[:-1], dtype=torch.float32, device=self._torch_device)
+        rstd = torch.empty_like(mean)
         self._vec("layer_norm", self._lib.hgb_layer_norm, (x, weight, bias, out, mean, rstd), xp, xt, xs, n, dim, wp, bp,
                   pt, float(eps), yp, ys, mean.data_ptr(), rstd.data_ptr())
         return out, mean, rstd
 
-    def _param_type(self, *params):
-        types = {t.dtype for t in params if t is not None}
-        if len(types) > 1:
+    def _param_type(self, a, b=None):
+        if a is None:
+            a = b
+        if b is not None and a.dtype != b.dtype:
             raise ValueError("the parameters must have one type")
-        return self._types[types.pop()] if types else 0
+        return self._types[a.dtype] if a is not None else 0
 
     def layer_norm_backward(self, grad, x, mean, rstd, weight=None, bias: bool = True, out=None):
         """Gradients of layer_norm: (dx, dweight, dbias), dweight None without a
@@ -591,14 +618,14 @@ class Context:
         gp, gt, n, dim, gs = self._rows(grad, "grad")
         xp, _, _, _, xs = self._rows(x, "x", dim, n, grad.dtype)
         wp = self._param(weight, "weight", dim, x.dtype)
-        mp, rp = self._dev(mean, "mean", torch.float32, n), self._dev(rstd, "rstd", torch.float32, n)
+        mp, rp = self._plain(mean, "mean", torch.float32), self._plain(rstd, "rstd", torch.float32)
+        if mean.numel() < n or rstd.numel() < n:
+            raise ValueError(f"mean and rstd must hold {n} values")
         pt = self._param_type(weight)
-        if out is None:
-            out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-        dp, _, _, _, ds = self._rows(out, "out", dim, n, x.dtype)
-        ptype = weight.dtype if weight is not None else torch.float32
-        dw = torch.empty(dim, dtype=ptype, device=x.device) if weight is not None else None
-        db = torch.empty(dim, dtype=ptype, device=x.device) if bias else None
+        out, dp, _, ds = self._out(out, x.shape, x.dtype, dim, n)
+        dw = torch.empty_like(weight) if weight is not None else None
+        db = torch.empty(dim, dtype=weight.dtype if weight is not None else torch.float32,
+                         device=self._torch_device) if bias else None
         nbytes = self._lib.hgb_layer_norm_backward_workspace(n, dim) if dw is not None or db is not None else 0
         ws = self._workspace(nbytes)
         self._vec("layer_norm_backward", self._lib.hgb_layer_norm_backward,
@@ -617,68 +644,55 @@ class Context:
         E = int(n_experts)
         nbytes = self._lib.hgb_route_workspace(n, top, E)
         ws = self._workspace(nbytes)
-        order = torch.empty(n * top, dtype=torch.int32, device=experts.device)
-        position = torch.empty((n, top), dtype=torch.int32, device=experts.device)
-        offsets = torch.empty(E + 1, dtype=torch.int32, device=experts.device)
+        position = torch.empty_like(experts)
+        order = torch.empty(n * top, dtype=torch.int32, device=self._torch_device)
+        offsets = torch.empty(E + 1, dtype=torch.int32, device=self._torch_device)
         self._vec("route", self._lib.hgb_route, (experts, order, position, offsets, ws), ep, n, top, E,
                   order.data_ptr(), position.data_ptr(), offsets.data_ptr(), ws.data_ptr() if nbytes else None, nbytes)
         return Route(order, position, offsets)
 
     def _routed(self, route, n=None):
         """(position pointer, offsets pointer, rows, top, experts) of a Route."""
-        pp, op = self._ints(route.position, "route.position"), self._ints(route.offsets, "route.offsets")
-        if route.position.dim() != 2 or route.offsets.dim() != 1 or route.offsets.shape[0] < 2:
+        position, offsets = route.position, route.offsets
+        pp, op = self._ints(position, "route.position"), self._ints(offsets, "route.offsets")
+        shape, ends = position.shape, offsets.shape
+        if len(shape) != 2 or len(ends) != 1 or ends[0] < 2:
             raise ValueError("route is not what Context.route returns")
-        rows, top = route.position.shape
+        rows, top = shape
         if n is not None and n != rows:
             raise ValueError(f"{n} rows for a route of {rows}")
-        return pp, op, rows, top, route.offsets.shape[0] - 1
+        return pp, op, rows, top, ends[0] - 1
 
     def route_gather(self, x, route: Route, out=None):
         """x's rows in the experts' order: [rows * top, dim], zeros past the last
         routed place."""
-        torch = self._torch
         xp, xt, n, dim, xs = self._rows(x, "x")
         pp, fp, n, top, E = self._routed(route, n)
-        if out is None:
-            out = torch.empty((n * top, dim), dtype=x.dtype, device=x.device)
-        op, _, _, _, os_ = self._rows(out, "out", dim, n * top, x.dtype)
+        out, op, _, os_ = self._out(out, (n * top, dim), x.dtype, dim, n * top)
         self._vec("route_gather", self._lib.hgb_route_gather, (x, *route, out), xp, xt, xs, n, top, dim, pp, fp, E, op, os_)
         return out
 
     def route_gather_backward(self, grad, route: Route, out=None):
         """The gradient of route_gather's x: [rows, dim] sums of grad's rows
         ([rows * top, dim])."""
-        torch = self._torch
         pp, _, n, top, _ = self._routed(route)
         gp, gt, _, dim, gs = self._rows(grad, "grad", rows=n * top)
-        if out is None:
-            out = torch.empty((n, dim), dtype=grad.dtype, device=grad.device)
-        op, _, _, _, os_ = self._rows(out, "out", dim, n, grad.dtype)
+        out, op, _, os_ = self._out(out, (n, dim), grad.dtype, dim, n)
         self._vec("route_gather_backward", self._lib.hgb_route_gather_backward, (grad, *route, out), gp, gt, gs, n, top,
                   dim, pp, op, os_)
         return out
 
     def _weights(self, weights, n, top):
-        torch = self._torch
-        if weights is None:
-            return None
-        p = self._dev(weights, "weights", torch.float32)
-        if tuple(weights.shape) != (n, top):
-            raise ValueError(f"weights has shape {tuple(weights.shape)}, needs {(n, top)}")
-        return p
+        return None if weights is None else self._plain(weights, "weights", self._torch.float32, (n, top))
 
     def route_combine(self, y, route: Route, weights=None, out=None):
         """The experts' answers y ([rows * top, dim], in their order) back in the
         rows' order and summed with `weights` (float32 [rows, top], None: ones):
         [rows, dim]."""
-        torch = self._torch
         pp, _, n, top, _ = self._routed(route)
         yp, yt, _, dim, ys = self._rows(y, "y", rows=n * top)
         wp = self._weights(weights, n, top)
-        if out is None:
-            out = torch.empty((n, dim), dtype=y.dtype, device=y.device)
-        op, _, _, _, os_ = self._rows(out, "out", dim, n, y.dtype)
+        out, op, _, os_ = self._out(out, (n, dim), y.dtype, dim, n)
         self._vec("route_combine", self._lib.hgb_route_combine, (y, *route, weights, out), yp, yt, ys, n, top, dim, pp, wp,
                   op, os_)
         return out
@@ -686,15 +700,12 @@ class Context:
     def route_combine_backward(self, grad, y, route: Route, weights=None, out=None):
         """Gradients of route_combine: (dy [rows * top, dim], dweights [rows, top],
         None without weights)."""
-        torch = self._torch
         gp, gt, n, dim, gs = self._rows(grad, "grad")
         pp, fp, n, top, E = self._routed(route, n)
         yp, _, _, _, ys = self._rows(y, "y", dim, n * top, grad.dtype)
         wp = self._weights(weights, n, top)
-        if out is None:
-            out = torch.empty((n * top, dim), dtype=grad.dtype, device=grad.device)
-        op, _, _, _, os_ = self._rows(out, "out", dim, n * top, grad.dtype)
-        dw = torch.empty((n, top), dtype=torch.float32, device=grad.device) if weights is not None else None
+        out, op, _, os_ = self._out(out, (n * top, dim), grad.dtype, dim, n * top)
+        dw = self._torch.empty_like(weights) if weights is not None else None
         self._vec("route_combine_backward", self._lib.hgb_route_combine_backward, (grad, y, *route, weights, out, dw), gp,
                   gt, gs, yp, ys, n, top, dim, pp, fp, E, wp, op, os_, dw.data_ptr() if dw is not None else None)
         return out, dw
