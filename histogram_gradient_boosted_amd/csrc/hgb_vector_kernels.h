@@ -8,6 +8,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "hgb_ctx.h"
 #include "hgb_vector_plan.h"
 
@@ -142,21 +144,25 @@ __device__ inline void tile_ranks(const uint32_t (&digit)[ITEMS], int live, int 
     for (int i = threadIdx.x; i < waves * radix; i += blockDim.x) count[i] = 0;
     __syncthreads();
     uint32_t* mine = count + w * radix;
-    const uint64_t below = (1ull << lane) - 1;
 #pragma unroll
     for (int i = 0; i < ITEMS; ++i) {
         const int at = w * 64 * ITEMS + i * 64 + lane;
         const bool in = at < live;
-        uint64_t same = __ballot(in);
-        for (int b = 0; b < bits; ++b) {
-            const bool one = (digit[i] >> b) & 1;
-            const uint64_t m = __ballot(one);
-            same &= one ? m : ~m;
-        }
-        const int before = __popcll(same & below);
+        // the lanes with this lane's digit, a bit at a time
+        const uint64_t lanes = __ballot(in);
+        uint32_t lo = (uint32_t)lanes, hi = (uint32_t)(lanes >> 32);
+#pragma unroll
+        for (int b = 0; b < kSortBits; ++b)
+            if (b < bits) {
+                const uint32_t one = (uint32_t)((int32_t)(digit[i] << (31 - b)) >> 31);   // the bit, 32 times
+                const uint64_t m = __ballot(one != 0);
+                lo &= ~((uint32_t)m ^ one);
+                hi &= ~((uint32_t)(m >> 32) ^ one);
+            }
+        const int before = __builtin_amdgcn_mbcnt_hi(hi, __builtin_amdgcn_mbcnt_lo(lo, 0));
         if (in) rank[i] = mine[digit[i]] + before;
         wave_order();
-        if (in && before == 0) mine[digit[i]] = rank[i] + __popcll(same);
+        if (in && before == 0) mine[digit[i]] = rank[i] + __popc(lo) + __popc(hi);
         wave_order();
     }
     __syncthreads();
@@ -280,7 +286,25 @@ __global__ __launch_bounds__(kSortThreads) void k_sort_small(SortIn in, SortOut 
     }
 }
 
-// counts[block][digit] of one pass; blocks past p.blocks write the zeros.
+// hist[digit of key i] += 1 for the keys [begin, end), by the whole block.
+// Eight keys a thread are loaded before they are counted.
+template <bool FIRST>
+__device__ inline bool count_digits(const SortIn& in, const SortPlan& p, int shift, int64_t begin, int64_t end,
+                                    uint32_t* hist)
+{
+    bool bad = false;
+    for (int64_t i = begin + threadIdx.x; i < end; i += 8 * kSortThreads) {
+        uint32_t key[8];
+#pragma unroll
+        for (int u = 0; u < 8; ++u) key[u] = i + u * kSortThreads < end ? sort_load<FIRST>(in, i + u * kSortThreads, &bad).x : 0;
+#pragma unroll
+        for (int u = 0; u < 8; ++u)
+            if (i + u * kSortThreads < end) atomicAdd(&hist[(key[u] >> shift) & (p.radix - 1)], 1u);
+    }
+    return bad;
+}
+
+// counts[block][digit] of one pass, rows of p.row; blocks past p.blocks write the zeros.
 template <bool FIRST>
 __global__ __launch_bounds__(kSortThreads) void k_sort_count(SortIn in, SortPlan p, int shift, uint32_t* counts,
                                                              ZeroFill z)
@@ -290,80 +314,140 @@ __global__ __launch_bounds__(kSortThreads) void k_sort_count(SortIn in, SortPlan
         return;
     }
     extern __shared__ uint32_t lds[];
-    for (int d = threadIdx.x; d < p.radix; d += blockDim.x) lds[d] = 0;
+    for (int d = threadIdx.x; d < p.row; d += blockDim.x) lds[d] = 0;
     __syncthreads();
-    const int64_t begin = (int64_t)blockIdx.x * p.tiles * kSortTile;
-    const int64_t end = begin + (int64_t)p.tiles * kSortTile < in.n ? begin + (int64_t)p.tiles * kSortTile : in.n;
-    bool bad = false;
-    for (int64_t i = begin + threadIdx.x; i < end; i += blockDim.x)
-        atomicAdd(&lds[(sort_load<FIRST>(in, i, &bad).x >> shift) & (p.radix - 1)], 1u);
-    if (bad) atomicOr(in.err, in.flag);
+    const int64_t share = (int64_t)p.tiles * p.items * kSortThreads, begin = blockIdx.x * share;
+    if (count_digits<FIRST>(in, p, shift, begin, begin + share < in.n ? begin + share : in.n, lds)) atomicOr(in.err, in.flag);
     __syncthreads();
-    for (int d = threadIdx.x; d < p.radix; d += blockDim.x) counts[(int64_t)blockIdx.x * p.radix + d] = lds[d];
+    for (int d = threadIdx.x; d < p.row; d += blockDim.x) counts[(int64_t)blockIdx.x * p.row + d] = lds[d];
 }
 
-// The pass's scatter: each block sums the counts before it (there are at most
-// kSortMaxBlocks rows of them, read from L2) instead of a scan in a launch of
-// its own, then ranks its tiles in order.
-template <bool FIRST>
-__global__ __launch_bounds__(kSortThreads) void k_sort_scatter(SortIn in, SortOut out, SortPlan p, int shift,
-                                                               const uint32_t* counts)
+// The pass's scatter: each block finds where its digits' keys begin (from the
+// shares' counts, at most kSortMaxBlocks rows of them and read from L2, or by
+// counting all keys itself) instead of a scan in a launch of its own, then
+// ranks its tiles in order.  Blocks past p.blocks write the zeros.  3,670,016
+// keys by 128 digits: 28 us, of which 5 for the counts, 6 for the ranks, 4 to
+// pass through LDS and out (38 us with the pairs stored from their lanes and
+// the counts read a word at a time).
+template <bool FIRST, int ITEMS>
+__global__ __launch_bounds__(kSortThreads, 8) void k_sort_scatter(SortIn in, SortOut out, SortPlan p, int shift,
+                                                               const uint32_t* counts, ZeroFill z)
 {
+    if ((int)blockIdx.x >= p.blocks) {
+        zero_fill(z, blockIdx.x - p.blocks, gridDim.x - p.blocks);
+        return;
+    }
     extern __shared__ uint32_t lds[];
+    constexpr int kTile = ITEMS * kSortThreads;
     const int waves = blockDim.x >> 6;
-    uint32_t* count = lds;                        // [waves][radix]
-    uint32_t* total = count + waves * p.radix;    // [radix]
-    uint32_t* base = total + p.radix;             // [radix]
-    uint32_t* tmp = base + p.radix;               // [waves]
+    uint2* pairs = (uint2*)lds;                        // [kTile], where ITEMS > 1
+    uint32_t* count = lds + scatter_pair_words(ITEMS);  // [waves][radix]
+    uint32_t* total = count + waves * p.radix;         // [radix]
+    uint32_t* base = total + p.radix;                  // [radix]
+    uint32_t* tmp = base + p.radix;                    // [waves]
     // base[d] = keys of smaller digits + keys of digit d in earlier blocks
-    {
-        const int d = threadIdx.x & (p.radix - 1), g = threadIdx.x / p.radix, groups = blockDim.x / p.radix;
-        uint32_t all = 0, before = 0;
-        for (int b = g; b < p.blocks; b += groups) {
-            const uint32_t c = counts[(int64_t)b * p.radix + d];
-            all += c;
-            if (b < (int)blockIdx.x) before += c;
+    if ((int)threadIdx.x < p.radix) total[threadIdx.x] = base[threadIdx.x] = 0;
+    __syncthreads();
+    if (p.count) {
+        // four digits a thread, eight shares at a time
+        const int quads = p.row / 4, d = (threadIdx.x & (quads - 1)) * 4, g = threadIdx.x / quads, groups = blockDim.x / quads;
+        uint32_t all[4] = {0, 0, 0, 0}, before[4] = {0, 0, 0, 0};
+        for (int b = g; b < p.blocks; b += 8 * groups) {
+            uint4 c[8];
+#pragma unroll
+            for (int u = 0; u < 8; ++u) {
+                const int k = b + u * groups;
+                c[u] = k < p.blocks ? *(const uint4*)(counts + (int64_t)k * p.row + d) : make_uint4(0, 0, 0, 0);
+            }
+#pragma unroll
+            for (int u = 0; u < 8; ++u) {
+                const uint32_t v[4] = {c[u].x, c[u].y, c[u].z, c[u].w};
+                const bool earlier = b + u * groups < (int)blockIdx.x;
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    all[k] += v[k];
+                    before[k] += earlier ? v[k] : 0;
+                }
+            }
         }
-        if (g == 0) total[d] = base[d] = 0;
+        if (g < p.blocks)
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                if (d + k < p.radix) {
+                    atomicAdd(&total[d + k], all[k]);
+                    atomicAdd(&base[d + k], before[k]);
+                }
         __syncthreads();
-        atomicAdd(&total[d], all);
-        atomicAdd(&base[d], before);
+    } else {
+        const int64_t begin = (int64_t)blockIdx.x * p.tiles * kTile;
+        bool bad = count_digits<FIRST>(in, p, shift, 0, begin, base);
+        bad |= count_digits<FIRST>(in, p, shift, begin, in.n, total);
+        if (bad && blockIdx.x == 0) atomicOr(in.err, in.flag);
         __syncthreads();
-        block_scan(total, p.radix, tmp);
-        if (out.offsets && blockIdx.x == 0)
-            for (int k = threadIdx.x; k <= in.limit; k += blockDim.x) out.offsets[k] = (int32_t)total[k];
-        if (g == 0) base[d] += total[d];
+        if ((int)threadIdx.x < p.radix) total[threadIdx.x] += base[threadIdx.x];
         __syncthreads();
     }
-    const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, first = w * 64 * kSortItems + lane;
+    block_scan(total, p.radix, tmp);
+    if (out.offsets && blockIdx.x == 0)
+        for (int k = threadIdx.x; k <= in.limit; k += blockDim.x) out.offsets[k] = (int32_t)total[k];
+    if ((int)threadIdx.x < p.radix) base[threadIdx.x] += total[threadIdx.x];
+    __syncthreads();
+    const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, first = w * 64 * ITEMS + lane;
     for (int t = 0; t < p.tiles; ++t) {
-        const int64_t begin = ((int64_t)blockIdx.x * p.tiles + t) * kSortTile;
+        const int64_t begin = ((int64_t)blockIdx.x * p.tiles + t) * kTile;
         if (begin >= in.n) break;
-        const int live = in.n - begin < kSortTile ? (int)(in.n - begin) : kSortTile;
-        uint2 kv[kSortItems];
-        uint32_t digit[kSortItems], rank[kSortItems];
+        const int live = in.n - begin < kTile ? (int)(in.n - begin) : kTile;
+        uint2 kv[ITEMS];
+        uint32_t digit[ITEMS], rank[ITEMS];
         bool bad = false;
 #pragma unroll
-        for (int i = 0; i < kSortItems; ++i) {
+        for (int i = 0; i < ITEMS; ++i) {
             kv[i] = make_uint2(0, 0);
             if (first + i * 64 < live) kv[i] = sort_load<FIRST>(in, begin + first + i * 64, &bad);
             digit[i] = (kv[i].x >> shift) & (p.radix - 1);
         }
-        tile_ranks<kSortItems>(digit, live, p.bits, p.radix, count, total, rank);
-#pragma unroll
-        for (int i = 0; i < kSortItems; ++i)
-            if (first + i * 64 < live) {
-                const int64_t at = base[digit[i]] + count[w * p.radix + digit[i]] + rank[i];
+        tile_ranks<ITEMS>(digit, live, p.bits, p.radix, count, total, rank);
+        if (ITEMS == 1) {
+            if (first < live) {
+                const int64_t at = base[digit[0]] + count[w * p.radix + digit[0]] + rank[0];
+                const bool keep = kv[0].x < (uint32_t)in.limit;
                 if (out.to) {
-                    out.to[at] = kv[i];
+                    out.to[at] = kv[0];
                 } else {
-                    const bool keep = kv[i].x < (uint32_t)in.limit;
-                    out.order[at] = keep ? (int32_t)kv[i].y : -1;
-                    out.position[kv[i].y] = keep ? (int32_t)at : -1;
+                    out.order[at] = keep ? (int32_t)kv[0].y : -1;
+                    out.position[kv[0].y] = keep ? (int32_t)at : -1;
                 }
             }
+            __syncthreads();
+            if ((int)threadIdx.x < p.radix) base[threadIdx.x] += total[threadIdx.x];
+            continue;
+        }
+        // in LDS at their place in the tile: total becomes the digits' first
+        // places there, and base what leads from such a place to the output's
+        const uint32_t keys = (int)threadIdx.x < p.radix ? total[threadIdx.x] : 0;
+        block_scan(total, p.radix, tmp);
+        if ((int)threadIdx.x < p.radix) base[threadIdx.x] -= total[threadIdx.x];
         __syncthreads();
-        if ((int)threadIdx.x < p.radix) base[threadIdx.x] += total[threadIdx.x];
+#pragma unroll
+        for (int i = 0; i < ITEMS; ++i)
+            if (first + i * 64 < live) {
+                const uint32_t at = total[digit[i]] + count[w * p.radix + digit[i]] + rank[i];
+                pairs[at] = kv[i];
+                if (!out.to) out.position[kv[i].y] = kv[i].x < (uint32_t)in.limit ? (int32_t)(base[digit[i]] + at) : -1;
+            }
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < ITEMS; ++i) {
+            const int at = i * kSortThreads + threadIdx.x;
+            if (at < live) {
+                const uint2 v = pairs[at];
+                const uint32_t to = base[(v.x >> shift) & (p.radix - 1)] + at;
+                if (out.to) out.to[to] = v;
+                else out.order[to] = v.x < (uint32_t)in.limit ? (int32_t)v.y : -1;
+            }
+        }
+        __syncthreads();
+        if ((int)threadIdx.x < p.radix) base[threadIdx.x] += total[threadIdx.x] + keys;
     }
 }
 
@@ -419,14 +503,17 @@ __global__ __launch_bounds__(256) void k_zero_rows(ZeroFill z) { zero_fill(z, bl
 // walks one chunk of sorted positions; a run that lies in its chunk is
 // finished there, and a run that crosses a border leaves its part in the
 // chunk's partial rows: row 0 a run that began before the chunk, row 1 one
-// that begins in it and goes on.
+// that begins in it and goes on.  The order of the sums depends on the tokens
+// alone.  Bound by the gradient's rows, 128 bytes each in the measured case, in
+// the tokens' order: 3,670,016 rows of 64 bf16 values in 113 us, 4.2 TB/s (the
+// same reads in row order: 105; a large copy: 4.9 TB/s).
 template <typename T, typename U>
 __global__ __launch_bounds__(256) void k_embed_sum(const uint2* __restrict__ pairs, int64_t n, const T* __restrict__ grad,
                                                    int64_t grad_stride, int64_t dim, int64_t vocab, float scale,
                                                    U* __restrict__ out, int64_t out_stride, float* __restrict__ part,
                                                    int64_t part_stride, int chunk, int log_group)
 {
-    constexpr int V = kVals<T, U>, STEP = 8;
+    constexpr int V = kVals<T, U>;
     const int lane = threadIdx.x & ((1 << log_group) - 1);
     const int64_t id = (int64_t)blockIdx.x * (256 >> log_group) + (threadIdx.x >> log_group);
     const int64_t c = ((int64_t)blockIdx.y << log_group) * V + (int64_t)lane * V;
@@ -434,56 +521,61 @@ __global__ __launch_bounds__(256) void k_embed_sum(const uint2* __restrict__ pai
     if (begin >= n || c >= dim) return;
     const uint32_t none = 0xffffffffu;
     const uint32_t prev = begin > 0 ? pairs[begin - 1].x : none, next = end < n ? pairs[end].x : none;
-    uint32_t cur = pairs[begin].x;
-    bool head = cur == prev;
-    float acc[V];
+    // STEP rows in flight; fewer where the row ends in the lane's columns, whose
+    // values are loaded one by one
+    auto walk = [&](auto step) {
+        constexpr int STEP = decltype(step)::value;
+        const int64_t left = STEP == 8 ? V : dim - c;
+        uint32_t cur = pairs[begin].x;
+        bool head = cur == prev;
+        float acc[V];
 #pragma unroll
-    for (int k = 0; k < V; ++k) acc[k] = 0.0f;
-    auto flush = [&](bool open) {
-        if (cur >= (uint32_t)vocab) return;
-        if (head || open) {
-            float* p = part + (id * 2 + (head ? 0 : 1)) * part_stride + c;
+        for (int k = 0; k < V; ++k) acc[k] = 0.0f;
+        auto flush = [&](bool open) {
+            if (cur >= (uint32_t)vocab) return;
+            if (head || open) {
+                store_vals<V>(acc, part + (id * 2 + (head ? 0 : 1)) * part_stride + c, left);
+            } else {
 #pragma unroll
-            for (int k = 0; k < V; ++k)
-                if (c + k < dim) p[k] = acc[k];
-        } else {
+                for (int k = 0; k < V; ++k) acc[k] *= scale;
+                store_vals<V>(acc, out + (int64_t)cur * out_stride + c, left);
+            }
+        };
+        for (int64_t j = begin; j < end; j += STEP) {
+            uint2 kv[STEP];
+            typename Vals<T, V>::type v[STEP];
 #pragma unroll
-            for (int k = 0; k < V; ++k) acc[k] *= scale;
-            store_vals<V>(acc, out + (int64_t)cur * out_stride + c, dim - c);
+            for (int u = 0; u < STEP; ++u) kv[u] = pairs[j + u < end ? j + u : end - 1];
+            // a dropped token's row is not read: its sum, which no one stores, takes row 0
+#pragma unroll
+            for (int u = 0; u < STEP; ++u)
+                v[u] = load_raw<V>(grad + (kv[u].x < (uint32_t)vocab ? (int64_t)kv[u].y : 0) * grad_stride + c, left);
+#pragma unroll
+            for (int u = 0; u < STEP; ++u) {
+                if (j + u >= end) break;
+                if (kv[u].x != cur) {
+                    flush(false);
+                    cur = kv[u].x;
+                    head = false;
+#pragma unroll
+                    for (int k = 0; k < V; ++k) acc[k] = 0.0f;
+                }
+#pragma unroll
+                for (int k = 0; k < V; ++k) acc[k] += (float)v[u][k];
+            }
         }
+        flush(cur == next);
     };
-    for (int64_t j = begin; j < end; j += STEP) {
-        uint2 kv[STEP];
-        float v[STEP][V];
-#pragma unroll
-        for (int u = 0; u < STEP; ++u) kv[u] = pairs[j + u < end ? j + u : end - 1];
-#pragma unroll
-        for (int u = 0; u < STEP; ++u)
-            if (kv[u].x < (uint32_t)vocab) load_vals<V>(v[u], grad + (int64_t)kv[u].y * grad_stride + c, dim - c);
-#pragma unroll
-        for (int u = 0; u < STEP; ++u) {
-            if (j + u >= end) break;
-            if (kv[u].x != cur) {
-                flush(false);
-                cur = kv[u].x;
-                head = false;
-#pragma unroll
-                for (int k = 0; k < V; ++k) acc[k] = 0.0f;
-            }
-            if (cur < (uint32_t)vocab) {
-#pragma unroll
-                for (int k = 0; k < V; ++k) acc[k] += v[u][k];
-            }
-        }
-    }
-    flush(cur == next);
+    if (dim - c >= V) walk(std::integral_constant<int, 8>());
+    else walk(std::integral_constant<int, 4>());
 }
 
 // Runs that cross chunk borders: the partial row of the chunk where the run
 // begins plus row 0 of each chunk it goes on in.  A block takes kJoinChunks
 // chunks and 64 columns: a wave sums a short run, the whole block a long one
-// (16 rows at a time, joined in a fixed order).
-constexpr int kJoinChunks = 16;
+// (16 rows at a time, joined in a fixed order).  Bound by its chain of loads
+// that wait for one another: 4 us for 5,001 tokens, 9 us for 3,670,016.
+constexpr int kJoinChunks = 4;
 constexpr int kJoinLong = 32;
 
 template <typename U>
@@ -496,32 +588,37 @@ __global__ __launch_bounds__(256) void k_embed_join(const uint2* __restrict__ pa
     __shared__ uint32_t key[kJoinChunks];
     __shared__ float4 sums[4][16];
     const int64_t base = (int64_t)blockIdx.x * kJoinChunks;
-    if (threadIdx.x < kJoinChunks) {
-        const int64_t id = base + threadIdx.x;
+    const int w = threadIdx.x >> 6, lane = threadIdx.x & 63, row = lane >> 4;
+    // each wave looks for the runs of its chunks, 64 chunks at a glance
+    constexpr int EACH = kJoinChunks / 4;
+    uint32_t front[EACH], k[EACH], after[EACH], prev[EACH];
+#pragma unroll
+    for (int u = 0; u < EACH; ++u) {
+        const int64_t id = base + w * EACH + u, begin = id * chunk, end = begin + chunk;
+        const bool more = id + 1 < chunks;
+        front[u] = more ? pairs[begin].x : 0;
+        k[u] = more ? pairs[end - 1].x : 0;
+        after[u] = more ? pairs[end].x : ~0u;
+        prev[u] = more && begin > 0 ? pairs[begin - 1].x : ~0u;
+    }
+#pragma unroll
+    for (int u = 0; u < EACH; ++u) {
         int64_t e = -1;
-        uint32_t k = 0;
-        if (id + 1 < chunks) {
-            const int64_t begin = id * chunk, end = begin + chunk;
-            k = pairs[end - 1].x;
-            const bool open = pairs[end].x == k;
-            const bool whole = pairs[begin].x == k && begin > 0 && pairs[begin - 1].x == k;
-            if (open && !whole && k < (uint32_t)vocab) {
-                // the last chunk that begins with the run: doubling, then halving
-                int64_t lo = id + 1, step = 1;
-                while (lo + step < chunks && pairs[(lo + step) * chunk].x == k) {
-                    lo += step;
-                    step *= 2;
-                }
-                for (; step > 0; step /= 2)
-                    if (lo + step < chunks && pairs[(lo + step) * chunk].x == k) lo += step;
-                e = lo;
+        const bool whole = front[u] == k[u] && prev[u] == k[u];   // the run began before this chunk
+        if (after[u] == k[u] && !whole && k[u] < (uint32_t)vocab) {
+            e = base + w * EACH + u + 1;   // a chunk that begins with the run
+            for (int len = 64; len == 64; e += len) {
+                const int64_t at = e + 1 + lane;
+                const uint64_t other = ~__ballot(at < chunks && pairs[at * chunk].x == k[u]);
+                len = other ? __ffsll((unsigned long long)other) - 1 : 64;
             }
         }
-        last[threadIdx.x] = e;
-        key[threadIdx.x] = k;
+        if (lane == 0) {
+            last[w * EACH + u] = e;
+            key[w * EACH + u] = k[u];
+        }
     }
     __syncthreads();
-    const int w = threadIdx.x >> 6, lane = threadIdx.x & 63, row = lane >> 4;
     const int64_t c = (int64_t)blockIdx.y * 64 + (lane & 15) * 4;
     const bool in = c < dim;   // part rows are padded to four floats
     for (int s = 0; s < kJoinChunks; ++s) {
@@ -532,6 +629,7 @@ __global__ __launch_bounds__(256) void k_embed_join(const uint2* __restrict__ pa
         const int rows = whole_block ? 16 : 4;
         float4 a = make_float4(0, 0, 0, 0);
         if (in)
+#pragma unroll 4
             for (int64_t k = id + (whole_block ? w * 4 + row : row); k <= e; k += rows) {
                 const float4 v = *(const float4*)(part + (k * 2 + (k == id ? 1 : 0)) * part_stride + c);
                 a.x += v.x;

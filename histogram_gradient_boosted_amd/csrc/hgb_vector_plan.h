@@ -30,25 +30,32 @@ inline int vec_pow2(int64_t v)   // the smallest power of two >= v
 }
 
 // Stable sort of n keys in [0, limit], least significant digit first.
-// Up to kSortSmall keys one block sorts in LDS; above that, each pass is a
-// count and a scatter over `blocks` equal shares of the keys, a share being
-// `tiles` tiles of kSortTile keys taken one after the other.
+// Up to kSortSmall keys one block sorts in LDS, all passes in one launch.
+// Above that, each pass scatters from `blocks` equal shares of the keys, a
+// share being `tiles` tiles of `items` keys a thread taken one after the other.
+// Where each block's keys go follows from the digits of all keys: up to
+// kSortSelf blocks each counts them itself, beyond that a launch of its own
+// counts each share (`count`), and a block sums the counts before it.
 constexpr int kSortThreads = 1024;
-constexpr int kSortItems = 16;
-constexpr int kSortTile = kSortThreads * kSortItems;
-constexpr int kSortSmall = kSortTile;
-constexpr int kSortSmallBits = 8;
-constexpr int kSortBits = 10;
+constexpr int kSortItems = 8;
+constexpr int kSortSmall = 4 * kSortThreads;
+constexpr int kSortBits = 10;        // of a digit at most, and
+constexpr int kSortManyBits = 8;     // where more than kSortFew blocks' counts are summed
+constexpr int kSortFew = 32;
+constexpr int kSortSelf = 16;
 constexpr int kSortMaxBlocks = 512;
 
 struct SortPlan {
     int64_t n = 0;
     int passes = 0;
     int bits = 0;        // of every digit
-    int radix = 0;       // digits' values: 2^bits, or limit + 1 for one pass
+    int radix = 0;       // digits' values: 2^bits
+    int row = 4;         // words of a share's counts: the radix, at least a 16-byte load
     bool small = false;
-    int blocks = 0;
-    int tiles = 0;
+    bool count = false;
+    int items = 1;       // keys a thread holds of a tile: 1, 4 or kSortItems
+    int blocks = 1;
+    int tiles = 1;
 };
 
 inline SortPlan plan_sort(int64_t n, int64_t limit, bool one_pass)
@@ -56,20 +63,28 @@ inline SortPlan plan_sort(int64_t n, int64_t limit, bool one_pass)
     SortPlan p;
     p.n = n;
     p.small = n <= kSortSmall;
+    if (p.small) {
+        p.items = n <= kSortThreads ? 1 : 4;
+    } else {
+        // few keys a thread while that gives no CU two blocks
+        p.items = n <= 256 * kSortThreads ? 1 : n <= 1024 * kSortThreads ? 4 : kSortItems;
+        const int64_t tiles = vec_ceil(n, (int64_t)p.items * kSortThreads);
+        p.tiles = (int)vec_ceil(tiles, kSortMaxBlocks);
+        p.blocks = (int)vec_ceil(tiles, p.tiles);
+        p.count = p.blocks > kSortSelf;
+    }
     const int bits = vec_bits(limit);
-    const int most = one_pass ? kSortBits : p.small ? kSortSmallBits : kSortBits;
+    const int most = one_pass || p.blocks <= kSortFew ? kSortBits : kSortManyBits;
     p.passes = (int)vec_ceil(bits, most);
     p.bits = (int)vec_ceil(bits, p.passes);
     p.radix = 1 << p.bits;
-    if (p.small) {
-        p.blocks = p.tiles = 1;
-        return p;
-    }
-    const int64_t tiles = vec_ceil(n, kSortTile);
-    p.tiles = (int)vec_ceil(tiles, kSortMaxBlocks);
-    p.blocks = (int)vec_ceil(tiles, p.tiles);
+    p.row = std::max(p.radix, 4);
     return p;
 }
+
+// Keys that pass through LDS on their way out, so that a digit's keys of a tile
+// are stored side by side; with one key a thread the runs are too short.
+constexpr int scatter_pair_words(int items) { return items > 1 ? 2 * items * kSortThreads : 0; }
 
 // LDS words in which the one-block sort exchanges its pairs between passes:
 // the launch and the kernel lay the rest out behind them.
@@ -89,8 +104,8 @@ struct EmbedPlan {
     int64_t off_a = 0, off_b = 0, off_part = 0, bytes = 0;
 };
 
-constexpr int kEmbedChunk = 64;          // largest chunk
-constexpr int64_t kEmbedWaves = 4096;    // chunks are halved until this many waves run (16 a CU)
+constexpr int kEmbedChunk = 256;         // largest chunk
+constexpr int64_t kEmbedWaves = 2048;    // chunks are halved until this many waves run (8 a CU)
 
 inline EmbedPlan plan_embed(int64_t n, int64_t vocab, int64_t dim)
 {
@@ -100,10 +115,10 @@ inline EmbedPlan plan_embed(int64_t n, int64_t vocab, int64_t dim)
     // workspace do not depend on the types.
     const int64_t group = vec_group(dim, 4), slices = vec_ceil(dim, 64 * 4);
     p.chunk = kEmbedChunk;
-    while (p.chunk > 4 && vec_ceil(n, p.chunk) * group * slices / 64 < kEmbedWaves) p.chunk /= 2;
+    while (p.chunk > 8 && vec_ceil(n, p.chunk) * group * slices / 64 < kEmbedWaves) p.chunk /= 2;
     p.chunks = vec_ceil(n, p.chunk);
     p.part_stride = vec_up(dim, 4);
-    p.off_a = vec_up((int64_t)p.sort.blocks * p.sort.radix * 4, 256);
+    p.off_a = p.sort.count ? vec_up((int64_t)p.sort.blocks * p.sort.row * 4, 256) : 0;
     p.off_b = p.off_a + vec_up(n * 8, 256);
     p.off_part = p.off_b + (p.sort.small ? 0 : vec_up(n * 8, 256));
     p.bytes = p.off_part + vec_up(p.chunks * 2 * p.part_stride * 4, 256);
@@ -114,7 +129,7 @@ inline EmbedPlan plan_embed(int64_t n, int64_t vocab, int64_t dim)
 inline int64_t route_workspace(int64_t slots, int experts)
 {
     const SortPlan p = plan_sort(slots, experts, true);
-    return p.small ? 0 : vec_up((int64_t)p.blocks * p.radix * 4, 256);
+    return p.count ? vec_up((int64_t)p.blocks * p.row * 4, 256) : 0;
 }
 
 // The layer norm's launch: `values` of a row in each lane's registers, a row

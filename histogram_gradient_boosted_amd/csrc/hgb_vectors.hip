@@ -158,34 +158,58 @@ hgb_status launch_sort_small(hgb_ctx* c, const SortIn& in, const SortOut& out, c
     return HGB_OK;
 }
 
+template <bool FIRST, int ITEMS>
+hgb_status launch_scatter(hgb_ctx* c, const SortIn& in, const SortOut& out, const SortPlan& p, int shift,
+                          const uint32_t* counts, const ZeroFill& z)
+{
+    const size_t lds = 4 * (scatter_pair_words(ITEMS) + (size_t)(kSortThreads / 64) * p.radix + 2 * (size_t)p.radix + 16);
+    HGB_TRY(raise_lds(c, (const void*)k_sort_scatter<FIRST, ITEMS>, lds));
+    k_sort_scatter<FIRST, ITEMS><<<p.blocks + zero_blocks(c, z.rows * z.cols * z.elem, kSortThreads), kSortThreads, lds,
+                                   c->stream>>>(in, out, p, shift, counts, z);
+    HGB_LAUNCHED(c, "k_sort_scatter");
+    return HGB_OK;
+}
+
+template <bool FIRST>
+hgb_status launch_pass(hgb_ctx* c, const SortIn& in, const SortOut& out, const SortPlan& p, int shift, uint32_t* counts,
+                       const ZeroFill& z)
+{
+    ZeroFill rest = z;
+    if (p.count) {
+        k_sort_count<FIRST><<<p.blocks + zero_blocks(c, z.rows * z.cols * z.elem, kSortThreads), kSortThreads, 4 * p.row,
+                              c->stream>>>(in, p, shift, counts, z);
+        HGB_LAUNCHED(c, "k_sort_count");
+        rest = ZeroFill{};
+    }
+    if (p.items == 1) return launch_scatter<FIRST, 1>(c, in, out, p, shift, counts, rest);
+    if (p.items == 4) return launch_scatter<FIRST, 4>(c, in, out, p, shift, counts, rest);
+    return launch_scatter<FIRST, kSortItems>(c, in, out, p, shift, counts, rest);
+}
+
 // The sort of in.tokens into `out` (out.to: into whichever of a and b the
-// last pass writes; returned in *sorted), and the zeros beside it.
+// last pass writes; returned in *sorted), and the zeros beside it: an equal
+// part of their rows with each pass, so that the fill hides the passes' waits.
 hgb_status launch_sort(hgb_ctx* c, SortIn in, SortOut out, const SortPlan& p, const ZeroFill& z, uint32_t* counts, uint2* a,
                        uint2* b, const uint2** sorted)
 {
     if (p.small) {
         if (a) out.to = a;
         if (sorted) *sorted = a;
-        if (in.n <= 1024) return launch_sort_small<1>(c, in, out, p, z);
-        if (in.n <= 4096) return launch_sort_small<4>(c, in, out, p, z);
-        return launch_sort_small<kSortItems>(c, in, out, p, z);
+        return p.items == 1 ? launch_sort_small<1>(c, in, out, p, z) : launch_sort_small<4>(c, in, out, p, z);
     }
-    const size_t lds = 4 * ((size_t)(kSortThreads / 64) * p.radix + 2 * (size_t)p.radix + 16);
-    HGB_TRY(raise_lds(c, (const void*)k_sort_scatter<true>, lds));
-    HGB_TRY(raise_lds(c, (const void*)k_sort_scatter<false>, lds));
     for (int pass = 0; pass < p.passes; ++pass) {
         const int shift = pass * p.bits;
+        const int64_t first = z.rows * pass / p.passes, end = z.rows * (pass + 1) / p.passes;
+        ZeroFill part = z;
+        part.out = (char*)z.out + first * z.stride * z.elem;
+        part.rows = end - first;
         if (a) out.to = pass & 1 ? b : a;
         if (pass == 0) {
-            k_sort_count<true><<<p.blocks + zero_blocks(c, z.rows * z.cols * z.elem, kSortThreads), kSortThreads, 4 * p.radix,
-                                 c->stream>>>(in, p, shift, counts, z);
-            k_sort_scatter<true><<<p.blocks, kSortThreads, lds, c->stream>>>(in, out, p, shift, counts);
+            HGB_TRY(launch_pass<true>(c, in, out, p, shift, counts, part));
         } else {
             in.from = pass & 1 ? a : b;
-            k_sort_count<false><<<p.blocks, kSortThreads, 4 * p.radix, c->stream>>>(in, p, shift, counts, ZeroFill{});
-            k_sort_scatter<false><<<p.blocks, kSortThreads, lds, c->stream>>>(in, out, p, shift, counts);
+            HGB_TRY(launch_pass<false>(c, in, out, p, shift, counts, part));
         }
-        HGB_LAUNCHED(c, "k_sort_scatter");
     }
     if (sorted) *sorted = out.to;
     return HGB_OK;

@@ -37,15 +37,19 @@ static void plans()
                 CHECK((int64_t)p.bits * p.passes >= vec_bits(limit) && p.bits <= kSortBits);
                 CHECK(p.radix == 1 << p.bits && p.radix <= kSortThreads);
                 CHECK(p.small == (n <= kSortSmall));
+                CHECK(p.items == 1 || p.items == 4 || p.items == kSortItems);
+                const int64_t tile = (int64_t)p.items * kSortThreads;
+                // the blocks' shares cover every key, and none starts past the last
+                CHECK(p.blocks >= 1 && p.blocks <= kSortMaxBlocks);
+                CHECK(p.blocks * p.tiles * tile >= n);
+                CHECK((p.blocks - 1) * p.tiles * tile < n);
                 if (p.small) {
-                    CHECK(p.passes == 1 || p.bits <= kSortSmallBits);
-                    const int64_t pairs = p.passes > 1 ? 2 * kSortTile : 0;
+                    CHECK(p.blocks == 1 && p.tiles == 1 && p.items <= 4 && !p.count);
+                    const int64_t pairs = p.passes > 1 ? 2 * tile : 0;
                     CHECK(4 * (pairs + 16 * (int64_t)p.radix + p.radix + 16) <= 163840);
                 } else {
-                    // the blocks' shares cover every key, and none starts past the last
-                    CHECK(p.blocks >= 1 && p.blocks <= kSortMaxBlocks);
-                    CHECK((int64_t)p.blocks * p.tiles * kSortTile >= n);
-                    CHECK((int64_t)(p.blocks - 1) * p.tiles * kSortTile < n);
+                    CHECK(4 * (scatter_pair_words(p.items) + 18 * (int64_t)p.radix + 16) <= 163840);
+                    CHECK(p.count || p.blocks <= kSortSelf);
                 }
             }
     for (int64_t n : ns)
@@ -53,7 +57,7 @@ static void plans()
             const EmbedPlan p = plan_embed(n, 7196, dim);
             CHECK(p.chunk >= 1 && p.chunk <= kEmbedChunk && p.chunks * p.chunk >= n && (p.chunks - 1) * p.chunk < n);
             CHECK(p.part_stride >= dim && p.part_stride % 4 == 0);
-            CHECK(p.off_a >= (int64_t)p.sort.blocks * p.sort.radix * 4 && p.off_a % 16 == 0);
+            CHECK(p.off_a >= (p.sort.count ? (int64_t)p.sort.blocks * p.sort.radix * 4 : 0) && p.off_a % 16 == 0);
             CHECK(p.off_b >= p.off_a + n * 8 && p.off_b % 16 == 0);
             CHECK(p.off_part >= p.off_b + (p.sort.passes > 1 && !p.sort.small ? n * 8 : 0) && p.off_part % 16 == 0);
             CHECK(p.bytes >= p.off_part + p.chunks * 2 * p.part_stride * 4);
