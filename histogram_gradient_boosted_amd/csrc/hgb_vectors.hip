@@ -124,6 +124,19 @@ void by_shape(const NormPlan& p, F&& f)
     else with(std::integral_constant<int, 32>());
 }
 
+// Whether an output's rows are stored past the caches, in a call that reads
+// and writes `bytes`: where these exceed three quarters of the 256 MB of the
+// memory-side cache, what is left there of the output must be written out
+// beside a later kernel's reads.  In us, past the caches and not, bf16: embed of 3,670,016
+// tokens 81 and 152, then layer_norm of the same values 301 and 334 together;
+// of 1,835,008 tokens 129 and 173 together; of 917,504 tokens (a call of 118
+// MB) 71 and 64 together, so not below; route_gather and route_combine of
+// 32,768 rows of 1,024, four experts each, 136 and 158.
+bool streams(int64_t bytes, const void* out, int32_t type, int64_t stride)
+{
+    return bytes >= (int64_t)192 << 20 && (uintptr_t)out % 16 == 0 && stride * elem_size(type) % 16 == 0;
+}
+
 int log2_of(int p) { return 31 - __builtin_clz((unsigned)p); }
 
 hgb_status raise_lds(hgb_ctx* c, const void* fn, size_t bytes)
@@ -241,16 +254,10 @@ hgb_status hgb_embed(hgb_ctx* c, const void* table, int32_t table_type, int64_t 
             using U = std::remove_pointer_t<decltype(u)>;
             const int lg = log2_of(vec_group(dim, kVals<T, U>));
             const int64_t groups = 256 >> lg;
-            // four rows a group keep four loads in flight, where the tokens still give every CU a few blocks
-            if (n_tokens >= groups * 4 * 8 * c->n_cu) {
-                k_embed<T, U, 4><<<(unsigned)vec_ceil(n_tokens, groups * 4), 256, 0, c->stream>>>(
-                    (const T*)table, table_stride, vocab, dim, tokens, n_tokens, pad, scale, (U*)out, out_stride, lg,
-                    c->dev_words + kWordVectors);
-            } else {
-                k_embed<T, U, 1><<<(unsigned)vec_ceil(n_tokens, groups), 256, 0, c->stream>>>(
-                    (const T*)table, table_stride, vocab, dim, tokens, n_tokens, pad, scale, (U*)out, out_stride, lg,
-                    c->dev_words + kWordVectors);
-            }
+            const int64_t bytes = dim * (n_tokens * (int64_t)sizeof(U) + std::min(n_tokens, vocab) * (int64_t)sizeof(T));
+            k_embed<T, U><<<(unsigned)vec_ceil(n_tokens, groups), 256, 0, c->stream>>>(
+                (const T*)table, table_stride, (int)vocab, (int)dim, tokens, (int)n_tokens, pad, scale, (U*)out, out_stride, lg,
+                streams(bytes, out, out_type, out_stride), c->dev_words + kWordVectors);
             HGB_LAUNCHED(c, "k_embed");
             return HGB_OK;
         });
@@ -288,6 +295,7 @@ hgb_status hgb_embed_backward(hgb_ctx* c, const void* grad, int32_t grad_type, i
         z.cols = dim;
         z.stride = out_stride;
         z.elem = elem_size(out_type);
+        z.stream = streams(dim * (n_tokens * elem_size(grad_type) + vocab * z.elem), out, out_type, out_stride);
         if (n_tokens == 0) {
             k_zero_rows<<<(unsigned)std::min<int64_t>(vec_ceil(vocab * dim * z.elem, 4096 * 4), 8 * c->n_cu), 256, 0,
                           c->stream>>>(z);
@@ -349,7 +357,7 @@ hgb_status hgb_layer_norm(hgb_ctx* c, const void* x, int32_t type, int64_t x_str
                     const unsigned blocks =
                         (unsigned)std::min<int64_t>(vec_ceil(n_rows, p.per_block), (int64_t)c->n_cu * 2048 / THREADS);
                     k_norm<T, NV, WPR><<<blocks, THREADS, 0, c->stream>>>((const T*)x, x_stride, n_rows, (int)dim, weight, bias,
-                                                                          param_type, eps, (T*)y, y_stride, mean, rstd, p.log_group);
+                                                                          param_type, eps, (T*)y, y_stride, mean, rstd, p.log_group, streams(2 * n_rows * dim * elem_size(type), y, type, y_stride));
                 });
             }
             HGB_LAUNCHED(c, "k_norm");
@@ -408,7 +416,7 @@ hgb_status hgb_layer_norm_backward(hgb_ctx* c, const void* grad, int64_t grad_st
                     constexpr int NV = decltype(values)::value, WPR = decltype(waves)::value;
                     k_norm_grad<T, NV, WPR><<<(unsigned)parts, norm_threads(WPR), 0, c->stream>>>(
                         g, grad_stride, (const T*)x, x_stride, n_rows, (int)dim, mean, rstd, weight, param_type, (T*)dx,
-                        dx_stride, params ? (float*)workspace : nullptr, p.log_group);
+                        dx_stride, params ? (float*)workspace : nullptr, p.log_group, streams(3 * n_rows * dim * elem_size(type), dx, type, dx_stride));
                 });
                 HGB_LAUNCHED(c, "k_norm_grad");
             }
@@ -487,7 +495,7 @@ hgb_status hgb_route_gather(hgb_ctx* c, const void* x, int32_t type, int64_t x_s
             using T = std::remove_pointer_t<decltype(t)>;
             const int lg = log2_of(vec_group(dim, kVals<T>));
             k_route_gather<T><<<(unsigned)vec_ceil(n_rows, 256 >> lg), 256, 0, c->stream>>>(
-                (const T*)x, x_stride, n_rows, top, dim, position, offsets + n_experts, (T*)out, out_stride, lg);
+                (const T*)x, x_stride, n_rows, top, dim, position, offsets + n_experts, (T*)out, out_stride, lg, streams(n_rows * (top + 1) * dim * elem_size(type), out, type, out_stride));
             HGB_LAUNCHED(c, "k_route_gather");
             return HGB_OK;
         });
@@ -510,7 +518,7 @@ static hgb_status combine(hgb_ctx* c, const char* verb, const void* y, int32_t t
         using T = std::remove_pointer_t<decltype(t)>;
         const int lg = log2_of(vec_group(dim, kVals<T>));
         k_route_combine<T><<<(unsigned)vec_ceil(n_rows, 256 >> lg), 256, 0, c->stream>>>(
-            (const T*)y, y_stride, n_rows, top, dim, position, weight, (T*)out, out_stride, lg);
+            (const T*)y, y_stride, n_rows, top, dim, position, weight, (T*)out, out_stride, lg, streams(n_rows * (top + 1) * dim * elem_size(type), out, type, out_stride));
         HGB_LAUNCHED(c, "k_route_combine");
         return HGB_OK;
     });
@@ -556,7 +564,7 @@ hgb_status hgb_route_combine_backward(hgb_ctx* c, const void* grad, int32_t type
             using T = std::remove_pointer_t<decltype(t)>;
             k_route_combine_grad<T><<<(unsigned)vec_ceil(n_rows, 4), 256, 0, c->stream>>>(
                 (const T*)grad, grad_stride, (const T*)y, y_stride, n_rows, top, dim, position, offsets + n_experts, weight,
-                (T*)dy, dy_stride, dweight);
+                (T*)dy, dy_stride, dweight, streams(n_rows * ((dweight ? 2 : 1) * top + 1) * dim * elem_size(type), dy, type, dy_stride));
             HGB_LAUNCHED(c, "k_route_combine_grad");
             return HGB_OK;
         });

@@ -521,6 +521,24 @@ def test_route_leaves_out_bad_values_of_dropped_slots(torch, ctx):
     assert bool(torch.isfinite(dy).all()) and bool((dy[used:] == 0).all()) and bool((dw[7] == 0).all())
 
 
+# -- calls of more bytes than the caches keep, whose outputs are stored past them ---
+
+@pytest.mark.parametrize("n,vocab,dim,tt,vt,extra", [(1700001, 7196, 64, "f32", "bf16", 0), (100, 262144, 512, "bf16", "bf16", 0),
+                                                     (700000, 999, 100, "f32", "f32", 4), (150001, 300, 700, "f16", "f16", 1)])
+def test_large_embed(torch, ctx, n, vocab, dim, tt, vt, extra):
+    test_embed_and_its_gradient(torch, ctx, n, vocab, dim, "skewed", tt, vt, 3, extra, 0)
+
+
+@pytest.mark.parametrize("rows,dim,kind", [(34001, 1500, "bf16"), (60000, 501, "f32"), (150001, 400, "f16")])
+def test_large_layer_norm(torch, ctx, rows, dim, kind):
+    test_layer_norm_and_its_gradient(torch, ctx, rows, dim, kind, "f32", 0, 0, "both")
+
+
+@pytest.mark.parametrize("rows,top,dim,kind", [(20001, 4, 1024, "bf16"), (15000, 5, 603, "f32")])
+def test_large_route(torch, ctx, rows, top, dim, kind):
+    test_route_and_back(torch, ctx, rows, top, 64, dim, kind, 0.1, 0)
+
+
 # -- streams, graphs, refusals ------------------------------------------------------
 
 def step(torch, ctx, table, tok, w, b, e, share, n, top):
