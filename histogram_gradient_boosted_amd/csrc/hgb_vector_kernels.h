@@ -26,50 +26,52 @@ struct Vals {
     typedef T type __attribute__((ext_vector_type(V), aligned(sizeof(T))));
 };
 
-template <int V, typename T>
+// `left` of the values lie in the row, the others are zeros; EVEN: all do or
+// none, which spares the code for a part.
+template <int V, bool EVEN = false, typename T>
 __device__ inline typename Vals<T, V>::type load_raw(const T* p, int64_t left)
 {
-    typename Vals<T, V>::type v;
-    if (left >= V) {
+    typename Vals<T, V>::type v{};
+    if (EVEN ? left > 0 : left >= V) {
         v = *(const typename Vals<T, V>::type*)p;
-    } else {
+    } else if (!EVEN) {
 #pragma unroll
         for (int k = 0; k < V; ++k) v[k] = k < left ? p[k] : (T)0.0f;
     }
     return v;
 }
 
-template <int V, typename T>
+template <int V, bool EVEN = false, typename T>
 __device__ inline void load_vals(float (&r)[V], const T* p, int64_t left)
 {
-    const typename Vals<T, V>::type v = load_raw<V>(p, left);
+    const typename Vals<T, V>::type v = load_raw<V, EVEN>(p, left);
 #pragma unroll
     for (int k = 0; k < V; ++k) r[k] = (float)v[k];
 }
 
 // `stream`: past the caches, for large calls whose rows are 16-byte aligned.
-template <int V, typename T>
+template <int V, bool EVEN = false, typename T>
 __device__ inline void store_raw(const typename Vals<T, V>::type& v, T* p, int64_t left, bool stream)
 {
     typedef typename Vals<T, V>::type Vec;
     typedef uint32_t Words __attribute__((ext_vector_type(sizeof(Vec) / 4)));   // aligned: else the compiler drops the hint
-    if (left >= V) {
+    if (EVEN ? left > 0 : left >= V) {
         if (stream) __builtin_nontemporal_store(__builtin_bit_cast(Words, v), (Words*)p);
         else *(Vec*)p = v;
-    } else {
+    } else if (!EVEN) {
 #pragma unroll
         for (int k = 0; k < V; ++k)
             if (k < left) p[k] = v[k];
     }
 }
 
-template <int V, typename T>
+template <int V, bool EVEN = false, typename T>
 __device__ inline void store_vals(const float (&r)[V], T* p, int64_t left, bool stream = false)
 {
     typename Vals<T, V>::type v;
 #pragma unroll
     for (int k = 0; k < V; ++k) v[k] = (T)r[k];
-    store_raw<V>(v, p, left, stream);
+    store_raw<V, EVEN>(v, p, left, stream);
 }
 
 // x plus the value of the lane that CTRL names in its row of 16.
@@ -703,7 +705,8 @@ __device__ inline float block_sum(float x, float* tmp)   // 256 threads; tmp: fo
 // (k * span + lane) * V, where `span` lanes share the row: a part of a wave, a
 // wave (WPR = 1), or WPR waves, which are the whole block then.  With more than
 // 8 values a lane a row is longer than half of its columns (plan_norm), so that
-// only the upper half of the runs can pass its end.
+// only the upper half of the runs can pass its end.  EVEN: the row is a multiple
+// of V.
 template <typename T, int NV, int WPR>
 struct NormShape {
     static constexpr int V = kVals<T>, K = NV / V, kThreads = norm_threads(WPR);
@@ -763,18 +766,18 @@ __device__ inline void row_sums(float (&x)[N], int log_group, float* tmp, int& t
 }
 
 // V values of a parameter from column c on; `other` where there is none.
-template <int V>
+template <int V, bool EVEN>
 __device__ inline void load_param(float (&r)[V], const void* p, int type, int64_t c, int64_t left, float other)
 {
     if (!p || left <= 0) {
 #pragma unroll
         for (int k = 0; k < V; ++k) r[k] = other;
     } else if (type == 0) {
-        load_vals<V>(r, (const float*)p + c, left);
+        load_vals<V, EVEN>(r, (const float*)p + c, left);
     } else if (type == 1) {
-        load_vals<V>(r, (const __bf16*)p + c, left);
+        load_vals<V, EVEN>(r, (const __bf16*)p + c, left);
     } else {
-        load_vals<V>(r, (const _Float16*)p + c, left);
+        load_vals<V, EVEN>(r, (const _Float16*)p + c, left);
     }
 }
 
@@ -782,9 +785,9 @@ __device__ inline void load_param(float (&r)[V], const void* p, int type, int64_
 // mean) rstd weight + bias.  Bound by bytes: the row stays in registers between
 // its three uses, so x is read once, and the parameters stay there from row to
 // row.  A wave takes a row of up to 2,048 values: its sums need no barrier.
-// 32,768 rows of 1,792 bf16 values: 42.5 us, 5.5 TB/s (a large copy: 4.9); a
+// 32,768 rows of 1,792 bf16 values: 44 us, 5.3 TB/s (a large copy: 4.9); a
 // block a row that read the row three times took 235 us.
-template <typename T, int NV, int WPR>
+template <typename T, int NV, int WPR, bool EVEN>
 __global__ __launch_bounds__(norm_threads(WPR)) void k_norm(
     const T* __restrict__ x, int64_t x_stride, int64_t rows, int dim, const void* __restrict__ weight,
     const void* __restrict__ bias, int wtype, float eps, T* __restrict__ y, int64_t y_stride, float* __restrict__ mean,
@@ -794,14 +797,15 @@ __global__ __launch_bounds__(norm_threads(WPR)) void k_norm(
     constexpr int V = S::V, K = S::K;
     __shared__ float tmp[2 * WPR];
     int turn = 0;
+    if (NV > 8) log_group = 6;   // known to the compiler: the columns are fixed offsets then
     const int span = WPR > 1 ? S::kThreads : 1 << log_group, lane = threadIdx.x & (span - 1);
     const int per = S::kThreads / span;   // rows a block takes at a time
     float w[K][V], b[K][V];
 #pragma unroll
     for (int k = 0; k < K; ++k) {
         const int c = (k * span + lane) * V;
-        load_param<V>(w[k], weight, wtype, c, dim - c, 1.0f);
-        load_param<V>(b[k], bias, wtype, c, dim - c, 0.0f);
+        load_param<V, EVEN>(w[k], weight, wtype, c, dim - c, 1.0f);
+        load_param<V, EVEN>(b[k], bias, wtype, c, dim - c, 0.0f);
     }
     for (int64_t r = norm_row<NV>((int64_t)blockIdx.x * per, threadIdx.x / span); r < rows; r += (int64_t)gridDim.x * per) {
         const T* p = x + r * x_stride;
@@ -809,7 +813,7 @@ __global__ __launch_bounds__(norm_threads(WPR)) void k_norm(
 #pragma unroll
         for (int k = 0; k < K; ++k) {
             const int c = (k * span + lane) * V;
-            load_vals<V>(v[k], p + c, norm_left<S>(k, c, dim));
+            load_vals<V, EVEN>(v[k], p + c, norm_left<S>(k, c, dim));
         }
 #pragma unroll
         for (int k = 0; k < K; ++k)
@@ -823,7 +827,7 @@ __global__ __launch_bounds__(norm_threads(WPR)) void k_norm(
 #pragma unroll
             for (int i = 0; i < V; ++i) {
                 v[k][i] -= m;
-                if (k < S::kFull || (k * span + lane) * V + i < dim) s[0] = fmaf(v[k][i], v[k][i], s[0]);
+                if (k < S::kFull || (k * span + lane) * V + (EVEN ? 0 : i) < dim) s[0] = fmaf(v[k][i], v[k][i], s[0]);
             }
         row_sums<1, WPR>(s, log_group, tmp, turn);
         const float q = 1.0f / sqrtf(s[0] / (float)dim + eps);
@@ -832,7 +836,7 @@ __global__ __launch_bounds__(norm_threads(WPR)) void k_norm(
             const int c = (k * span + lane) * V;
 #pragma unroll
             for (int i = 0; i < V; ++i) v[k][i] = fmaf(v[k][i] * q, w[k][i], b[k][i]);
-            store_vals<V>(v[k], y + r * y_stride + c, norm_left<S>(k, c, dim), stream);
+            store_vals<V, EVEN>(v[k], y + r * y_stride + c, norm_left<S>(k, c, dim), stream);
         }
         if (lane == 0) {
             mean[r] = m;
@@ -845,32 +849,45 @@ __global__ __launch_bounds__(norm_threads(WPR)) void k_norm(
 // pass: a lane keeps the sums of its columns in registers, the block's waves
 // join theirs through LDS at the end (a fixed tree), and part
 // [blocks][2][dim] holds the blocks' sums for k_norm_join.  Bound by bytes,
-// each read and written once.  32,768 rows of 1,792 bf16 values: 78 us, 4.5
-// TB/s, and 5 us for k_norm_join; 120 us without the row ahead, 94 us with both
-// forms of the row in registers (which spill), 298 us as passes of their own
-// for dx and for the sums.
-template <typename T, int NV, int WPR>
-__global__ __launch_bounds__(norm_threads(WPR)) void k_norm_grad(
+// each read and written once.  32,768 rows of 1,792 bf16 values: 74 us, 4.8
+// TB/s, and 5 us for k_norm_join.  On the way: 298 us as passes of their own
+// for dx and for the sums, 120 in one pass, 94 with the next row ahead but both
+// forms of a row in registers, 78 with one form and two waves on a SIMD.
+template <typename T, int NV, int WPR, bool EVEN>
+__global__ __launch_bounds__(norm_grad_threads(NV, WPR)) void k_norm_grad(
     const T* __restrict__ grad, int64_t grad_stride, const T* __restrict__ x, int64_t x_stride, int64_t rows, int dim,
     const float* __restrict__ mean, const float* __restrict__ rstd, const void* __restrict__ weight, int wtype,
     T* __restrict__ dx, int64_t dx_stride, float* __restrict__ part, int log_group, bool stream)
 {
     using S = NormShape<T, NV, WPR>;
-    constexpr int V = S::V, K = S::K, WAVES = S::kThreads / 64;
+    constexpr int V = S::V, K = S::K, THREADS = norm_grad_threads(NV, WPR), WAVES = THREADS / 64;
+    // with 32 values a lane the weights are in LDS: a third wave on a SIMD is
+    // worth more than their registers
+    constexpr bool FAR = NV == 32;
     __shared__ float tmp[2 * 2 * WPR];
     __shared__ float sums[WPR > 1 ? 1 : WAVES / 2][WPR > 1 ? 1 : 64 * NV];
+    __shared__ __align__(16) float far[FAR ? 64 * WPR * NV : 1];
     int turn = 0;
-    const int span = WPR > 1 ? S::kThreads : 1 << log_group, lane = threadIdx.x & (span - 1);
-    const int per = S::kThreads / span;
+    if (NV > 8) log_group = 6;
+    const int span = WPR > 1 ? THREADS : 1 << log_group, lane = threadIdx.x & (span - 1);
+    const int per = THREADS / span;
     float w[K][V], dw[K][V], db[K][V];
 #pragma unroll
     for (int k = 0; k < K; ++k) {
         const int c = (k * span + lane) * V;
-        load_param<V>(w[k], weight, wtype, c, dim - c, 1.0f);
+        if (!FAR || (int)threadIdx.x < span) load_param<V, EVEN>(w[k], weight, wtype, c, dim - c, 1.0f);
 #pragma unroll
-        for (int i = 0; i < V; ++i) dw[k][i] = db[k][i] = 0.0f;
+        for (int i = 0; i < V; ++i) {
+            if (FAR && (int)threadIdx.x < span) far[c + i] = w[k][i];
+            dw[k][i] = db[k][i] = 0.0f;
+        }
     }
-    // The next row is on its way while a row is summed: with two waves on a
+    if (FAR) __syncthreads();
+    auto weights = [&](float (&v)[V], int k) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) v[i] = FAR ? far[(k * span + lane) * V + i] : w[k][i];
+    };
+    // The next row is on its way while a row is summed: with three waves on a
     // SIMD (the sums take the registers) nothing else hides its latency.  A row
     // is held as it was loaded and converted twice, for the same reason.  Where
     // the registers do not reach for that (32 values of 32 bits; the 128 a lane
@@ -884,8 +901,8 @@ __global__ __launch_bounds__(norm_threads(WPR)) void k_norm_grad(
         for (int k = 0; k < K; ++k) {
             const int c = (k * span + lane) * V;
             const int left = norm_left<S>(k, c, dim);
-            next_g[k] = load_raw<V>(grad + r * grad_stride + c, left);
-            next_x[k] = load_raw<V>(x + r * x_stride + c, left);
+            next_g[k] = load_raw<V, EVEN>(grad + r * grad_stride + c, left);
+            next_x[k] = load_raw<V, EVEN>(x + r * x_stride + c, left);
         }
         next_m = mean[r];
         next_q = rstd[r];
@@ -905,18 +922,24 @@ __global__ __launch_bounds__(norm_threads(WPR)) void k_norm_grad(
         if (AHEAD && r + step < rows) fetch(r + step);
         float s[2] = {0.0f, 0.0f};
 #pragma unroll
-        for (int k = 0; k < K; ++k)
+        for (int k = 0; k < K; ++k) {
+            float wk[V];
+            weights(wk, k);
 #pragma unroll
             for (int i = 0; i < V; ++i) {
                 float h = ((float)p[k][i] - m) * q;
                 // past the row's end g is 0, and h too: not a mean or rstd that may be infinite
-                if (k >= S::kFull && (k * span + lane) * V + i >= dim) h = 0.0f;
-                const float u = (float)g[k][i], v = u * w[k][i];
+                if (k >= S::kFull && (k * span + lane) * V + (EVEN ? 0 : i) >= dim) h = 0.0f;
+                const float u = (float)g[k][i], v = u * wk[i];
                 dw[k][i] = fmaf(u, h, dw[k][i]);
                 db[k][i] += u;
                 s[0] += v;
                 s[1] = fmaf(v, h, s[1]);
+                // added here and now: put off to the loop's end, which the compiler
+                // does, u and h of the whole row stay in registers
+                asm volatile("" : "+v"(dw[k][i]), "+v"(db[k][i]));
             }
+        }
         row_sums<2, WPR>(s, log_group, tmp, turn);
         const float a = s[0] / (float)dim, b = s[1] / (float)dim;
         if (sizeof(T) < 4) {
@@ -931,9 +954,10 @@ __global__ __launch_bounds__(norm_threads(WPR)) void k_norm_grad(
         for (int k = 0; k < K; ++k) {
             const int c = (k * span + lane) * V;
             float v[V];
+            weights(v, k);
 #pragma unroll
-            for (int i = 0; i < V; ++i) v[i] = q * fmaf(((float)p[k][i] - m) * q, -b, (float)g[k][i] * w[k][i] - a);
-            store_vals<V>(v, dx + r * dx_stride + c, norm_left<S>(k, c, dim), stream);
+            for (int i = 0; i < V; ++i) v[i] = q * fmaf(((float)p[k][i] - m) * q, -b, (float)g[k][i] * v[i] - a);
+            store_vals<V, EVEN>(v, dx + r * dx_stride + c, norm_left<S>(k, c, dim), stream);
         }
     }
     if (!part) return;
@@ -947,14 +971,15 @@ __global__ __launch_bounds__(norm_threads(WPR)) void k_norm_grad(
                     dw[k][i] += __shfl_xor(dw[k][i], d, 64);
                     db[k][i] += __shfl_xor(db[k][i], d, 64);
                 }
-        auto join = [&](float (&v)[K][V], int half) {
-            if (wave >= half && wave < 2 * half)
+        // waves [half, waves) add theirs to the first waves - half
+        auto join = [&](float (&v)[K][V], int waves, int half) {
+            if (wave >= half && wave < waves)
 #pragma unroll
                 for (int k = 0; k < K; ++k)
 #pragma unroll
                     for (int i = 0; i < V; ++i) sums[wave - half][(k * V + i) * 64 + l] = v[k][i];
             __syncthreads();
-            if (wave < half)
+            if (wave < waves - half)
 #pragma unroll
                 for (int k = 0; k < K; ++k)
 #pragma unroll
@@ -962,9 +987,9 @@ __global__ __launch_bounds__(norm_threads(WPR)) void k_norm_grad(
             __syncthreads();
         };
 #pragma unroll
-        for (int half = WAVES / 2; half > 0; half /= 2) {
-            join(dw, half);
-            join(db, half);
+        for (int waves = WAVES; waves > 1; waves = (waves + 1) / 2) {
+            join(dw, waves, (waves + 1) / 2);
+            join(db, waves, (waves + 1) / 2);
         }
         if ((int)threadIdx.x >= span) return;
     }
@@ -972,8 +997,8 @@ __global__ __launch_bounds__(norm_threads(WPR)) void k_norm_grad(
 #pragma unroll
     for (int k = 0; k < K; ++k) {
         const int c = (k * span + lane) * V;
-        store_vals<V>(dw[k], to + c, dim - c);
-        store_vals<V>(db[k], to + dim + c, dim - c);
+        store_vals<V, EVEN>(dw[k], to + c, dim - c);
+        store_vals<V, EVEN>(db[k], to + dim + c, dim - c);
     }
 }
 

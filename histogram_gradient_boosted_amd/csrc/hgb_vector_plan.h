@@ -140,6 +140,10 @@ constexpr int kNormMaxDim = 16384;     // 16 values a lane, 16 waves (32 spill: 
 constexpr int kNormParts = 256;        // blocks of the backward pass: one a CU
 constexpr int norm_threads(int waves) { return waves > 1 ? 64 * waves : kNormThreads; }
 
+// Threads of a block of the backward pass: with 32 values a lane the registers
+// hold three waves on a SIMD.
+constexpr int norm_grad_threads(int values, int waves) { return waves == 1 && values == 32 ? 768 : norm_threads(waves); }
+
 struct NormPlan {
     int values = 0;
     int waves = 1;
@@ -168,7 +172,8 @@ inline int norm_parts(int64_t rows) { return (int)std::min<int64_t>(kNormParts, 
 inline int norm_blocks(int64_t rows, const NormPlan& p)
 {
     const int64_t most = p.waves == 4 ? 2 * kNormParts : kNormParts;   // blocks of four waves: two a CU
-    return (int)std::min<int64_t>(most, std::max<int64_t>(1, vec_ceil(rows, p.per_block)));
+    const int64_t each = p.waves > 1 ? 1 : norm_grad_threads(p.values, 1) >> p.log_group;   // rows of a block at a time
+    return (int)std::min<int64_t>(most, std::max<int64_t>(1, vec_ceil(rows, each)));
 }
 inline int64_t norm_workspace(int64_t rows, int64_t dim)
 {

@@ -110,16 +110,21 @@ hgb_status by_pair(int32_t table, int32_t vec, F&& f)
     return by_type(vec, [&](auto* v) { return f(v, v); });
 }
 
-// f with the plan's values a lane and waves a row as types.
+// f with the plan's values a lane and waves a row, and whether the rows are
+// `even`, as types.
 template <typename F>
-void by_shape(const NormPlan& p, F&& f)
+void by_shape(const NormPlan& p, bool even, F&& f)
 {
-    auto with = [&](auto values) {
-        if (p.waves == 4) f(values, std::integral_constant<int, 4>());
-        else f(values, std::integral_constant<int, 1>());
+    auto shaped = [&](auto values, auto waves) {
+        if (even) f(values, waves, std::true_type());
+        else f(values, waves, std::false_type());
     };
-    if (p.waves == 16) f(std::integral_constant<int, 16>(), std::integral_constant<int, 16>());
-    else if (p.values == 8) f(std::integral_constant<int, 8>(), std::integral_constant<int, 1>());
+    auto with = [&](auto values) {
+        if (p.waves == 4) shaped(values, std::integral_constant<int, 4>());
+        else shaped(values, std::integral_constant<int, 1>());
+    };
+    if (p.waves == 16) shaped(std::integral_constant<int, 16>(), std::integral_constant<int, 16>());
+    else if (p.values == 8) shaped(std::integral_constant<int, 8>(), std::integral_constant<int, 1>());
     else if (p.values == 16) with(std::integral_constant<int, 16>());
     else with(std::integral_constant<int, 32>());
 }
@@ -352,11 +357,11 @@ hgb_status hgb_layer_norm(hgb_ctx* c, const void* x, int32_t type, int64_t x_str
                 k_norm_wide<T><<<(unsigned)std::min<int64_t>(n_rows, 65536), 256, 0, c->stream>>>(
                     (const T*)x, x_stride, n_rows, dim, weight, bias, param_type, eps, (T*)y, y_stride, mean, rstd);
             } else {
-                by_shape(p, [&](auto values, auto waves) {
+                by_shape(p, dim % kVals<T> == 0, [&](auto values, auto waves, auto even) {
                     constexpr int NV = decltype(values)::value, WPR = decltype(waves)::value, THREADS = norm_threads(WPR);
                     const unsigned blocks =
                         (unsigned)std::min<int64_t>(vec_ceil(n_rows, p.per_block), (int64_t)c->n_cu * 2048 / THREADS);
-                    k_norm<T, NV, WPR><<<blocks, THREADS, 0, c->stream>>>((const T*)x, x_stride, n_rows, (int)dim, weight, bias,
+                    k_norm<T, NV, WPR, decltype(even)::value><<<blocks, THREADS, 0, c->stream>>>((const T*)x, x_stride, n_rows, (int)dim, weight, bias,
                                                                           param_type, eps, (T*)y, y_stride, mean, rstd, p.log_group, streams(2 * n_rows * dim * elem_size(type), y, type, y_stride));
                 });
             }
@@ -412,9 +417,9 @@ hgb_status hgb_layer_norm_backward(hgb_ctx* c, const void* grad, int64_t grad_st
                     HGB_LAUNCHED(c, "k_norm_wide_params");
                 }
             } else if (n_rows > 0 || params) {
-                by_shape(p, [&](auto values, auto waves) {
+                by_shape(p, dim % kVals<T> == 0, [&](auto values, auto waves, auto even) {
                     constexpr int NV = decltype(values)::value, WPR = decltype(waves)::value;
-                    k_norm_grad<T, NV, WPR><<<(unsigned)parts, norm_threads(WPR), 0, c->stream>>>(
+                    k_norm_grad<T, NV, WPR, decltype(even)::value><<<(unsigned)parts, norm_grad_threads(NV, WPR), 0, c->stream>>>(
                         g, grad_stride, (const T*)x, x_stride, n_rows, (int)dim, mean, rstd, weight, param_type, (T*)dx,
                         dx_stride, params ? (float*)workspace : nullptr, p.log_group, streams(3 * n_rows * dim * elem_size(type), dx, type, dx_stride));
                 });
