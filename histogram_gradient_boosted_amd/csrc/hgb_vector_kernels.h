@@ -549,15 +549,20 @@ __global__ __launch_bounds__(256) void k_embed_sum(const uint2* __restrict__ pai
                 store_vals<V>(acc, out + (int64_t)cur * out_stride + c, left);
             }
         };
+        uint2 ahead[STEP];   // the next step's pairs
+#pragma unroll
+        for (int u = 0; u < STEP; ++u) ahead[u] = pairs[begin + u < end ? begin + u : end - 1];
         for (int64_t j = begin; j < end; j += STEP) {
             uint2 kv[STEP];
             typename Vals<T, V>::type v[STEP];
 #pragma unroll
-            for (int u = 0; u < STEP; ++u) kv[u] = pairs[j + u < end ? j + u : end - 1];
+            for (int u = 0; u < STEP; ++u) kv[u] = ahead[u];
             // a dropped token's row is not read: its sum, which no one stores, takes row 0
 #pragma unroll
             for (int u = 0; u < STEP; ++u)
-                v[u] = load_raw<V>(grad + (kv[u].x < (uint32_t)vocab ? (int64_t)kv[u].y : 0) * grad_stride + c, left);
+                v[u] = load_raw<V>(grad + (kv[u].x < (uint32_t)vocab ? (uint64_t)kv[u].y : 0) * (uint64_t)grad_stride + c, left);
+#pragma unroll
+            for (int u = 0; u < STEP; ++u) ahead[u] = pairs[j + STEP + u < end ? j + STEP + u : end - 1];
 #pragma unroll
             for (int u = 0; u < STEP; ++u) {
                 if (j + u >= end) break;

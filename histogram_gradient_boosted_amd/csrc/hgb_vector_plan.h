@@ -105,6 +105,7 @@ struct EmbedPlan {
 };
 
 constexpr int kEmbedChunk = 256;         // largest chunk
+constexpr int kEmbedFew = 32;
 constexpr int64_t kEmbedWaves = 2048;    // chunks are halved until this many waves run (8 a CU)
 
 inline EmbedPlan plan_embed(int64_t n, int64_t vocab, int64_t dim)
@@ -114,8 +115,9 @@ inline EmbedPlan plan_embed(int64_t n, int64_t vocab, int64_t dim)
     // The narrowest lanes' values (4) decide, so that the plan and the
     // workspace do not depend on the types.
     const int64_t group = vec_group(dim, 4), slices = vec_ceil(dim, 64 * 4);
-    p.chunk = kEmbedChunk;
-    while (p.chunk > 8 && vec_ceil(n, p.chunk) * group * slices / 64 < kEmbedWaves) p.chunk /= 2;
+    // a handful of tokens is one chunk: nothing to join
+    p.chunk = n <= kEmbedFew ? kEmbedFew : kEmbedChunk;
+    while (n > kEmbedFew && p.chunk > 8 && vec_ceil(n, p.chunk) * group * slices / 64 < kEmbedWaves) p.chunk /= 2;
     p.chunks = vec_ceil(n, p.chunk);
     p.part_stride = vec_up(dim, 4);
     p.off_a = p.sort.count ? vec_up((int64_t)p.sort.blocks * p.sort.row * 4, 256) : 0;
