@@ -499,7 +499,7 @@ class Context:
             code = self._types.get(dtype)
             if code is None:
                 raise ValueError(f"dtype must be float32, bfloat16 or float16, got {dtype}")
-            out = self._torch.empty(shape, dtype=dtype, device=self._torch_device)
+            out = self._torch.empty(*shape, dtype=dtype, device=self._torch_device)
             return out, out.data_ptr(), code, dim
         p, code, _, _, stride = self._rows(out, "out", dim, rows, dtype)
         return out, p, code, stride
