@@ -26,52 +26,82 @@ struct Vals {
     typedef T type __attribute__((ext_vector_type(V), aligned(sizeof(T))));
 };
 
-// `left` of the values lie in the row, the others are zeros; EVEN: all do or
-// none, which spares the code for a part.
-template <int V, bool EVEN = false, typename T>
+// `left` of the values lie in the row, the others are zeros.  WHOLE: all do or
+// none, which spares the code for a part: a row's last vector then ends where
+// the row does and shares values with the one before it (both store the same).
+template <int V, bool WHOLE = false, typename T>
 __device__ inline typename Vals<T, V>::type load_raw(const T* p, int64_t left)
 {
     typename Vals<T, V>::type v{};
-    if (EVEN ? left > 0 : left >= V) {
+    if (WHOLE ? left > 0 : left >= V) {
         v = *(const typename Vals<T, V>::type*)p;
-    } else if (!EVEN) {
+    } else if (!WHOLE) {
 #pragma unroll
         for (int k = 0; k < V; ++k) v[k] = k < left ? p[k] : (T)0.0f;
     }
     return v;
 }
 
-template <int V, bool EVEN = false, typename T>
+template <int V, bool WHOLE = false, typename T>
 __device__ inline void load_vals(float (&r)[V], const T* p, int64_t left)
 {
-    const typename Vals<T, V>::type v = load_raw<V, EVEN>(p, left);
+    const typename Vals<T, V>::type v = load_raw<V, WHOLE>(p, left);
 #pragma unroll
     for (int k = 0; k < V; ++k) r[k] = (float)v[k];
 }
 
 // `stream`: past the caches, for large calls whose rows are 16-byte aligned.
-template <int V, bool EVEN = false, typename T>
+template <int V, bool WHOLE = false, typename T>
 __device__ inline void store_raw(const typename Vals<T, V>::type& v, T* p, int64_t left, bool stream)
 {
     typedef typename Vals<T, V>::type Vec;
     typedef uint32_t Words __attribute__((ext_vector_type(sizeof(Vec) / 4)));   // aligned: else the compiler drops the hint
-    if (EVEN ? left > 0 : left >= V) {
+    if (WHOLE ? left > 0 : left >= V) {
         if (stream) __builtin_nontemporal_store(__builtin_bit_cast(Words, v), (Words*)p);
         else *(Vec*)p = v;
-    } else if (!EVEN) {
+    } else if (!WHOLE) {
 #pragma unroll
         for (int k = 0; k < V; ++k)
             if (k < left) p[k] = v[k];
     }
 }
 
-template <int V, bool EVEN = false, typename T>
+template <int V, bool WHOLE = false, typename T>
 __device__ inline void store_vals(const float (&r)[V], T* p, int64_t left, bool stream = false)
 {
     typename Vals<T, V>::type v;
 #pragma unroll
     for (int k = 0; k < V; ++k) v[k] = (T)r[k];
-    store_raw<V, EVEN>(v, p, left, stream);
+    store_raw<V, WHOLE>(v, p, left, stream);
+}
+
+// A thread's place among rows of `dim` (plan_rows): its row, the first column
+// of its vector (the last vector is moved back to end with the row) and
+// whether it has one.
+struct RowPlace {
+    int64_t r;
+    int c;
+    bool in;
+};
+
+template <int V>
+__device__ inline RowPlace row_place(const RowMap& m, int64_t rows, int dim)
+{
+    const int t = threadIdx.x;
+    RowPlace p;
+    int j;
+    if (m.slices > 1) {
+        p.r = blockIdx.x / (uint32_t)m.slices;
+        j = (int)(blockIdx.x % (uint32_t)m.slices) * 256 + t;
+        p.in = j < m.vecs;
+    } else {
+        const int q = (t * m.magic) >> 16;
+        j = t - q * m.vecs;
+        p.r = (int64_t)blockIdx.x * m.per + q;
+        p.in = q < m.per && p.r < rows;
+    }
+    p.c = dim < V ? 0 : min(j * V, dim - V);
+    return p;
 }
 
 // x plus the value of the lane that CTRL names in its row of 16.
@@ -472,43 +502,40 @@ __global__ __launch_bounds__(kSortThreads, 8) void k_sort_scatter(SortIn in, Sor
 // Embedding
 // ---------------------------------------------------------------------------
 
-// out[i] = scale * table[token i]; a group of lanes takes a token.  Bound by
-// the bytes written (the table's rows come from L2): 3,670,016 rows of 64 bf16
-// values in 81 us, 5.8 TB/s (a fill: 84 us).  Four tokens a group 90 us: more
+// out[i] = scale * table[token i], a vector a thread.  Bound by the bytes
+// written (the table's rows come from L2): 3,670,016 rows of 64 bf16 values in
+// 81 us, 5.8 TB/s (a fill: 84 us).  Four tokens a thread 90 us: more
 // instructions before the first store, and blocks less in order.
 template <typename T, typename U>
 __global__ __launch_bounds__(256) void k_embed(const T* __restrict__ table, int64_t table_stride, int vocab, int dim,
                                                const int32_t* __restrict__ tokens, int n, int32_t pad, float scale,
-                                               U* __restrict__ out, int64_t out_stride, int log_group, bool stream,
+                                               U* __restrict__ out, int64_t out_stride, RowMap m, bool stream,
                                                uint32_t* err)
 {
     constexpr int V = kVals<T, U>;
-    const int groups = 256 >> log_group, g = threadIdx.x >> log_group, lane = threadIdx.x & ((1 << log_group) - 1);
-    const int64_t first = (int64_t)blockIdx.x * groups;
-    if (first + g >= n) return;
-    const int32_t t = tokens[first + g];
+    const RowPlace at = row_place<V>(m, n, dim);
+    if (!at.in) return;
+    const int32_t t = tokens[at.r];
     const bool live = t != pad && (uint32_t)t < (uint32_t)vocab;
-    if (!live && t != pad && lane == 0) atomicOr(err, kVecErrToken);
-    const T* from = table + (uint64_t)(live ? (uint32_t)t : 0) * (uint64_t)table_stride;
-    U* to = out + first * out_stride + (uint64_t)(uint32_t)g * (uint64_t)out_stride;
-    auto row = [&](auto even) {
-        for (int c = lane * V; c < dim; c += V << log_group) {
-            const int left = decltype(even)::value ? V : dim - c;
-            float v[V];
-            if (live) load_vals<V>(v, from + c, left);
+    if (!live && t != pad && at.c == 0) atomicOr(err, kVecErrToken);
+    const T* from = table + (uint64_t)(live ? (uint32_t)t : 0) * (uint64_t)table_stride + at.c;
+    U* to = out + (uint64_t)(uint32_t)at.r * (uint64_t)out_stride + at.c;
+    auto copy = [&](auto whole) {
+        constexpr bool WHOLE = decltype(whole)::value;
+        float v[V];
+        load_vals<V, WHOLE>(v, from, live ? dim : 0);
 #pragma unroll
-            for (int k = 0; k < V; ++k) v[k] = live ? v[k] * scale : 0.0f;
-            store_vals<V>(v, to + c, left, stream);
-        }
+        for (int k = 0; k < V; ++k) v[k] = live ? v[k] * scale : 0.0f;
+        store_vals<V, WHOLE>(v, to, dim, stream);
     };
-    if (dim % V == 0) row(std::true_type());
-    else row(std::false_type());
+    if (dim >= V) copy(std::true_type());
+    else copy(std::false_type());
 }
 
 __global__ __launch_bounds__(256) void k_zero_rows(ZeroFill z) { zero_fill(z, blockIdx.x, gridDim.x); }
 
-// Sums of the gradient's rows over each run of equal keys.  A group of lanes
-// walks one chunk of sorted positions; a run that lies in its chunk is
+// Sums of the gradient's rows over each run of equal keys.  The threads of a
+// row's vectors walk one chunk of sorted positions; a run that lies in its chunk is
 // finished there, and a run that crosses a border leaves its part in the
 // chunk's partial rows: row 0 a run that began before the chunk, row 1 one
 // that begins in it and goes on.  The order of the sums depends on the tokens
@@ -519,21 +546,19 @@ template <typename T, typename U>
 __global__ __launch_bounds__(256) void k_embed_sum(const uint2* __restrict__ pairs, int64_t n, const T* __restrict__ grad,
                                                    int64_t grad_stride, int64_t dim, int64_t vocab, float scale,
                                                    U* __restrict__ out, int64_t out_stride, float* __restrict__ part,
-                                                   int64_t part_stride, int chunk, int log_group)
+                                                   int64_t part_stride, int chunk, int64_t chunks, RowMap m)
 {
     constexpr int V = kVals<T, U>;
-    const int lane = threadIdx.x & ((1 << log_group) - 1);
-    const int64_t id = (int64_t)blockIdx.x * (256 >> log_group) + (threadIdx.x >> log_group);
-    const int64_t c = ((int64_t)blockIdx.y << log_group) * V + (int64_t)lane * V;
-    const int64_t begin = id * chunk, end = begin + chunk < n ? begin + chunk : n;
-    if (begin >= n || c >= dim) return;
+    const RowPlace at = row_place<V>(m, chunks, (int)dim);
+    if (!at.in) return;
+    const int64_t id = at.r, c = at.c, begin = id * chunk, end = begin + chunk < n ? begin + chunk : n;
     const uint32_t none = 0xffffffffu;
     const uint32_t prev = begin > 0 ? pairs[begin - 1].x : none, next = end < n ? pairs[end].x : none;
-    // STEP rows in flight; fewer where the row ends in the lane's columns, whose
+    // STEP rows in flight; fewer where a row is shorter than a vector and its
     // values are loaded one by one
     auto walk = [&](auto step) {
         constexpr int STEP = decltype(step)::value;
-        const int64_t left = STEP == 8 ? V : dim - c;
+        constexpr bool WHOLE = STEP == 8;
         uint32_t cur = pairs[begin].x;
         bool head = cur == prev;
         float acc[V];
@@ -542,11 +567,11 @@ __global__ __launch_bounds__(256) void k_embed_sum(const uint2* __restrict__ pai
         auto flush = [&](bool open) {
             if (cur >= (uint32_t)vocab) return;
             if (head || open) {
-                store_vals<V>(acc, part + (id * 2 + (head ? 0 : 1)) * part_stride + c, left);
+                store_vals<V, WHOLE>(acc, part + (id * 2 + (head ? 0 : 1)) * part_stride + c, dim);
             } else {
 #pragma unroll
                 for (int k = 0; k < V; ++k) acc[k] *= scale;
-                store_vals<V>(acc, out + (int64_t)cur * out_stride + c, left);
+                store_vals<V, WHOLE>(acc, out + (int64_t)cur * out_stride + c, dim);
             }
         };
         uint2 ahead[STEP];   // the next step's pairs
@@ -560,7 +585,7 @@ __global__ __launch_bounds__(256) void k_embed_sum(const uint2* __restrict__ pai
             // a dropped token's row is not read: its sum, which no one stores, takes row 0
 #pragma unroll
             for (int u = 0; u < STEP; ++u)
-                v[u] = load_raw<V>(grad + (kv[u].x < (uint32_t)vocab ? (uint64_t)kv[u].y : 0) * (uint64_t)grad_stride + c, left);
+                v[u] = load_raw<V, WHOLE>(grad + (kv[u].x < (uint32_t)vocab ? (uint64_t)kv[u].y : 0) * (uint64_t)grad_stride + c, dim);
 #pragma unroll
             for (int u = 0; u < STEP; ++u) ahead[u] = pairs[j + STEP + u < end ? j + STEP + u : end - 1];
 #pragma unroll
@@ -579,101 +604,99 @@ __global__ __launch_bounds__(256) void k_embed_sum(const uint2* __restrict__ pai
         }
         flush(cur == next);
     };
-    if (dim - c >= V) walk(std::integral_constant<int, 8>());
+    if (dim >= V) walk(std::integral_constant<int, 8>());
     else walk(std::integral_constant<int, 4>());
 }
 
 // Runs that cross chunk borders: the partial row of the chunk where the run
 // begins plus row 0 of each chunk it goes on in.  A block takes kJoinChunks
-// chunks and 64 columns: a wave sums a short run, the whole block a long one
-// (16 rows at a time, joined in a fixed order).  Bound by its chain of loads
-// that wait for one another: 4 us for 5,001 tokens, 9 us for 3,670,016.
-constexpr int kJoinChunks = 4;
+// chunks and 64 columns: a wave sums a short run, the whole block a long one,
+// joined in a fixed order.  Bound by its chain of loads that wait for one
+// another.
+constexpr int kJoinThreads = 256;
+constexpr int kJoinChunks = kJoinThreads / 64;
 constexpr int kJoinLong = 32;
 
 template <typename U>
-__global__ __launch_bounds__(256) void k_embed_join(const uint2* __restrict__ pairs, int64_t n, int64_t dim, int64_t vocab,
-                                                    float scale, U* __restrict__ out, int64_t out_stride,
-                                                    const float* __restrict__ part, int64_t part_stride, int chunk,
-                                                    int64_t chunks)
+__global__ __launch_bounds__(kJoinThreads) void k_embed_join(const uint2* __restrict__ pairs, int64_t n, int64_t dim,
+                                                             int64_t vocab, float scale, U* __restrict__ out,
+                                                             int64_t out_stride, const float* __restrict__ part,
+                                                             int64_t part_stride, int chunk, int64_t chunks, int log_cols)
 {
     __shared__ int64_t last[kJoinChunks];   // the run's last chunk; -1: no run to join here
     __shared__ uint32_t key[kJoinChunks];
-    __shared__ float4 sums[4][16];
-    const int64_t base = (int64_t)blockIdx.x * kJoinChunks;
-    const int w = threadIdx.x >> 6, lane = threadIdx.x & 63, row = lane >> 4;
-    // each wave looks for the runs of its chunks, 64 chunks at a glance
-    constexpr int EACH = kJoinChunks / 4;
-    uint32_t front[EACH], k[EACH], after[EACH], prev[EACH];
-#pragma unroll
-    for (int u = 0; u < EACH; ++u) {
-        const int64_t id = base + w * EACH + u, begin = id * chunk, end = begin + chunk;
-        const bool more = id + 1 < chunks;
-        front[u] = more ? pairs[begin].x : 0;
-        k[u] = more ? pairs[end - 1].x : 0;
-        after[u] = more ? pairs[end].x : ~0u;
-        prev[u] = more && begin > 0 ? pairs[begin - 1].x : ~0u;
-    }
-#pragma unroll
-    for (int u = 0; u < EACH; ++u) {
+    __shared__ float4 sums[kJoinChunks][16];
+    const int w = threadIdx.x >> 6, lane = threadIdx.x & 63;
+    const int64_t id = (int64_t)blockIdx.x * kJoinChunks + w;
+    // each wave looks for the run of its chunk, 64 chunks at a glance
+    {
         int64_t e = -1;
-        const bool whole = front[u] == k[u] && prev[u] == k[u];   // the run began before this chunk
-        if (after[u] == k[u] && !whole && k[u] < (uint32_t)vocab) {
-            e = base + w * EACH + u + 1;   // a chunk that begins with the run
-            for (int len = 64; len == 64; e += len) {
-                const int64_t at = e + 1 + lane;
-                const uint64_t other = ~__ballot(at < chunks && pairs[at * chunk].x == k[u]);
-                len = other ? __ffsll((unsigned long long)other) - 1 : 64;
+        uint32_t k = 0;
+        if (id + 1 < chunks) {
+            const int64_t begin = id * chunk, end = begin + chunk;
+            const uint32_t front = pairs[begin].x, after = pairs[end].x, prev = begin > 0 ? pairs[begin - 1].x : ~0u;
+            k = pairs[end - 1].x;
+            const bool whole = front == k && prev == k;   // the run began before this chunk
+            if (after == k && !whole && k < (uint32_t)vocab) {
+                e = id + 1;   // a chunk that begins with the run
+                for (int len = 64; len == 64; e += len) {
+                    const int64_t at = e + 1 + lane;
+                    const uint64_t other = ~__ballot(at < chunks && pairs[at * chunk].x == k);
+                    len = other ? __ffsll((unsigned long long)other) - 1 : 64;
+                }
             }
         }
         if (lane == 0) {
-            last[w * EACH + u] = e;
-            key[w * EACH + u] = k[u];
+            last[w] = e;
+            key[w] = k;
         }
     }
     __syncthreads();
-    const int64_t c = (int64_t)blockIdx.y * 64 + (lane & 15) * 4;
+    // 2^log_cols lanes hold a row's columns, four each; the others take further rows
+    const int cols = 1 << log_cols, row = lane >> log_cols, rows = 64 >> log_cols;
+    const int64_t c = (int64_t)blockIdx.y * 64 + (lane & (cols - 1)) * 4;
     const bool in = c < dim;   // part rows are padded to four floats
-    for (int s = 0; s < kJoinChunks; ++s) {
-        const int64_t e = last[s], id = base + s;
-        if (e < 0) continue;
-        const bool whole_block = e - id > kJoinLong;
-        if (!whole_block && (s & 3) != w) continue;
-        const int rows = whole_block ? 16 : 4;
+    auto sum = [&](int64_t first, int64_t e, int from, int step) {
         float4 a = make_float4(0, 0, 0, 0);
         if (in)
-#pragma unroll 4
-            for (int64_t k = id + (whole_block ? w * 4 + row : row); k <= e; k += rows) {
-                const float4 v = *(const float4*)(part + (k * 2 + (k == id ? 1 : 0)) * part_stride + c);
+#pragma unroll 8
+            for (int64_t k = first + from; k <= e; k += step) {
+                const float4 v = *(const float4*)(part + (k * 2 + (k == first ? 1 : 0)) * part_stride + c);
                 a.x += v.x;
                 a.y += v.y;
                 a.z += v.z;
                 a.w += v.w;
             }
-#pragma unroll
-        for (int d = 16; d < 64; d *= 2) {
+        for (int d = cols; d < 64; d *= 2) {
             a.x += __shfl_xor(a.x, d, 64);
             a.y += __shfl_xor(a.y, d, 64);
             a.z += __shfl_xor(a.z, d, 64);
             a.w += __shfl_xor(a.w, d, 64);
         }
-        if (whole_block) {
-            __syncthreads();
-            if (lane < 16) sums[w][lane] = a;
-            __syncthreads();
-            if (w != 0) continue;
-            a = make_float4(0, 0, 0, 0);
-            for (int k = 0; k < 4; ++k) {
-                const float4 v = sums[k][lane & 15];
-                a.x += v.x;
-                a.y += v.y;
-                a.z += v.z;
-                a.w += v.w;
+        return a;
+    };
+    auto store = [&](const float4& a, uint32_t k) {
+        const float r[4] = {a.x * scale, a.y * scale, a.z * scale, a.w * scale};
+        if (lane < cols && in) store_vals<4>(r, out + (int64_t)k * out_stride + c, dim - c);
+    };
+    if (last[w] >= 0 && last[w] - id <= kJoinLong) store(sum(id, last[w], row, rows), key[w]);
+    for (int s = 0; s < kJoinChunks; ++s) {
+        const int64_t first = (int64_t)blockIdx.x * kJoinChunks + s;
+        if (last[s] - first <= kJoinLong) continue;
+        const float4 a = sum(first, last[s], w * rows + row, kJoinChunks * rows);
+        __syncthreads();
+        if (lane < cols) sums[w][lane] = a;
+        __syncthreads();
+        if (w == 0) {
+            float4 t = make_float4(0, 0, 0, 0);
+            for (int k = 0; k < kJoinChunks; ++k) {
+                const float4 v = sums[k][lane & (cols - 1)];
+                t.x += v.x;
+                t.y += v.y;
+                t.z += v.z;
+                t.w += v.w;
             }
-        }
-        if (lane < 16 && in) {
-            const float r[4] = {a.x * scale, a.y * scale, a.z * scale, a.w * scale};
-            store_vals<4>(r, out + (int64_t)key[s] * out_stride + c, dim - c);
+            store(t, key[s]);
         }
     }
 }
@@ -710,8 +733,13 @@ __device__ inline float block_sum(float x, float* tmp)   // 256 threads; tmp: fo
 // (k * span + lane) * V, where `span` lanes share the row: a part of a wave, a
 // wave (WPR = 1), or WPR waves, which are the whole block then.  With more than
 // 8 values a lane a row is longer than half of its columns (plan_norm), so that
-// only the upper half of the runs can pass its end.  EVEN: the row is a multiple
-// of V.
+// only the upper half of the runs can pass its end.  TAIL says how a row ends:
+// with a vector (kEven), inside one, which is moved back then so that it ends
+// with the row and shares values with the one before (kBack: both compute the
+// same, and the sums over the row leave the shared values of the last one out),
+// or it is shorter than a vector (kPart).
+constexpr int kEven = 0, kBack = 1, kPart = 2;
+
 template <typename T, int NV, int WPR>
 struct NormShape {
     static constexpr int V = kVals<T>, K = NV / V, kThreads = norm_threads(WPR);
@@ -719,12 +747,23 @@ struct NormShape {
     static_assert(NV % V == 0, "whole vectors");
 };
 
-// How many of the values from column c on, of run k, lie in the row.
-template <typename S>
-__device__ inline int norm_left(int k, int c, int dim)
-{
-    return k < S::kFull ? S::V : dim - c;
-}
+// Run k of a lane: how many values from its column on lie in the row (any
+// positive number where TAIL is not kPart), its first column, and the first of
+// its values that counts in sums over the row.
+template <typename S, int TAIL>
+struct NormRun {
+    int left, c, own;
+    __device__ NormRun(int k, int span, int lane, int dim)
+    {
+        const int at = (k * span + lane) * S::V;
+        const bool full = k < S::kFull;
+        left = full ? S::V : dim - at;
+        c = TAIL == kBack && !full ? min(at, dim - S::V) : at;
+        own = at - c;
+    }
+    // value i counts
+    __device__ bool counts(int i) const { return TAIL == kPart ? i < left : left > 0 && (TAIL == kEven || i >= own); }
+};
 
 // The row of a lane's span: the same for the whole wave unless several rows
 // share one (8 values a lane), and known to be, so that it stays in scalar
@@ -771,18 +810,18 @@ __device__ inline void row_sums(float (&x)[N], int log_group, float* tmp, int& t
 }
 
 // V values of a parameter from column c on; `other` where there is none.
-template <int V, bool EVEN>
+template <int V, bool WHOLE>
 __device__ inline void load_param(float (&r)[V], const void* p, int type, int64_t c, int64_t left, float other)
 {
     if (!p || left <= 0) {
 #pragma unroll
         for (int k = 0; k < V; ++k) r[k] = other;
     } else if (type == 0) {
-        load_vals<V, EVEN>(r, (const float*)p + c, left);
+        load_vals<V, WHOLE>(r, (const float*)p + c, left);
     } else if (type == 1) {
-        load_vals<V, EVEN>(r, (const __bf16*)p + c, left);
+        load_vals<V, WHOLE>(r, (const __bf16*)p + c, left);
     } else {
-        load_vals<V, EVEN>(r, (const _Float16*)p + c, left);
+        load_vals<V, WHOLE>(r, (const _Float16*)p + c, left);
     }
 }
 
@@ -792,7 +831,7 @@ __device__ inline void load_param(float (&r)[V], const void* p, int type, int64_
 // row.  A wave takes a row of up to 2,048 values: its sums need no barrier.
 // 32,768 rows of 1,792 bf16 values: 44 us, 5.3 TB/s (a large copy: 4.9); a
 // block a row that read the row three times took 235 us.
-template <typename T, int NV, int WPR, bool EVEN>
+template <typename T, int NV, int WPR, int TAIL>
 __global__ __launch_bounds__(norm_threads(WPR)) void k_norm(
     const T* __restrict__ x, int64_t x_stride, int64_t rows, int dim, const void* __restrict__ weight,
     const void* __restrict__ bias, int wtype, float eps, T* __restrict__ y, int64_t y_stride, float* __restrict__ mean,
@@ -800,6 +839,7 @@ __global__ __launch_bounds__(norm_threads(WPR)) void k_norm(
 {
     using S = NormShape<T, NV, WPR>;
     constexpr int V = S::V, K = S::K;
+    constexpr bool WHOLE = TAIL != kPart;
     __shared__ float tmp[2 * WPR];
     int turn = 0;
     if (NV > 8) log_group = 6;   // known to the compiler: the columns are fixed offsets then
@@ -808,40 +848,44 @@ __global__ __launch_bounds__(norm_threads(WPR)) void k_norm(
     float w[K][V], b[K][V];
 #pragma unroll
     for (int k = 0; k < K; ++k) {
-        const int c = (k * span + lane) * V;
-        load_param<V, EVEN>(w[k], weight, wtype, c, dim - c, 1.0f);
-        load_param<V, EVEN>(b[k], bias, wtype, c, dim - c, 0.0f);
+        const NormRun<S, TAIL> run(k, span, lane, dim);
+        load_param<V, WHOLE>(w[k], weight, wtype, run.c, run.left, 1.0f);
+        load_param<V, WHOLE>(b[k], bias, wtype, run.c, run.left, 0.0f);
     }
     for (int64_t r = norm_row<NV>((int64_t)blockIdx.x * per, threadIdx.x / span); r < rows; r += (int64_t)gridDim.x * per) {
         const T* p = x + r * x_stride;
         float v[K][V], s[1] = {0.0f};
 #pragma unroll
         for (int k = 0; k < K; ++k) {
-            const int c = (k * span + lane) * V;
-            load_vals<V, EVEN>(v[k], p + c, norm_left<S>(k, c, dim));
+            const NormRun<S, TAIL> run(k, span, lane, dim);
+            load_vals<V, WHOLE>(v[k], p + run.c, run.left);
         }
 #pragma unroll
-        for (int k = 0; k < K; ++k)
+        for (int k = 0; k < K; ++k) {
+            const NormRun<S, TAIL> run(k, span, lane, dim);
 #pragma unroll
-            for (int i = 0; i < V; ++i) s[0] += v[k][i];
+            for (int i = 0; i < V; ++i) s[0] += TAIL != kBack || k < S::kFull || run.counts(i) ? v[k][i] : 0.0f;
+        }
         row_sums<1, WPR>(s, log_group, tmp, turn);
         const float m = s[0] / (float)dim;
         s[0] = 0.0f;
 #pragma unroll
-        for (int k = 0; k < K; ++k)
+        for (int k = 0; k < K; ++k) {
+            const NormRun<S, TAIL> run(k, span, lane, dim);
 #pragma unroll
             for (int i = 0; i < V; ++i) {
                 v[k][i] -= m;
-                if (k < S::kFull || (k * span + lane) * V + (EVEN ? 0 : i) < dim) s[0] = fmaf(v[k][i], v[k][i], s[0]);
+                if (k < S::kFull || run.counts(i)) s[0] = fmaf(v[k][i], v[k][i], s[0]);
             }
+        }
         row_sums<1, WPR>(s, log_group, tmp, turn);
         const float q = 1.0f / sqrtf(s[0] / (float)dim + eps);
 #pragma unroll
         for (int k = 0; k < K; ++k) {
-            const int c = (k * span + lane) * V;
+            const NormRun<S, TAIL> run(k, span, lane, dim);
 #pragma unroll
             for (int i = 0; i < V; ++i) v[k][i] = fmaf(v[k][i] * q, w[k][i], b[k][i]);
-            store_vals<V, EVEN>(v[k], y + r * y_stride + c, norm_left<S>(k, c, dim), stream);
+            store_vals<V, WHOLE>(v[k], y + r * y_stride + run.c, run.left, stream);
         }
         if (lane == 0) {
             mean[r] = m;
@@ -858,7 +902,7 @@ __global__ __launch_bounds__(norm_threads(WPR)) void k_norm(
 // TB/s, and 5 us for k_norm_join.  On the way: 298 us as passes of their own
 // for dx and for the sums, 120 in one pass, 94 with the next row ahead but both
 // forms of a row in registers, 78 with one form and two waves on a SIMD.
-template <typename T, int NV, int WPR, bool EVEN>
+template <typename T, int NV, int WPR, int TAIL>
 __global__ __launch_bounds__(norm_grad_threads(NV, WPR)) void k_norm_grad(
     const T* __restrict__ grad, int64_t grad_stride, const T* __restrict__ x, int64_t x_stride, int64_t rows, int dim,
     const float* __restrict__ mean, const float* __restrict__ rstd, const void* __restrict__ weight, int wtype,
@@ -868,7 +912,7 @@ __global__ __launch_bounds__(norm_grad_threads(NV, WPR)) void k_norm_grad(
     constexpr int V = S::V, K = S::K, THREADS = norm_grad_threads(NV, WPR), WAVES = THREADS / 64;
     // with 32 values a lane the weights are in LDS: a third wave on a SIMD is
     // worth more than their registers
-    constexpr bool FAR = NV == 32;
+    constexpr bool FAR = NV == 32, WHOLE = TAIL != kPart;
     __shared__ float tmp[2 * 2 * WPR];
     __shared__ float sums[WPR > 1 ? 1 : WAVES / 2][WPR > 1 ? 1 : 64 * NV];
     __shared__ __align__(16) float far[FAR ? 64 * WPR * NV : 1];
@@ -879,11 +923,11 @@ __global__ __launch_bounds__(norm_grad_threads(NV, WPR)) void k_norm_grad(
     float w[K][V], dw[K][V], db[K][V];
 #pragma unroll
     for (int k = 0; k < K; ++k) {
-        const int c = (k * span + lane) * V;
-        if (!FAR || (int)threadIdx.x < span) load_param<V, EVEN>(w[k], weight, wtype, c, dim - c, 1.0f);
+        const NormRun<S, TAIL> run(k, span, lane, dim);
+        if (!FAR || (int)threadIdx.x < span) load_param<V, WHOLE>(w[k], weight, wtype, run.c, run.left, 1.0f);
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-            if (FAR && (int)threadIdx.x < span) far[c + i] = w[k][i];
+            if (FAR && (int)threadIdx.x < span) far[(k * span + lane) * V + i] = w[k][i];
             dw[k][i] = db[k][i] = 0.0f;
         }
     }
@@ -904,10 +948,9 @@ __global__ __launch_bounds__(norm_grad_threads(NV, WPR)) void k_norm_grad(
     auto fetch = [&](int64_t r) {
 #pragma unroll
         for (int k = 0; k < K; ++k) {
-            const int c = (k * span + lane) * V;
-            const int left = norm_left<S>(k, c, dim);
-            next_g[k] = load_raw<V, EVEN>(grad + r * grad_stride + c, left);
-            next_x[k] = load_raw<V, EVEN>(x + r * x_stride + c, left);
+            const NormRun<S, TAIL> run(k, span, lane, dim);
+            next_g[k] = load_raw<V, WHOLE>(grad + r * grad_stride + run.c, run.left);
+            next_x[k] = load_raw<V, WHOLE>(x + r * x_stride + run.c, run.left);
         }
         next_m = mean[r];
         next_q = rstd[r];
@@ -928,14 +971,15 @@ __global__ __launch_bounds__(norm_grad_threads(NV, WPR)) void k_norm_grad(
         float s[2] = {0.0f, 0.0f};
 #pragma unroll
         for (int k = 0; k < K; ++k) {
+            const NormRun<S, TAIL> run(k, span, lane, dim);
             float wk[V];
             weights(wk, k);
 #pragma unroll
             for (int i = 0; i < V; ++i) {
                 float h = ((float)p[k][i] - m) * q;
                 // past the row's end g is 0, and h too: not a mean or rstd that may be infinite
-                if (k >= S::kFull && (k * span + lane) * V + (EVEN ? 0 : i) >= dim) h = 0.0f;
-                const float u = (float)g[k][i], v = u * wk[i];
+                if (k >= S::kFull && !(TAIL == kBack ? run.left > 0 : run.counts(i))) h = 0.0f;
+                const float u = (float)g[k][i], v = TAIL != kBack || k < S::kFull || i >= run.own ? u * wk[i] : 0.0f;
                 dw[k][i] = fmaf(u, h, dw[k][i]);
                 db[k][i] += u;
                 s[0] += v;
@@ -957,12 +1001,12 @@ __global__ __launch_bounds__(norm_grad_threads(NV, WPR)) void k_norm_grad(
         }
 #pragma unroll
         for (int k = 0; k < K; ++k) {
-            const int c = (k * span + lane) * V;
+            const NormRun<S, TAIL> run(k, span, lane, dim);
             float v[V];
             weights(v, k);
 #pragma unroll
             for (int i = 0; i < V; ++i) v[i] = q * fmaf(((float)p[k][i] - m) * q, -b, (float)g[k][i] * v[i] - a);
-            store_vals<V, EVEN>(v, dx + r * dx_stride + c, norm_left<S>(k, c, dim), stream);
+            store_vals<V, WHOLE>(v, dx + r * dx_stride + run.c, run.left, stream);
         }
     }
     if (!part) return;
@@ -1001,9 +1045,9 @@ __global__ __launch_bounds__(norm_grad_threads(NV, WPR)) void k_norm_grad(
     float* to = part + (int64_t)blockIdx.x * 2 * dim;
 #pragma unroll
     for (int k = 0; k < K; ++k) {
-        const int c = (k * span + lane) * V;
-        store_vals<V, EVEN>(dw[k], to + c, dim - c);
-        store_vals<V, EVEN>(db[k], to + dim + c, dim - c);
+        const NormRun<S, TAIL> run(k, span, lane, dim);
+        store_vals<V, WHOLE>(dw[k], to + run.c, run.left);
+        store_vals<V, WHOLE>(db[k], to + dim + run.c, run.left);
     }
 }
 
@@ -1115,49 +1159,48 @@ __global__ __launch_bounds__(256) void k_norm_join(const float* __restrict__ par
 // Rows sorted by expert, and back
 // ---------------------------------------------------------------------------
 
-// Rows to their slots' places; a group of lanes takes one row.  It also
-// zeroes the places of its number range that lie past the last routed slot.
-// Bound by bytes: 32,768 rows of 1,024 bf16 values, four places each, in 65 us,
-// 5.2 TB/s.
+// Rows to their slots' places, a vector a thread.  It also zeroes the places of
+// its number range that lie past the last routed slot.  Bound by bytes: 32,768
+// rows of 1,024 bf16 values, four places each, in 65 us, 5.2 TB/s.
 template <typename T>
 __global__ __launch_bounds__(256) void k_route_gather(const T* __restrict__ x, int64_t x_stride, int64_t rows, int top,
-                                                      int64_t dim, const int32_t* __restrict__ position,
+                                                      int dim, const int32_t* __restrict__ position,
                                                       const int32_t* __restrict__ routed, T* __restrict__ out,
-                                                      int64_t out_stride, int log_group, bool stream)
+                                                      int64_t out_stride, RowMap m, bool stream)
 {
     constexpr int V = kVals<T>;
-    const int lane = threadIdx.x & ((1 << log_group) - 1);
-    const int64_t r = (int64_t)blockIdx.x * (256 >> log_group) + (threadIdx.x >> log_group);
-    if (r >= rows) return;
-    const int64_t slots = rows * top, used = *routed;
-    for (int64_t c = (int64_t)lane * V; c < dim; c += (int64_t)V << log_group) {
-        float v[V], zero[V];
-        load_vals<V>(v, x + r * x_stride + c, dim - c);
-#pragma unroll
-        for (int k = 0; k < V; ++k) zero[k] = 0.0f;
+    const RowPlace p = row_place<V>(m, rows, dim);
+    if (!p.in) return;
+    const int64_t slots = rows * top, used = *routed, first = p.r * top;
+    auto copy = [&](auto whole) {
+        constexpr bool WHOLE = decltype(whole)::value;
+        const typename Vals<T, V>::type v = load_raw<V, WHOLE>(x + p.r * x_stride + p.c, dim);
         for (int k = 0; k < top; ++k) {
-            const int64_t at = position[r * top + k];
-            if (at >= 0 && at < slots) store_vals<V>(v, out + at * out_stride + c, dim - c, stream);
-            if (r * top + k >= used) store_vals<V>(zero, out + (r * top + k) * out_stride + c, dim - c);
+            const int64_t at = position[first + k];
+            if (at >= 0 && at < slots) store_raw<V, WHOLE>(v, out + at * out_stride + p.c, dim, stream);
+            if (first + k >= used)
+                store_raw<V, WHOLE>(typename Vals<T, V>::type{}, out + (first + k) * out_stride + p.c, dim, stream);
         }
-    }
+    };
+    if (dim >= V) copy(std::true_type());
+    else copy(std::false_type());
 }
 
 // out[r] = sum over k of weight[r][k] * y[position[r][k]], in the order of k,
-// four rows of y in flight.  Bound by bytes: 32,768 rows of 1,024 bf16 values,
-// four each, in 61 us, 5.5 TB/s.
+// a vector a thread, four rows of y in flight.  Bound by bytes: 32,768 rows of
+// 1,024 bf16 values, four each, in 61 us, 5.5 TB/s.
 template <typename T>
 __global__ __launch_bounds__(256) void k_route_combine(const T* __restrict__ y, int64_t y_stride, int64_t rows, int top,
-                                                       int64_t dim, const int32_t* __restrict__ position,
+                                                       int dim, const int32_t* __restrict__ position,
                                                        const float* __restrict__ weight, T* __restrict__ out,
-                                                       int64_t out_stride, int log_group, bool stream)
+                                                       int64_t out_stride, RowMap m, bool stream)
 {
     constexpr int V = kVals<T>, STEP = 4;
-    const int lane = threadIdx.x & ((1 << log_group) - 1);
-    const int64_t r = (int64_t)blockIdx.x * (256 >> log_group) + (threadIdx.x >> log_group);
-    if (r >= rows) return;
-    const int64_t slots = rows * top;
-    for (int64_t c = (int64_t)lane * V; c < dim; c += (int64_t)V << log_group) {
+    const RowPlace p = row_place<V>(m, rows, dim);
+    if (!p.in) return;
+    const int64_t slots = rows * top, first = p.r * top;
+    auto sum = [&](auto whole) {
+        constexpr bool WHOLE = decltype(whole)::value;
         float acc[V];
 #pragma unroll
         for (int k = 0; k < V; ++k) acc[k] = 0.0f;
@@ -1166,66 +1209,85 @@ __global__ __launch_bounds__(256) void k_route_combine(const T* __restrict__ y, 
             float w[STEP];
 #pragma unroll
             for (int u = 0; u < STEP; ++u) {
-                const int64_t at = k + u < top ? position[r * top + k + u] : -1;
+                const int64_t at = k + u < top ? position[first + k + u] : -1;
                 const bool live = at >= 0 && at < slots;
-                w[u] = live && weight ? weight[r * top + k + u] : live;
-                v[u] = live ? load_raw<V>(y + at * y_stride + c, dim - c) : typename Vals<T, V>::type{};
+                w[u] = live && weight ? weight[first + k + u] : live;
+                v[u] = live ? load_raw<V, WHOLE>(y + at * y_stride + p.c, dim) : typename Vals<T, V>::type{};
             }
 #pragma unroll
             for (int u = 0; u < STEP; ++u)
 #pragma unroll
                 for (int i = 0; i < V; ++i) acc[i] = fmaf(w[u], (float)v[u][i], acc[i]);
         }
-        store_vals<V>(acc, out + r * out_stride + c, dim - c, stream);
-    }
+        store_vals<V, WHOLE>(acc, out + p.r * out_stride + p.c, dim, stream);
+    };
+    if (dim >= V) sum(std::true_type());
+    else sum(std::false_type());
 }
 
 // dy[position[r][k]] = weight[r][k] * grad[r]; dweight[r][k] = <grad[r], y[position[r][k]]>.
-// A wave takes one row; places past the last routed slot are zeroed as in
-// k_route_gather.  Bound by bytes: 32,768 rows of 1,024 bf16 values, four slots
-// each, in 116 us, 5.2 TB/s.
-template <typename T>
+// A wave takes a slot, or several where a row has few vectors (WAVE false), four
+// vectors of each row in flight; a row's slots are neighbours, so that its
+// gradient comes from the cache after the first.  Places past the last routed
+// slot are zeroed as in k_route_gather.  Bound by bytes: 32,768 rows of 1,024
+// bf16 values, four slots each, in 106 us, 5.7 TB/s (a wave a row: 116, and 3
+// times as long for 186 rows of 3,304 values).
+template <typename T, bool WAVE>
 __global__ __launch_bounds__(256) void k_route_combine_grad(const T* __restrict__ grad, int64_t grad_stride,
                                                             const T* __restrict__ y, int64_t y_stride, int64_t rows,
-                                                            int top, int64_t dim, const int32_t* __restrict__ position,
+                                                            int top, int dim, const int32_t* __restrict__ position,
                                                             const int32_t* __restrict__ routed,
                                                             const float* __restrict__ weight, T* __restrict__ dy,
-                                                            int64_t dy_stride, float* __restrict__ dweight, bool stream)
+                                                            int64_t dy_stride, float* __restrict__ dweight, int log_group,
+                                                            bool stream)
 {
-    constexpr int V = kVals<T>;
-    const int lane = threadIdx.x & 63;
-    const int64_t r = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
-    if (r >= rows) return;
-    const int64_t slots = rows * top, used = *routed;
-    for (int k = 0; k < top; ++k) {
-        const int64_t s = r * top + k, at = position[s];
-        const bool live = at >= 0 && at < slots;
-        const float w = weight ? weight[s] : 1.0f;
-        float dot = 0.0f;
-        if (live)
-            for (int64_t c = lane * V; c < dim; c += 64 * V) {
-                float g[V], v[V];
-                load_vals<V>(g, grad + r * grad_stride + c, dim - c);
-                if (dweight) {
-                    load_vals<V>(v, y + at * y_stride + c, dim - c);
+    constexpr int V = kVals<T>, STEP = WAVE ? 4 : 1;
+    if (WAVE) log_group = 6;
+    const int lane = threadIdx.x & ((1 << log_group) - 1), group = threadIdx.x >> log_group;
+    const uint32_t slots = (uint32_t)(rows * top);
+    const uint32_t s = blockIdx.x * (256u >> log_group) + (WAVE ? __builtin_amdgcn_readfirstlane(group) : group);
+    if (s >= slots) return;
+    const uint32_t r = s / (uint32_t)top, used = (uint32_t)*routed, at = (uint32_t)position[s];
+    const bool live = at < slots;   // -1 is not
+    const float w = weight ? weight[s] : 1.0f;
+    const T* g_row = grad + (int64_t)r * grad_stride;
+    const T* y_row = y + (live ? (int64_t)at : 0) * y_stride;
+    T* to = dy + (live ? (int64_t)at : 0) * dy_stride;
+    T* zero = dy + (int64_t)s * dy_stride;
+    typedef typename Vals<T, V>::type Vec;
+    float dot = 0.0f;
+    auto slot = [&](auto whole) {
+        constexpr bool WHOLE = decltype(whole)::value;
+        for (int first = lane * V; first < dim; first += (STEP * V) << log_group) {
+            Vec g[STEP], v[STEP];
+            int c[STEP];
 #pragma unroll
-                    for (int u = 0; u < V; ++u) dot = fmaf(g[u], v[u], dot);
+            for (int u = 0; u < STEP; ++u) {
+                const int from = first + ((u * V) << log_group);
+                c[u] = WHOLE ? min(from, dim - V) : from;
+                g[u] = load_raw<V, WHOLE>(g_row + c[u], live ? dim - from : 0);
+                v[u] = load_raw<V, WHOLE>(y_row + c[u], live && dweight ? dim - from : 0);
+            }
+#pragma unroll
+            for (int u = 0; u < STEP; ++u) {
+                const int from = first + ((u * V) << log_group);
+                float out[V];
+#pragma unroll
+                for (int i = 0; i < V; ++i) {
+                    // values shared with the vector before count there
+                    if (c[u] + i >= from) dot = fmaf((float)g[u][i], (float)v[u][i], dot);
+                    out[i] = (float)g[u][i] * w;
                 }
-#pragma unroll
-                for (int u = 0; u < V; ++u) g[u] *= w;
-                store_vals<V>(g, dy + at * dy_stride + c, dim - c, stream);
+                if (live) store_vals<V, WHOLE>(out, to + c[u], dim - from, stream);
+                if (s >= used) store_raw<V, WHOLE>(Vec{}, zero + c[u], dim - from, stream);
             }
-        if (dweight) {
-            dot = wave_sum(dot);
-            if (lane == 0) dweight[s] = dot;
         }
-        if (s >= used)
-            for (int64_t c = lane * V; c < dim; c += 64 * V) {
-                float zero[V];
-#pragma unroll
-                for (int u = 0; u < V; ++u) zero[u] = 0.0f;
-                store_vals<V>(zero, dy + s * dy_stride + c, dim - c);
-            }
+    };
+    if (dim >= V) slot(std::true_type());
+    else slot(std::false_type());
+    if (dweight) {
+        dot = group_sum(dot, log_group);
+        if (lane == 0) dweight[s] = dot;
     }
 }
 

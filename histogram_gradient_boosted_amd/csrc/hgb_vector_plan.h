@@ -90,9 +90,31 @@ constexpr int scatter_pair_words(int items) { return items > 1 ? 2 * items * kSo
 // the launch and the kernel lay the rest out behind them.
 constexpr int small_pair_words(const SortPlan& p, int items, int threads) { return p.passes > 1 ? 2 * items * threads : 0; }
 
-// Lanes that share a row of `dim` values, V values a lane: a power of two up
-// to a wave; wider rows are cut into slices of 64 * V columns or walked in steps.
-inline int vec_group(int64_t dim, int V) { return std::min(64, vec_pow2(vec_ceil(dim, V))); }
+// One vector of V values a thread, for rows of `dim`: 256 threads take `per`
+// whole rows where a row has at most 256 vectors, else one of its `slices`
+// (the idle threads are fewer than with groups of 2^k lanes: at most a third,
+// and a tenth for rows of up to 25 vectors, against a half).
+struct RowMap {
+    int vecs = 1;
+    int per = 1;
+    int slices = 1;
+    int magic = 0;   // thread / vecs = thread * magic >> 16
+};
+
+inline RowMap plan_rows(int64_t dim, int V)
+{
+    RowMap m;
+    m.vecs = (int)vec_ceil(dim, V);
+    if (m.vecs <= 256) {
+        m.per = 256 / m.vecs;
+        m.magic = 65536 / m.vecs + 1;
+    } else {
+        m.slices = (int)vec_ceil(m.vecs, 256);
+    }
+    return m;
+}
+
+inline int64_t row_blocks(const RowMap& m, int64_t rows) { return m.slices > 1 ? rows * m.slices : vec_ceil(rows, m.per); }
 
 // The embedding's gradient: the sort, then chunks of sorted positions.
 // Workspace: counts | pairs A | pairs B | partial sums (two rows a chunk).
@@ -106,7 +128,7 @@ struct EmbedPlan {
 
 constexpr int kEmbedChunk = 256;         // largest chunk
 constexpr int kEmbedFew = 32;
-constexpr int64_t kEmbedWaves = 2048;    // chunks are halved until this many waves run (8 a CU)
+constexpr int64_t kEmbedWaves = 2048;    // chunks are halved until this many waves run (8 a CU), below 32 a quarter
 
 inline EmbedPlan plan_embed(int64_t n, int64_t vocab, int64_t dim)
 {
@@ -114,10 +136,16 @@ inline EmbedPlan plan_embed(int64_t n, int64_t vocab, int64_t dim)
     p.sort = plan_sort(n, vocab, false);
     // The narrowest lanes' values (4) decide, so that the plan and the
     // workspace do not depend on the types.
-    const int64_t group = vec_group(dim, 4), slices = vec_ceil(dim, 64 * 4);
+    const int64_t vecs = vec_ceil(dim, 4);
     // a handful of tokens is one chunk: nothing to join
     p.chunk = n <= kEmbedFew ? kEmbedFew : kEmbedChunk;
-    while (n > kEmbedFew && p.chunk > 8 && vec_ceil(n, p.chunk) * group * slices / 64 < kEmbedWaves) p.chunk /= 2;
+    auto fewer = [&](int least, int64_t waves) {
+        while (p.chunk > least && vec_ceil(n, p.chunk) * vecs / 64 < waves) p.chunk /= 2;
+    };
+    if (n > kEmbedFew) {
+        fewer(32, kEmbedWaves);
+        fewer(8, kEmbedWaves / 4);
+    }
     p.chunks = vec_ceil(n, p.chunk);
     p.part_stride = vec_up(dim, 4);
     p.off_a = p.sort.count ? vec_up((int64_t)p.sort.blocks * p.sort.row * 4, 256) : 0;

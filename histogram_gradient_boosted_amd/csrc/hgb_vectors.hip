@@ -110,21 +110,24 @@ hgb_status by_pair(int32_t table, int32_t vec, F&& f)
     return by_type(vec, [&](auto* v) { return f(v, v); });
 }
 
-// f with the plan's values a lane and waves a row, and whether the rows are
-// `even`, as types.
+// f with the plan's values a lane and waves a row, and how the rows end in
+// vectors of V, as types.
 template <typename F>
-void by_shape(const NormPlan& p, bool even, F&& f)
+void by_shape(const NormPlan& p, int64_t dim, int V, F&& f)
 {
     auto shaped = [&](auto values, auto waves) {
-        if (even) f(values, waves, std::true_type());
-        else f(values, waves, std::false_type());
+        if (dim % V == 0) f(values, waves, std::integral_constant<int, kEven>());
+        else f(values, waves, std::integral_constant<int, kBack>());
     };
     auto with = [&](auto values) {
         if (p.waves == 4) shaped(values, std::integral_constant<int, 4>());
         else shaped(values, std::integral_constant<int, 1>());
     };
+    const std::integral_constant<int, 8> eight;
+    const std::integral_constant<int, 1> one;
     if (p.waves == 16) shaped(std::integral_constant<int, 16>(), std::integral_constant<int, 16>());
-    else if (p.values == 8) shaped(std::integral_constant<int, 8>(), std::integral_constant<int, 1>());
+    else if (p.values == 8 && dim < V) f(eight, one, std::integral_constant<int, kPart>());
+    else if (p.values == 8) shaped(eight, one);
     else if (p.values == 16) with(std::integral_constant<int, 16>());
     else with(std::integral_constant<int, 32>());
 }
@@ -137,9 +140,10 @@ void by_shape(const NormPlan& p, bool even, F&& f)
 // of 1,835,008 tokens 129 and 173 together; of 917,504 tokens (a call of 118
 // MB) 71 and 64 together, so not below; route_gather and route_combine of
 // 32,768 rows of 1,024, four experts each, 136 and 158.
-bool streams(int64_t bytes, const void* out, int32_t type, int64_t stride)
+bool streams(int64_t bytes, const void* out, int32_t type, int64_t dim, int64_t stride)
 {
-    return bytes >= (int64_t)192 << 20 && (uintptr_t)out % 16 == 0 && stride * elem_size(type) % 16 == 0;
+    const int e = elem_size(type);
+    return bytes >= (int64_t)192 << 20 && (uintptr_t)out % 16 == 0 && stride * e % 16 == 0 && dim * e % 16 == 0;
 }
 
 int log2_of(int p) { return 31 - __builtin_clz((unsigned)p); }
@@ -257,12 +261,11 @@ hgb_status hgb_embed(hgb_ctx* c, const void* table, int32_t table_type, int64_t 
         return by_pair(table_type, out_type, [&](auto* t, auto* u) -> hgb_status {
             using T = std::remove_pointer_t<decltype(t)>;
             using U = std::remove_pointer_t<decltype(u)>;
-            const int lg = log2_of(vec_group(dim, kVals<T, U>));
-            const int64_t groups = 256 >> lg;
+            const RowMap m = plan_rows(dim, kVals<T, U>);
             const int64_t bytes = dim * (n_tokens * (int64_t)sizeof(U) + std::min(n_tokens, vocab) * (int64_t)sizeof(T));
-            k_embed<T, U><<<(unsigned)vec_ceil(n_tokens, groups), 256, 0, c->stream>>>(
-                (const T*)table, table_stride, (int)vocab, (int)dim, tokens, (int)n_tokens, pad, scale, (U*)out, out_stride, lg,
-                streams(bytes, out, out_type, out_stride), c->dev_words + kWordVectors);
+            k_embed<T, U><<<(unsigned)row_blocks(m, n_tokens), 256, 0, c->stream>>>(
+                (const T*)table, table_stride, (int)vocab, (int)dim, tokens, (int)n_tokens, pad, scale, (U*)out, out_stride, m,
+                streams(bytes, out, out_type, dim, out_stride), c->dev_words + kWordVectors);
             HGB_LAUNCHED(c, "k_embed");
             return HGB_OK;
         });
@@ -300,7 +303,7 @@ hgb_status hgb_embed_backward(hgb_ctx* c, const void* grad, int32_t grad_type, i
         z.cols = dim;
         z.stride = out_stride;
         z.elem = elem_size(out_type);
-        z.stream = streams(dim * (n_tokens * elem_size(grad_type) + vocab * z.elem), out, out_type, out_stride);
+        z.stream = streams(dim * (n_tokens * elem_size(grad_type) + vocab * z.elem), out, out_type, dim, out_stride);
         if (n_tokens == 0) {
             k_zero_rows<<<(unsigned)std::min<int64_t>(vec_ceil(vocab * dim * z.elem, 4096 * 4), 8 * c->n_cu), 256, 0,
                           c->stream>>>(z);
@@ -315,16 +318,16 @@ hgb_status hgb_embed_backward(hgb_ctx* c, const void* grad, int32_t grad_type, i
             using U = std::remove_pointer_t<decltype(u)>;
             using T = std::remove_pointer_t<decltype(t)>;
             float* part = (float*)(ws + p.off_part);
-            constexpr int V = kVals<T, U>;
-            const int lg = log2_of(vec_group(dim, V));
-            const dim3 grid((unsigned)vec_ceil(p.chunks, 256 >> lg), (unsigned)vec_ceil(dim, (int64_t)V << lg));
-            k_embed_sum<T, U><<<grid, 256, 0, c->stream>>>(pairs, n_tokens, (const T*)grad, grad_stride, dim, vocab, scale,
-                                                           (U*)out, out_stride, part, p.part_stride, p.chunk, lg);
+            const RowMap m = plan_rows(dim, kVals<T, U>);
+            k_embed_sum<T, U><<<(unsigned)row_blocks(m, p.chunks), 256, 0, c->stream>>>(
+                pairs, n_tokens, (const T*)grad, grad_stride, dim, vocab, scale, (U*)out, out_stride, part, p.part_stride, p.chunk,
+                p.chunks, m);
             HGB_LAUNCHED(c, "k_embed_sum");
             if (p.chunks > 1) {
                 const dim3 jgrid((unsigned)vec_ceil(p.chunks, kJoinChunks), (unsigned)vec_ceil(dim, 64));
-                k_embed_join<U><<<jgrid, 256, 0, c->stream>>>(pairs, n_tokens, dim, vocab, scale, (U*)out, out_stride, part,
-                                                              p.part_stride, p.chunk, p.chunks);
+                k_embed_join<U><<<jgrid, kJoinThreads, 0, c->stream>>>(pairs, n_tokens, dim, vocab, scale, (U*)out, out_stride, part,
+                                                                       p.part_stride, p.chunk, p.chunks,
+                                                                       log2_of(std::min(16, vec_pow2(vec_ceil(dim, 4)))));
                 HGB_LAUNCHED(c, "k_embed_join");
             }
             return HGB_OK;
@@ -357,12 +360,13 @@ hgb_status hgb_layer_norm(hgb_ctx* c, const void* x, int32_t type, int64_t x_str
                 k_norm_wide<T><<<(unsigned)std::min<int64_t>(n_rows, 65536), 256, 0, c->stream>>>(
                     (const T*)x, x_stride, n_rows, dim, weight, bias, param_type, eps, (T*)y, y_stride, mean, rstd);
             } else {
-                by_shape(p, dim % kVals<T> == 0, [&](auto values, auto waves, auto even) {
+                by_shape(p, dim, kVals<T>, [&](auto values, auto waves, auto tail) {
                     constexpr int NV = decltype(values)::value, WPR = decltype(waves)::value, THREADS = norm_threads(WPR);
                     const unsigned blocks =
                         (unsigned)std::min<int64_t>(vec_ceil(n_rows, p.per_block), (int64_t)c->n_cu * 2048 / THREADS);
-                    k_norm<T, NV, WPR, decltype(even)::value><<<blocks, THREADS, 0, c->stream>>>((const T*)x, x_stride, n_rows, (int)dim, weight, bias,
-                                                                          param_type, eps, (T*)y, y_stride, mean, rstd, p.log_group, streams(2 * n_rows * dim * elem_size(type), y, type, y_stride));
+                    k_norm<T, NV, WPR, decltype(tail)::value><<<blocks, THREADS, 0, c->stream>>>(
+                        (const T*)x, x_stride, n_rows, (int)dim, weight, bias, param_type, eps, (T*)y, y_stride, mean, rstd,
+                        p.log_group, streams(2 * n_rows * dim * elem_size(type), y, type, dim, y_stride));
                 });
             }
             HGB_LAUNCHED(c, "k_norm");
@@ -417,11 +421,12 @@ hgb_status hgb_layer_norm_backward(hgb_ctx* c, const void* grad, int64_t grad_st
                     HGB_LAUNCHED(c, "k_norm_wide_params");
                 }
             } else if (n_rows > 0 || params) {
-                by_shape(p, dim % kVals<T> == 0, [&](auto values, auto waves, auto even) {
+                by_shape(p, dim, kVals<T>, [&](auto values, auto waves, auto tail) {
                     constexpr int NV = decltype(values)::value, WPR = decltype(waves)::value;
-                    k_norm_grad<T, NV, WPR, decltype(even)::value><<<(unsigned)parts, norm_grad_threads(NV, WPR), 0, c->stream>>>(
+                    k_norm_grad<T, NV, WPR, decltype(tail)::value><<<(unsigned)parts, norm_grad_threads(NV, WPR), 0, c->stream>>>(
                         g, grad_stride, (const T*)x, x_stride, n_rows, (int)dim, mean, rstd, weight, param_type, (T*)dx,
-                        dx_stride, params ? (float*)workspace : nullptr, p.log_group, streams(3 * n_rows * dim * elem_size(type), dx, type, dx_stride));
+                        dx_stride, params ? (float*)workspace : nullptr, p.log_group,
+                        streams(3 * n_rows * dim * elem_size(type), dx, type, dim, dx_stride));
                 });
                 HGB_LAUNCHED(c, "k_norm_grad");
             }
@@ -498,9 +503,10 @@ hgb_status hgb_route_gather(hgb_ctx* c, const void* x, int32_t type, int64_t x_s
         ProfScope ps(c, HGB_KERNEL_ROUTE);
         return by_type(type, [&](auto* t) -> hgb_status {
             using T = std::remove_pointer_t<decltype(t)>;
-            const int lg = log2_of(vec_group(dim, kVals<T>));
-            k_route_gather<T><<<(unsigned)vec_ceil(n_rows, 256 >> lg), 256, 0, c->stream>>>(
-                (const T*)x, x_stride, n_rows, top, dim, position, offsets + n_experts, (T*)out, out_stride, lg, streams(n_rows * (top + 1) * dim * elem_size(type), out, type, out_stride));
+            const RowMap m = plan_rows(dim, kVals<T>);
+            k_route_gather<T><<<(unsigned)row_blocks(m, n_rows), 256, 0, c->stream>>>(
+                (const T*)x, x_stride, n_rows, top, (int)dim, position, offsets + n_experts, (T*)out, out_stride, m,
+                streams(n_rows * (top + 1) * dim * elem_size(type), out, type, dim, out_stride));
             HGB_LAUNCHED(c, "k_route_gather");
             return HGB_OK;
         });
@@ -521,9 +527,10 @@ static hgb_status combine(hgb_ctx* c, const char* verb, const void* y, int32_t t
     ProfScope ps(c, HGB_KERNEL_ROUTE);
     return by_type(type, [&](auto* t) -> hgb_status {
         using T = std::remove_pointer_t<decltype(t)>;
-        const int lg = log2_of(vec_group(dim, kVals<T>));
-        k_route_combine<T><<<(unsigned)vec_ceil(n_rows, 256 >> lg), 256, 0, c->stream>>>(
-            (const T*)y, y_stride, n_rows, top, dim, position, weight, (T*)out, out_stride, lg, streams(n_rows * (top + 1) * dim * elem_size(type), out, type, out_stride));
+        const RowMap m = plan_rows(dim, kVals<T>);
+        k_route_combine<T><<<(unsigned)row_blocks(m, n_rows), 256, 0, c->stream>>>(
+            (const T*)y, y_stride, n_rows, top, (int)dim, position, weight, (T*)out, out_stride, m,
+            streams(n_rows * (top + 1) * dim * elem_size(type), out, type, dim, out_stride));
         HGB_LAUNCHED(c, "k_route_combine");
         return HGB_OK;
     });
@@ -567,9 +574,13 @@ hgb_status hgb_route_combine_backward(hgb_ctx* c, const void* grad, int32_t type
         ProfScope ps(c, HGB_KERNEL_ROUTE);
         return by_type(type, [&](auto* t) -> hgb_status {
             using T = std::remove_pointer_t<decltype(t)>;
-            k_route_combine_grad<T><<<(unsigned)vec_ceil(n_rows, 4), 256, 0, c->stream>>>(
-                (const T*)grad, grad_stride, (const T*)y, y_stride, n_rows, top, dim, position, offsets + n_experts, weight,
-                (T*)dy, dy_stride, dweight, streams(n_rows * ((dweight ? 2 : 1) * top + 1) * dim * elem_size(type), dy, type, dy_stride));
+            const int64_t vecs = vec_ceil(dim, kVals<T>), slots = n_rows * top;
+            const int lg = log2_of(vec_pow2(std::min<int64_t>(vecs, 64)));
+            const bool stream = streams(n_rows * ((dweight ? 2 : 1) * top + 1) * dim * elem_size(type), dy, type, dim, dy_stride);
+            auto* kernel = lg == 6 ? k_route_combine_grad<T, true> : k_route_combine_grad<T, false>;
+            kernel<<<(unsigned)vec_ceil(slots, 256 >> lg), 256, 0, c->stream>>>(
+                (const T*)grad, grad_stride, (const T*)y, y_stride, n_rows, top, (int)dim, position, offsets + n_experts, weight,
+                (T*)dy, dy_stride, dweight, lg, stream);
             HGB_LAUNCHED(c, "k_route_combine_grad");
             return HGB_OK;
         });

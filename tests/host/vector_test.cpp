@@ -81,9 +81,16 @@ static void plans()
         }
     }
     for (int V : {4, 8})
-        for (int64_t dim = 1; dim < 700; ++dim) {
-            const int g = vec_group(dim, V);
-            CHECK(g >= 1 && g <= 64 && (g & (g - 1)) == 0 && (g == 64 || (int64_t)g * V >= dim));
+        for (int64_t dim = 1; dim < 6000; ++dim) {
+            const RowMap m = plan_rows(dim, V);
+            CHECK((int64_t)m.vecs * V >= dim && (int64_t)(m.vecs - 1) * V < dim);
+            if (m.slices > 1) {
+                CHECK(m.slices * 256 >= m.vecs && (m.slices - 1) * 256 < m.vecs);
+                CHECK(row_blocks(m, 1000) == 1000 * m.slices);
+                continue;
+            }
+            CHECK(m.per >= 1 && m.per * m.vecs <= 256 && row_blocks(m, 1000) * m.per >= 1000);
+            for (int t = 0; t < 256; ++t) CHECK((t * m.magic) >> 16 == t / m.vecs);
         }
 }
 
