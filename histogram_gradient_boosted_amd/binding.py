@@ -130,25 +130,28 @@ def load():
     lib.hgb_profile_query.argtypes = [vp, c_int, ctypes.POINTER(ctypes.c_double),
                                       ctypes.POINTER(ctypes.c_int64)]
     lib.hgb_profile_query.restype = c_int
-    i64, f32 = ctypes.c_int64, ctypes.c_float
-    lib.hgb_embed.argtypes = [vp, vp, i32, i64, i64, i64, vp, i64, i32, f32, vp, i32, i64]
-    lib.hgb_embed_backward.argtypes = [vp, vp, i32, i64, i64, i64, vp, i32, f32, i64, vp, i32, i64, vp, i64]
-    lib.hgb_embed_backward_workspace.argtypes = [i64, i64, i64]
-    lib.hgb_layer_norm.argtypes = [vp, vp, i32, i64, i64, i64, vp, vp, i32, f32, vp, i64, vp, vp]
-    lib.hgb_layer_norm_backward.argtypes = [vp, vp, i64, vp, i64, i32, i64, i64, vp, vp, vp, i32, vp, i64,
-                                            vp, vp, vp, i64]
-    lib.hgb_layer_norm_backward_workspace.argtypes = [i64, i64]
-    lib.hgb_route.argtypes = [vp, vp, i64, i32, i32, vp, vp, vp, vp, i64]
-    lib.hgb_route_workspace.argtypes = [i64, i32, i32]
-    lib.hgb_route_gather.argtypes = [vp, vp, i32, i64, i64, i32, i64, vp, vp, i32, vp, i64]
-    lib.hgb_route_gather_backward.argtypes = [vp, vp, i32, i64, i64, i32, i64, vp, vp, i64]
-    lib.hgb_route_combine.argtypes = [vp, vp, i32, i64, i64, i32, i64, vp, vp, vp, i64]
-    lib.hgb_route_combine_backward.argtypes = [vp, vp, i32, i64, vp, i64, i64, i32, i64, vp, vp, i32, vp, vp,
-                                               i64, vp]
-    for name in EXPORTED[-12:]:
-        getattr(lib, name).restype = i64 if name.endswith("_workspace") else c_int
     _lib = lib
     return lib
+
+
+# what a verb returns instead of a result (csrc/hgb_verbs.cpp), beside hgb_status
+_ELSEWHERE, _TOO_LARGE = -1, -2
+
+_verbs = None
+
+
+def load_verbs():
+    """The vector verbs on torch tensors: the module _verbs, built beside libhgb.so."""
+    global _verbs
+    if _verbs is None:
+        import torch  # noqa: F401  (its libraries hold what the module needs)
+        load()
+        try:
+            from . import _verbs as module
+        except ImportError as e:
+            raise RuntimeError(f"{e}; build it with __graft_entry__.build()") from e
+        _verbs = module
+    return _verbs
 
 
 def available() -> bool:
@@ -173,23 +176,22 @@ class Context:
 
     stream: a torch.cuda.Stream (default: the current stream of `device`)."""
 
+    _handle = _stream_id = 0
+
     def __init__(self, device: int = 0, stream=None):
         import torch
         self._torch = torch
         self._lib = load()
         self.device = int(device)
-        self._torch_device = torch.device("cuda", self.device)
-        self._types = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}   # hgb_dtype
         if stream is None:
             stream = torch.cuda.current_stream(self.device)
         self.stream = stream
-        self._stream_id = stream.cuda_stream
-        self._current_stream_id = torch._C._cuda_getCurrentRawStream   # of a device; no Stream object made
+        self._stream_id = stream.stream_id
         h = ctypes.c_void_p()
         st = self._lib.hgb_create(self.device, ctypes.c_void_p(stream.cuda_stream), ctypes.byref(h))
         if st != HGB_OK:
             raise HGBError(st, "hgb_create failed")
-        self._h = h
+        self._h, self._handle = h, h.value
         self.n_rows = self.n_features = self.n_bins = self.n_slots = 0
         self.has_missing = False
 
@@ -218,7 +220,7 @@ class Context:
     def close(self):
         if getattr(self, "_h", None):
             self._lib.hgb_destroy(self._h)
-            self._h = None
+            self._h = self._handle = None
 
     def __del__(self):
         try:
@@ -452,260 +454,80 @@ class Context:
                                               float(gamma), op), "find_splits")
 
     # -- the vector verbs ---------------------------------------------------
-    # Tensors must be on the context's device.  A call whose tensors were made
-    # on another stream than the context's is ordered after that (the current)
-    # stream's work, and the current stream after the call.
-    # A small call's time is the host's: what a verb makes itself is not checked
-    # again, and the checks take few calls.
-    def _here(self, t, name):
-        if not isinstance(t, self._torch.Tensor) or not t.is_cuda or t.get_device() != self.device:
-            raise ValueError(f"{name} must be a CUDA tensor on device {self.device}")
+    # Tensors must be on the context's device.  The checks, outputs and
+    # workspaces are csrc/hgb_verbs.cpp's.  A call made on another stream than
+    # the context's is ordered after that (the current) stream's work, and the
+    # current stream after the call.
+    def _verb(self, name, *args):
+        verb = getattr(_verbs or load_verbs(), name)
+        result = verb(self._handle, self.device, self._stream_id, *args)
+        return self._answer(name, verb, args, result) if result.__class__ is int else result
 
-    def _rows(self, t, name, dim=None, rows=None, dtype=None):
-        """A [..., dim] vector argument as (pointer, type code, rows, dim, row stride)."""
-        self._here(t, name)
-        kind = t.dtype
-        code = self._types.get(kind)
-        if code is None:
-            raise ValueError(f"{name} must be float32, bfloat16 or float16, got {kind}")
-        if dtype is not None and kind != dtype:
-            raise ValueError(f"{name} must be {dtype}, got {kind}")
-        shape = t.shape
-        if len(shape) == 2:
-            n, d = shape
-            stride, step = t.stride()
-            if n < 2:
-                stride = d
-            if stride < d or (step != 1 and d > 1):
-                raise ValueError(f"{name}'s rows must be contiguous and apart")
-        elif len(shape) == 0:
-            raise ValueError(f"{name} must have a last dimension")
-        else:
-            stride = d = shape[-1]
-            n = t.numel() // d if d else 0
-            if not t.is_contiguous():
-                raise ValueError(f"{name} must be contiguous, or two-dimensional with contiguous rows")
-        if d < 1:
-            raise ValueError(f"{name} has rows of no values")
-        if dim is not None and d != dim:
-            raise ValueError(f"{name} has rows of {d} values, needs {dim}")
-        if rows is not None and n != rows:
-            raise ValueError(f"{name} holds {n} rows, needs {rows}")
-        return t.data_ptr(), code, n, d, stride
-
-    def _out(self, out, shape, dtype, dim, rows):
-        """The output tensor, given or made: (tensor, pointer, type code, row stride)."""
-        if out is None:
-            code = self._types.get(dtype)
-            if code is None:
-                raise ValueError(f"dtype must be float32, bfloat16 or float16, got {dtype}")
-            out = self._torch.empty(*shape, dtype=dtype, device=self._torch_device)
-            return out, out.data_ptr(), code, dim
-        p, code, _, _, stride = self._rows(out, "out", dim, rows, dtype)
-        return out, p, code, stride
-
-    def _param(self, t, name, dim, x_dtype):
-        """A [dim] parameter (x's type or float32), or None."""
-        if t is None:
-            return None
-        self._here(t, name)
-        kind = t.dtype
-        if kind != x_dtype and kind != self._torch.float32:
-            raise ValueError(f"{name} must be float32 or {x_dtype}, got {kind}")
-        if t.shape != (dim,):
-            raise ValueError(f"{name} must have shape [{dim}]")
-        if not t.is_contiguous():
-            raise ValueError(f"{name} must be contiguous")
-        return t.data_ptr()
-
-    def _plain(self, t, name, dtype, shape=None):
-        """A contiguous tensor of one type (and shape), as its pointer."""
-        self._here(t, name)
-        if t.dtype != dtype:
-            raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
-        if not t.is_contiguous():
-            raise ValueError(f"{name} must be contiguous")
-        if shape is not None and t.shape != shape:
-            raise ValueError(f"{name} has shape {tuple(t.shape)}, needs {tuple(shape)}")
-        return t.data_ptr()
-
-    def _ints(self, t, name):
-        return self._plain(t, name, self._torch.int32)
-
-    def _vec(self, what, fn, tensors, *args):
-        """One vector verb: fn(ctx, *args), ordered between the current stream's
-        work before and after it when that is not the context's stream."""
-        if self._current_stream_id(self.device) == self._stream_id:
-            st = fn(self._h, *args)
-        else:
-            cur = self._torch.cuda.current_stream(self.device)
-            self.stream.wait_stream(cur)
-            st = fn(self._h, *args)
-            for t in tensors:
-                if t is not None:
-                    t.record_stream(self.stream)
-            cur.wait_stream(self.stream)
-        if st != HGB_OK:
-            self._check(st, what)
-
-    def _workspace(self, nbytes):
+    def _answer(self, name, verb, args, result):
+        """What a verb's number stands for: a refusal, or a call on another stream."""
         torch = self._torch
-        if nbytes < 0:
-            raise HGBError(HGB_E_UNSUPPORTED, "sizes beyond the verb's limits")
-        return torch.empty(nbytes, dtype=torch.uint8, device=self._torch_device) if nbytes else None
+        if result == _ELSEWHERE:
+            cur = torch.cuda.current_stream(self.device)
+            self.stream.wait_stream(cur)
+            with torch.cuda.stream(self.stream):   # what the verb allocates is the context's stream's
+                result = verb(self._handle, self.device, self._stream_id, *args)
+            for t in args:
+                if isinstance(t, torch.Tensor):
+                    t.record_stream(self.stream)
+            for t in result if isinstance(result, tuple) else (result,):
+                if isinstance(t, torch.Tensor):
+                    t.record_stream(cur)
+            cur.wait_stream(self.stream)
+        if result.__class__ is int:
+            if result == _TOO_LARGE:
+                raise HGBError(HGB_E_UNSUPPORTED, f"{name}: sizes beyond the verb's limits")
+            self._check(result, name)
+        return result
 
     def embed(self, table, tokens, scale: float = 1.0, pad: int = -1, dtype=None, out=None):
         """scale * table[tokens]: [*tokens.shape, dim] of `dtype` (the table's
         type, or a 16-bit one beside a float32 table).  The token `pad` gives
         zeros; so does one out of range, which the next sync() reports."""
-        tp, tt, vocab, dim, ts = self._rows(table, "table")
-        if table.dim() != 2:
-            raise ValueError("table must be two-dimensional")
-        ip = self._ints(tokens, "tokens")
-        n = tokens.numel()
-        if out is None and dtype is None:
-            dtype = table.dtype
-        out, op, ot, os_ = self._out(out, (*tokens.shape, dim), dtype, dim, n)
-        self._vec("embed", self._lib.hgb_embed, (table, tokens, out), tp, tt, ts, vocab, dim, ip, n, int(pad),
-                  float(scale), op, ot, os_)
-        return out
+        return self._verb("embed", table, tokens, scale, pad, dtype, out)
 
     def embed_backward(self, grad, tokens, vocab: int, scale: float = 1.0, pad: int = -1, dtype=None, out=None):
         """The gradient of embed's table: [vocab, dim] of `dtype` (grad's type, or
         float32 beside a 16-bit one), zeros for tokens that do not occur."""
-        gp, gt, n, dim, gs = self._rows(grad, "grad")
-        ip = self._ints(tokens, "tokens")
-        if tokens.numel() != n:
-            raise ValueError(f"grad holds {n} rows for {tokens.numel()} tokens")
-        vocab = int(vocab)
-        if out is None and dtype is None:
-            dtype = grad.dtype
-        out, op, ot, os_ = self._out(out, (max(vocab, 0), dim), dtype, dim, vocab)
-        nbytes = self._lib.hgb_embed_backward_workspace(n, vocab, dim)
-        ws = self._workspace(nbytes)
-        self._vec("embed_backward", self._lib.hgb_embed_backward, (grad, tokens, out, ws), gp, gt, gs, n, dim, ip,
-                  int(pad), float(scale), vocab, op, ot, os_, ws.data_ptr() if nbytes else None, nbytes)
-        return out
+        return self._verb("embed_backward", grad, tokens, vocab, scale, pad, dtype, out)
 
     def layer_norm(self, x, weight=None, bias=None, eps: float = 1e-5, out=None):
         """Rows of x normalised: (y, mean, rstd); y has x's shape and type, mean
         and rstd are float32 [x.shape[:-1]].  weight and bias: [dim], float32 or
         x's type (both the same), or None."""
-        torch = self._torch
-        xp, xt, n, dim, xs = self._rows(x, "x")
-        wp, bp = self._param(weight, "weight", dim, x.dtype), self._param(bias, "bias", dim, x.dtype)
-        pt = self._param_type(weight, bias)
-        shape = x.shape
-        out, yp, _, ys = self._out(out, shape, x.dtype, dim, n)
-        mean = torch.empty(shape[:-1], dtype=torch.float32, device=self._torch_device)
-        rstd = torch.empty_like(mean)
-        self._vec("layer_norm", self._lib.hgb_layer_norm, (x, weight, bias, out, mean, rstd), xp, xt, xs, n, dim, wp, bp,
-                  pt, float(eps), yp, ys, mean.data_ptr(), rstd.data_ptr())
-        return out, mean, rstd
-
-    def _param_type(self, a, b=None):
-        if a is None:
-            a = b
-        if b is not None and a.dtype != b.dtype:
-            raise ValueError("the parameters must have one type")
-        return self._types[a.dtype] if a is not None else 0
+        return self._verb("layer_norm", x, weight, bias, eps, out)
 
     def layer_norm_backward(self, grad, x, mean, rstd, weight=None, bias: bool = True, out=None):
         """Gradients of layer_norm: (dx, dweight, dbias), dweight None without a
         weight and dbias None where `bias` is false.  The parameters' gradients
         have the weight's type (float32 without one)."""
-        torch = self._torch
-        gp, gt, n, dim, gs = self._rows(grad, "grad")
-        xp, _, _, _, xs = self._rows(x, "x", dim, n, grad.dtype)
-        wp = self._param(weight, "weight", dim, x.dtype)
-        mp, rp = self._plain(mean, "mean", torch.float32), self._plain(rstd, "rstd", torch.float32)
-        if mean.numel() < n or rstd.numel() < n:
-            raise ValueError(f"mean and rstd must hold {n} values")
-        pt = self._param_type(weight)
-        out, dp, _, ds = self._out(out, x.shape, x.dtype, dim, n)
-        dw = torch.empty_like(weight) if weight is not None else None
-        db = torch.empty(dim, dtype=weight.dtype if weight is not None else torch.float32,
-                         device=self._torch_device) if bias else None
-        nbytes = self._lib.hgb_layer_norm_backward_workspace(n, dim) if dw is not None or db is not None else 0
-        ws = self._workspace(nbytes)
-        self._vec("layer_norm_backward", self._lib.hgb_layer_norm_backward,
-                  (grad, x, mean, rstd, weight, out, dw, db, ws), gp, gs, xp, xs, gt, n, dim, mp, rp, wp, pt, dp, ds,
-                  dw.data_ptr() if dw is not None else None, db.data_ptr() if db is not None else None,
-                  ws.data_ptr() if nbytes else None, nbytes)
-        return out, dw, db
+        return self._verb("layer_norm_backward", grad, x, mean, rstd, weight, bias, out)
 
     def route(self, experts, n_experts: int) -> Route:
         """Sort the slots of experts ([rows, top] int32, -1: dropped) by expert."""
-        torch = self._torch
-        if not isinstance(experts, torch.Tensor) or experts.dim() != 2:
-            raise ValueError("experts must be a two-dimensional tensor")
-        ep = self._ints(experts, "experts")
-        n, top = experts.shape
-        E = int(n_experts)
-        nbytes = self._lib.hgb_route_workspace(n, top, E)
-        ws = self._workspace(nbytes)
-        position = torch.empty_like(experts)
-        order = torch.empty(n * top, dtype=torch.int32, device=self._torch_device)
-        offsets = torch.empty(E + 1, dtype=torch.int32, device=self._torch_device)
-        self._vec("route", self._lib.hgb_route, (experts, order, position, offsets, ws), ep, n, top, E,
-                  order.data_ptr(), position.data_ptr(), offsets.data_ptr(), ws.data_ptr() if nbytes else None, nbytes)
-        return Route(order, position, offsets)
-
-    def _routed(self, route, n=None):
-        """(position pointer, offsets pointer, rows, top, experts) of a Route."""
-        position, offsets = route.position, route.offsets
-        pp, op = self._ints(position, "route.position"), self._ints(offsets, "route.offsets")
-        shape, ends = position.shape, offsets.shape
-        if len(shape) != 2 or len(ends) != 1 or ends[0] < 2:
-            raise ValueError("route is not what Context.route returns")
-        rows, top = shape
-        if n is not None and n != rows:
-            raise ValueError(f"{n} rows for a route of {rows}")
-        return pp, op, rows, top, ends[0] - 1
+        return Route(*self._verb("route", experts, n_experts))
 
     def route_gather(self, x, route: Route, out=None):
         """x's rows in the experts' order: [rows * top, dim], zeros past the last
         routed place."""
-        xp, xt, n, dim, xs = self._rows(x, "x")
-        pp, fp, n, top, E = self._routed(route, n)
-        out, op, _, os_ = self._out(out, (n * top, dim), x.dtype, dim, n * top)
-        self._vec("route_gather", self._lib.hgb_route_gather, (x, *route, out), xp, xt, xs, n, top, dim, pp, fp, E, op, os_)
-        return out
+        return self._verb("route_gather", x, route.position, route.offsets, out)
 
     def route_gather_backward(self, grad, route: Route, out=None):
         """The gradient of route_gather's x: [rows, dim] sums of grad's rows
         ([rows * top, dim])."""
-        pp, _, n, top, _ = self._routed(route)
-        gp, gt, _, dim, gs = self._rows(grad, "grad", rows=n * top)
-        out, op, _, os_ = self._out(out, (n, dim), grad.dtype, dim, n)
-        self._vec("route_gather_backward", self._lib.hgb_route_gather_backward, (grad, *route, out), gp, gt, gs, n, top,
-                  dim, pp, op, os_)
-        return out
-
-    def _weights(self, weights, n, top):
-        return None if weights is None else self._plain(weights, "weights", self._torch.float32, (n, top))
+        return self._verb("route_gather_backward", grad, route.position, route.offsets, out)
 
     def route_combine(self, y, route: Route, weights=None, out=None):
         """The experts' answers y ([rows * top, dim], in their order) back in the
         rows' order and summed with `weights` (float32 [rows, top], None: ones):
         [rows, dim]."""
-        pp, _, n, top, _ = self._routed(route)
-        yp, yt, _, dim, ys = self._rows(y, "y", rows=n * top)
-        wp = self._weights(weights, n, top)
-        out, op, _, os_ = self._out(out, (n, dim), y.dtype, dim, n)
-        self._vec("route_combine", self._lib.hgb_route_combine, (y, *route, weights, out), yp, yt, ys, n, top, dim, pp, wp,
-                  op, os_)
-        return out
+        return self._verb("route_combine", y, route.position, route.offsets, weights, out)
 
     def route_combine_backward(self, grad, y, route: Route, weights=None, out=None):
         """Gradients of route_combine: (dy [rows * top, dim], dweights [rows, top],
         None without weights)."""
-        gp, gt, n, dim, gs = self._rows(grad, "grad")
-        pp, fp, n, top, E = self._routed(route, n)
-        yp, _, _, _, ys = self._rows(y, "y", dim, n * top, grad.dtype)
-        wp = self._weights(weights, n, top)
-        out, op, _, os_ = self._out(out, (n * top, dim), grad.dtype, dim, n * top)
-        dw = self._torch.empty_like(weights) if weights is not None else None
-        self._vec("route_combine_backward", self._lib.hgb_route_combine_backward, (grad, y, *route, weights, out, dw), gp,
-                  gt, gs, yp, ys, n, top, dim, pp, fp, E, wp, op, os_, dw.data_ptr() if dw is not None else None)
-        return out, dw
+        return self._verb("route_combine_backward", grad, y, route.position, route.offsets, weights, out)

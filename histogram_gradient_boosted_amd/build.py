@@ -12,6 +12,9 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libhgb.so")
 SOURCES = [os.path.join(CSRC, "hgb.hip"), os.path.join(CSRC, "hgb_vectors.hip")]
+# the vector verbs on torch tensors, host code over the C ABI
+VERBS_LIB = os.path.join(PKG, "_verbs.so")
+VERBS_SOURCE = os.path.join(CSRC, "hgb_verbs.cpp")
 # the LDS atomic-rate microbenchmark that bench.py reports beside the fill
 PROBE_LIB = os.path.join(PKG, "liblds_rate.so")
 PROBE_SOURCES = [os.path.join(CSRC, "lds_rate.hip")]
@@ -41,9 +44,29 @@ def _compile(lib: str, sources, verbose: bool) -> None:
     os.replace(tmp, lib)
 
 
+def _compile_verbs(verbose: bool) -> None:
+    import sysconfig
+
+    import torch
+    from torch.utils.cpp_extension import include_paths
+    tmp = VERBS_LIB + ".tmp"
+    libs = os.path.join(os.path.dirname(torch.__file__), "lib")
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden", "-Wall",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           *[f"-isystem{p}" for p in (*include_paths(), sysconfig.get_paths()["include"])], "-I", INCLUDE,
+           "-o", tmp, VERBS_SOURCE, "-L", PKG, "-l:libhgb.so", "-Wl,-rpath,$ORIGIN", "-L", libs, "-ltorch_python",
+           "-ltorch_cpu", "-lc10"]
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    subprocess.run(cmd, check=True)
+    os.replace(tmp, VERBS_LIB)
+
+
 def build(verbose: bool = False) -> str:
-    """Compile libhgb.so and the LDS-rate microbenchmark library."""
+    """Compile libhgb.so, the torch side of its vector verbs and the LDS-rate
+    microbenchmark library."""
     _compile(LIB, SOURCES, verbose)
+    _compile_verbs(verbose)
     _compile(PROBE_LIB, PROBE_SOURCES, verbose)
     return LIB
 
