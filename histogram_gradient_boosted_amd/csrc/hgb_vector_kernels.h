@@ -178,11 +178,12 @@ __device__ inline void wave_order()
 // rank[i]: the elements of the same digit before it in its wave; on return
 // count[w * radix + d] holds the digit's elements in the waves before w and
 // total[d] those of the whole tile.
-template <int ITEMS>
+// WAVES: the block's, where the compiler may know and the registers suffice.
+template <int ITEMS, int WAVES = 0>
 __device__ inline void tile_ranks(const uint32_t (&digit)[ITEMS], int live, int bits, int radix, uint32_t* count,
                                   uint32_t* total, uint32_t (&rank)[ITEMS])
 {
-    const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, waves = blockDim.x >> 6;
+    const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, waves = WAVES ? WAVES : blockDim.x >> 6;
     for (int i = threadIdx.x; i < waves * radix; i += blockDim.x) count[i] = 0;
     __syncthreads();
     uint32_t* mine = count + w * radix;
@@ -210,10 +211,21 @@ __device__ inline void tile_ranks(const uint32_t (&digit)[ITEMS], int live, int 
     __syncthreads();
     for (int d = threadIdx.x; d < radix; d += blockDim.x) {
         uint32_t sum = 0;
-        for (int k = 0; k < waves; ++k) {
-            const uint32_t c = count[k * radix + d];
-            count[k * radix + d] = sum;
-            sum += c;
+        if (WAVES) {   // all loads before the first store
+            uint32_t c[WAVES ? WAVES : 1];
+#pragma unroll
+            for (int k = 0; k < WAVES; ++k) c[k] = count[k * radix + d];
+#pragma unroll
+            for (int k = 0; k < WAVES; ++k) {
+                count[k * radix + d] = sum;
+                sum += c[k];
+            }
+        } else {
+            for (int k = 0; k < waves; ++k) {
+                const uint32_t c = count[k * radix + d];
+                count[k * radix + d] = sum;
+                sum += c;
+            }
         }
         total[d] = sum;
     }
@@ -222,9 +234,10 @@ __device__ inline void tile_ranks(const uint32_t (&digit)[ITEMS], int live, int 
 
 // Exclusive sums of v[0, radix) in place, radix <= the block's threads;
 // `tmp` holds a word per wave.
+template <int WAVES = 0>
 __device__ inline void block_scan(uint32_t* v, int radix, uint32_t* tmp)
 {
-    const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, waves = blockDim.x >> 6;
+    const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, waves = WAVES ? WAVES : blockDim.x >> 6;
     const uint32_t own = (int)threadIdx.x < radix ? v[threadIdx.x] : 0;
     uint32_t x = own;
 #pragma unroll
@@ -434,7 +447,7 @@ __global__ __launch_bounds__(kSortThreads, 8) void k_sort_scatter(SortIn in, Sor
         if ((int)threadIdx.x < p.radix) total[threadIdx.x] += base[threadIdx.x];
         __syncthreads();
     }
-    block_scan(total, p.radix, tmp);
+    block_scan<ITEMS == 1 ? kSortThreads / 64 : 0>(total, p.radix, tmp);
     if (out.offsets && blockIdx.x == 0)
         for (int k = threadIdx.x; k <= in.limit; k += blockDim.x) out.offsets[k] = (int32_t)total[k];
     if ((int)threadIdx.x < p.radix) base[threadIdx.x] += total[threadIdx.x];
@@ -453,7 +466,7 @@ __global__ __launch_bounds__(kSortThreads, 8) void k_sort_scatter(SortIn in, Sor
             if (first + i * 64 < live) kv[i] = sort_load<FIRST>(in, begin + first + i * 64, &bad);
             digit[i] = (kv[i].x >> shift) & (p.radix - 1);
         }
-        tile_ranks<ITEMS>(digit, live, p.bits, p.radix, count, total, rank);
+        tile_ranks<ITEMS, ITEMS == 1 ? kSortThreads / 64 : 0>(digit, live, p.bits, p.radix, count, total, rank);
         if (ITEMS == 1) {
             if (first < live) {
                 const int64_t at = base[digit[0]] + count[w * p.radix + digit[0]] + rank[0];
@@ -472,7 +485,7 @@ __global__ __launch_bounds__(kSortThreads, 8) void k_sort_scatter(SortIn in, Sor
         // in LDS at their place in the tile: total becomes the digits' first
         // places there, and base what leads from such a place to the output's
         const uint32_t keys = (int)threadIdx.x < p.radix ? total[threadIdx.x] : 0;
-        block_scan(total, p.radix, tmp);
+        block_scan<ITEMS == 1 ? kSortThreads / 64 : 0>(total, p.radix, tmp);
         if ((int)threadIdx.x < p.radix) base[threadIdx.x] -= total[threadIdx.x];
         __syncthreads();
 #pragma unroll
@@ -635,15 +648,20 @@ __global__ __launch_bounds__(kJoinThreads) void k_embed_join(const uint2* __rest
         if (id + 1 < chunks) {
             const int64_t begin = id * chunk, end = begin + chunk;
             const uint32_t front = pairs[begin].x, after = pairs[end].x, prev = begin > 0 ? pairs[begin - 1].x : ~0u;
+            const int64_t glance = id + 2 + lane;   // does not wait for the key
+            uint32_t seen = glance < chunks ? pairs[glance * chunk].x : ~0u;
             k = pairs[end - 1].x;
             const bool whole = front == k && prev == k;   // the run began before this chunk
             if (after == k && !whole && k < (uint32_t)vocab) {
                 e = id + 1;   // a chunk that begins with the run
-                for (int len = 64; len == 64; e += len) {
+                uint64_t other = ~__ballot(seen == k);
+                while (other == 0) {
+                    e += 64;
                     const int64_t at = e + 1 + lane;
-                    const uint64_t other = ~__ballot(at < chunks && pairs[at * chunk].x == k);
-                    len = other ? __ffsll((unsigned long long)other) - 1 : 64;
+                    seen = at < chunks ? pairs[at * chunk].x : ~0u;
+                    other = ~__ballot(seen == k);
                 }
+                e += __ffsll((unsigned long long)other) - 1;
             }
         }
         if (lane == 0) {

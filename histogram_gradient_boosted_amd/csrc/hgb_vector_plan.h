@@ -42,7 +42,7 @@ constexpr int kSortSmall = 4 * kSortThreads;
 constexpr int kSortBits = 10;        // of a digit at most, and
 constexpr int kSortManyBits = 8;     // where more than kSortFew blocks' counts are summed
 constexpr int kSortFew = 32;
-constexpr int kSortSelf = 16;
+constexpr int kSortSelf = 8;
 constexpr int kSortMaxBlocks = 512;
 
 struct SortPlan {
@@ -128,7 +128,7 @@ struct EmbedPlan {
 
 constexpr int kEmbedChunk = 256;         // largest chunk
 constexpr int kEmbedFew = 32;
-constexpr int64_t kEmbedWaves = 2048;    // chunks are halved until this many waves run (8 a CU), below 32 a quarter
+constexpr int64_t kEmbedWaves = 2048;    // chunks are halved until this many waves run (8 a CU), below 16 a quarter
 
 inline EmbedPlan plan_embed(int64_t n, int64_t vocab, int64_t dim)
 {
@@ -143,7 +143,7 @@ inline EmbedPlan plan_embed(int64_t n, int64_t vocab, int64_t dim)
         while (p.chunk > least && vec_ceil(n, p.chunk) * vecs / 64 < waves) p.chunk /= 2;
     };
     if (n > kEmbedFew) {
-        fewer(32, kEmbedWaves);
+        fewer(16, kEmbedWaves);
         fewer(8, kEmbedWaves / 4);
     }
     p.chunks = vec_ceil(n, p.chunk);

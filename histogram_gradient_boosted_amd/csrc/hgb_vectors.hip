@@ -194,23 +194,22 @@ hgb_status launch_scatter(hgb_ctx* c, const SortIn& in, const SortOut& out, cons
 
 template <bool FIRST>
 hgb_status launch_pass(hgb_ctx* c, const SortIn& in, const SortOut& out, const SortPlan& p, int shift, uint32_t* counts,
-                       const ZeroFill& z)
+                       const ZeroFill& with_count, const ZeroFill& with_scatter)
 {
-    ZeroFill rest = z;
     if (p.count) {
+        const ZeroFill& z = with_count;
         k_sort_count<FIRST><<<p.blocks + zero_blocks(c, z.rows * z.cols * z.elem, kSortThreads), kSortThreads, 4 * p.row,
                               c->stream>>>(in, p, shift, counts, z);
         HGB_LAUNCHED(c, "k_sort_count");
-        rest = ZeroFill{};
     }
-    if (p.items == 1) return launch_scatter<FIRST, 1>(c, in, out, p, shift, counts, rest);
-    if (p.items == 4) return launch_scatter<FIRST, 4>(c, in, out, p, shift, counts, rest);
-    return launch_scatter<FIRST, kSortItems>(c, in, out, p, shift, counts, rest);
+    if (p.items == 1) return launch_scatter<FIRST, 1>(c, in, out, p, shift, counts, with_scatter);
+    if (p.items == 4) return launch_scatter<FIRST, 4>(c, in, out, p, shift, counts, with_scatter);
+    return launch_scatter<FIRST, kSortItems>(c, in, out, p, shift, counts, with_scatter);
 }
 
 // The sort of in.tokens into `out` (out.to: into whichever of a and b the
 // last pass writes; returned in *sorted), and the zeros beside it: an equal
-// part of their rows with each pass, so that the fill hides the passes' waits.
+// part of their rows with each launch, so that the fill hides the sort's waits.
 hgb_status launch_sort(hgb_ctx* c, SortIn in, SortOut out, const SortPlan& p, const ZeroFill& z, uint32_t* counts, uint2* a,
                        uint2* b, const uint2** sorted)
 {
@@ -219,18 +218,23 @@ hgb_status launch_sort(hgb_ctx* c, SortIn in, SortOut out, const SortPlan& p, co
         if (sorted) *sorted = a;
         return p.items == 1 ? launch_sort_small<1>(c, in, out, p, z) : launch_sort_small<4>(c, in, out, p, z);
     }
+    const int launches = p.passes * (p.count ? 2 : 1);
+    auto part = [&](int launch) {
+        const int64_t first = z.rows * launch / launches, end = z.rows * (launch + 1) / launches;
+        ZeroFill r = z;
+        r.out = (char*)z.out + first * z.stride * z.elem;
+        r.rows = end - first;
+        return r;
+    };
     for (int pass = 0; pass < p.passes; ++pass) {
-        const int shift = pass * p.bits;
-        const int64_t first = z.rows * pass / p.passes, end = z.rows * (pass + 1) / p.passes;
-        ZeroFill part = z;
-        part.out = (char*)z.out + first * z.stride * z.elem;
-        part.rows = end - first;
+        const int shift = pass * p.bits, launch = p.count ? 2 * pass : pass;
+        const ZeroFill one = part(launch), two = p.count ? part(launch + 1) : one;
         if (a) out.to = pass & 1 ? b : a;
         if (pass == 0) {
-            HGB_TRY(launch_pass<true>(c, in, out, p, shift, counts, part));
+            HGB_TRY(launch_pass<true>(c, in, out, p, shift, counts, one, two));
         } else {
             in.from = pass & 1 ? a : b;
-            HGB_TRY(launch_pass<false>(c, in, out, p, shift, counts, part));
+            HGB_TRY(launch_pass<false>(c, in, out, p, shift, counts, one, two));
         }
     }
     if (sorted) *sorted = out.to;
