@@ -50,15 +50,20 @@ __device__ inline void load_vals(float (&r)[V], const T* p, int64_t left)
     for (int k = 0; k < V; ++k) r[k] = (float)v[k];
 }
 
-// `stream`: past the caches, for large calls whose rows are 16-byte aligned.
+// `stream`: past the caches, for large calls.
 template <int V, bool WHOLE = false, typename T>
 __device__ inline void store_raw(const typename Vals<T, V>::type& v, T* p, int64_t left, bool stream)
 {
     typedef typename Vals<T, V>::type Vec;
-    typedef uint32_t Words __attribute__((ext_vector_type(sizeof(Vec) / 4)));   // aligned: else the compiler drops the hint
     if (WHOLE ? left > 0 : left >= V) {
-        if (stream) __builtin_nontemporal_store(__builtin_bit_cast(Words, v), (Words*)p);
-        else *(Vec*)p = v;
+        if (stream) {
+            // the empty asm keeps the two stores apart: made one, they lose the hint
+            asm volatile("");
+            __builtin_nontemporal_store(v, (Vec*)p);
+            asm volatile("");
+        } else {
+            *(Vec*)p = v;
+        }
     } else if (!WHOLE) {
 #pragma unroll
         for (int k = 0; k < V; ++k)
@@ -259,17 +264,16 @@ struct ZeroFill {
     void* out = nullptr;
     int64_t rows = 0, cols = 0, stride = 0;   // elements
     int elem = 4;                             // bytes
-    bool stream = false;                      // past the caches; the rows are 16-byte aligned then
+    bool stream = false;                      // past the caches
 };
 
-typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x4_any __attribute__((ext_vector_type(4), aligned(2)));
 
 __device__ inline void zero_row(char* p, int64_t bytes, int64_t first, int64_t step, bool stream)
 {
     const int64_t whole = bytes / 16;
     if (stream)
-        for (int64_t i = first; i < whole; i += step) __builtin_nontemporal_store(u32x4{0, 0, 0, 0}, (u32x4*)(p + 16 * i));
+        for (int64_t i = first; i < whole; i += step) __builtin_nontemporal_store(u32x4_any{0, 0, 0, 0}, (u32x4_any*)(p + 16 * i));
     else
         for (int64_t i = first; i < whole; i += step) *(u32x4_any*)(p + 16 * i) = u32x4_any{0, 0, 0, 0};
     for (int64_t i = whole * 8 + first; i < bytes / 2; i += step) ((uint16_t*)p)[i] = 0;

@@ -140,11 +140,7 @@ void by_shape(const NormPlan& p, int64_t dim, int V, F&& f)
 // of 1,835,008 tokens 129 and 173 together; of 917,504 tokens (a call of 118
 // MB) 71 and 64 together, so not below; route_gather and route_combine of
 // 32,768 rows of 1,024, four experts each, 136 and 158.
-bool streams(int64_t bytes, const void* out, int32_t type, int64_t dim, int64_t stride)
-{
-    const int e = elem_size(type);
-    return bytes >= (int64_t)192 << 20 && (uintptr_t)out % 16 == 0 && stride * e % 16 == 0 && dim * e % 16 == 0;
-}
+bool streams(int64_t bytes) { return bytes >= (int64_t)192 << 20; }
 
 int log2_of(int p) { return 31 - __builtin_clz((unsigned)p); }
 
@@ -269,7 +265,7 @@ hgb_status hgb_embed(hgb_ctx* c, const void* table, int32_t table_type, int64_t 
             const int64_t bytes = dim * (n_tokens * (int64_t)sizeof(U) + std::min(n_tokens, vocab) * (int64_t)sizeof(T));
             k_embed<T, U><<<(unsigned)row_blocks(m, n_tokens), 256, 0, c->stream>>>(
                 (const T*)table, table_stride, (int)vocab, (int)dim, tokens, (int)n_tokens, pad, scale, (U*)out, out_stride, m,
-                streams(bytes, out, out_type, dim, out_stride), c->dev_words + kWordVectors);
+                streams(bytes), c->dev_words + kWordVectors);
             HGB_LAUNCHED(c, "k_embed");
             return HGB_OK;
         });
@@ -307,7 +303,7 @@ hgb_status hgb_embed_backward(hgb_ctx* c, const void* grad, int32_t grad_type, i
         z.cols = dim;
         z.stride = out_stride;
         z.elem = elem_size(out_type);
-        z.stream = streams(dim * (n_tokens * elem_size(grad_type) + vocab * z.elem), out, out_type, dim, out_stride);
+        z.stream = streams(dim * (n_tokens * elem_size(grad_type) + vocab * z.elem));
         if (n_tokens == 0) {
             k_zero_rows<<<(unsigned)std::min<int64_t>(vec_ceil(vocab * dim * z.elem, 4096 * 4), 8 * c->n_cu), 256, 0,
                           c->stream>>>(z);
@@ -370,7 +366,7 @@ hgb_status hgb_layer_norm(hgb_ctx* c, const void* x, int32_t type, int64_t x_str
                         (unsigned)std::min<int64_t>(vec_ceil(n_rows, p.per_block), (int64_t)c->n_cu * 2048 / THREADS);
                     k_norm<T, NV, WPR, decltype(tail)::value><<<blocks, THREADS, 0, c->stream>>>(
                         (const T*)x, x_stride, n_rows, (int)dim, weight, bias, param_type, eps, (T*)y, y_stride, mean, rstd,
-                        p.log_group, streams(2 * n_rows * dim * elem_size(type), y, type, dim, y_stride));
+                        p.log_group, streams(2 * n_rows * dim * elem_size(type)));
                 });
             }
             HGB_LAUNCHED(c, "k_norm");
@@ -430,7 +426,7 @@ hgb_status hgb_layer_norm_backward(hgb_ctx* c, const void* grad, int64_t grad_st
                     k_norm_grad<T, NV, WPR, decltype(tail)::value><<<(unsigned)parts, norm_grad_threads(NV, WPR), 0, c->stream>>>(
                         g, grad_stride, (const T*)x, x_stride, n_rows, (int)dim, mean, rstd, weight, param_type, (T*)dx,
                         dx_stride, params ? (float*)workspace : nullptr, p.log_group,
-                        streams(3 * n_rows * dim * elem_size(type), dx, type, dim, dx_stride));
+                        streams(3 * n_rows * dim * elem_size(type)));
                 });
                 HGB_LAUNCHED(c, "k_norm_grad");
             }
@@ -510,7 +506,7 @@ hgb_status hgb_route_gather(hgb_ctx* c, const void* x, int32_t type, int64_t x_s
             const RowMap m = plan_rows(dim, kVals<T>);
             k_route_gather<T><<<(unsigned)row_blocks(m, n_rows), 256, 0, c->stream>>>(
                 (const T*)x, x_stride, n_rows, top, (int)dim, position, offsets + n_experts, (T*)out, out_stride, m,
-                streams(n_rows * (top + 1) * dim * elem_size(type), out, type, dim, out_stride));
+                streams(n_rows * (top + 1) * dim * elem_size(type)));
             HGB_LAUNCHED(c, "k_route_gather");
             return HGB_OK;
         });
@@ -534,7 +530,7 @@ static hgb_status combine(hgb_ctx* c, const char* verb, const void* y, int32_t t
         const RowMap m = plan_rows(dim, kVals<T>);
         k_route_combine<T><<<(unsigned)row_blocks(m, n_rows), 256, 0, c->stream>>>(
             (const T*)y, y_stride, n_rows, top, (int)dim, position, weight, (T*)out, out_stride, m,
-            streams(n_rows * (top + 1) * dim * elem_size(type), out, type, dim, out_stride));
+            streams(n_rows * (top + 1) * dim * elem_size(type)));
         HGB_LAUNCHED(c, "k_route_combine");
         return HGB_OK;
     });
@@ -580,7 +576,7 @@ hgb_status hgb_route_combine_backward(hgb_ctx* c, const void* grad, int32_t type
             using T = std::remove_pointer_t<decltype(t)>;
             const int64_t vecs = vec_ceil(dim, kVals<T>), slots = n_rows * top;
             const int lg = log2_of(vec_pow2(std::min<int64_t>(vecs, 64)));
-            const bool stream = streams(n_rows * ((dweight ? 2 : 1) * top + 1) * dim * elem_size(type), dy, type, dim, dy_stride);
+            const bool stream = streams(n_rows * ((dweight ? 2 : 1) * top + 1) * dim * elem_size(type));
             auto* kernel = lg == 6 ? k_route_combine_grad<T, true> : k_route_combine_grad<T, false>;
             kernel<<<(unsigned)vec_ceil(slots, 256 >> lg), 256, 0, c->stream>>>(
                 (const T*)grad, grad_stride, (const T*)y, y_stride, n_rows, top, (int)dim, position, offsets + n_experts, weight,
