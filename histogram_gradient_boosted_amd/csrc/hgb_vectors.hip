@@ -13,6 +13,7 @@
 #include <hip/hip_runtime.h>
 
 #include <cmath>
+#include <initializer_list>
 #include <type_traits>
 
 using namespace hgb;
@@ -46,10 +47,31 @@ Span span(const void* p, int32_t type, int64_t rows, int64_t dim, int64_t stride
     return {(const char*)p, p && rows > 0 ? ((rows - 1) * stride + dim) * elem_size(type) : 0};
 }
 
-hgb_status check_apart(hgb_ctx* c, const char* verb, const Span& out, const Span& in)
+Span span(const int32_t* p, int64_t n) { return {(const char*)p, p ? n * 4 : 0}; }
+Span span(const float* p, int64_t n) { return {(const char*)p, p ? n * 4 : 0}; }
+
+bool overlap(const Span& a, const Span& b)
 {
-    if (out.bytes > 0 && in.bytes > 0 && out.begin < in.begin + in.bytes && in.begin < out.begin + out.bytes)
-        return fail(c, HGB_E_INVALID, "%s: an output overlaps an input", verb);
+    return a.bytes > 0 && b.bytes > 0 && a.begin < b.begin + b.bytes && b.begin < a.begin + a.bytes;
+}
+
+// No output overlaps an input or another output; a workspace counts as an output.
+hgb_status check_apart(hgb_ctx* c, const char* verb, std::initializer_list<Span> outs, std::initializer_list<Span> ins)
+{
+    for (auto o = outs.begin(); o != outs.end(); ++o) {
+        for (const Span& in : ins)
+            if (overlap(*o, in)) return fail(c, HGB_E_INVALID, "%s: an output overlaps an input", verb);
+        for (auto other = outs.begin(); other != o; ++other)
+            if (overlap(*o, *other)) return fail(c, HGB_E_INVALID, "%s: an output overlaps another", verb);
+    }
+    return HGB_OK;
+}
+
+// Pointers to 32-bit values are aligned to them.
+hgb_status check_words(hgb_ctx* c, const char* verb, std::initializer_list<const void*> words)
+{
+    for (const void* p : words)
+        if ((uintptr_t)p % 4) return fail(c, HGB_E_INVALID, "%s: a pointer is not aligned to 4 bytes", verb);
     return HGB_OK;
 }
 
@@ -253,8 +275,9 @@ hgb_status hgb_embed(hgb_ctx* c, const void* table, int32_t table_type, int64_t 
         if (!is_pair(table_type, out_type))
             return fail(c, HGB_E_UNSUPPORTED, "embed: out has the table's type, or 16 bits beside a 32-bit table");
         if (n_tokens > 0 && !tokens) return fail(c, HGB_E_INVALID, "embed: tokens is null");
-        HGB_TRY(check_apart(c, "embed", span(out, out_type, n_tokens, dim, out_stride),
-                            span(table, table_type, vocab, dim, table_stride)));
+        HGB_TRY(check_words(c, "embed", {tokens}));
+        HGB_TRY(check_apart(c, "embed", {span(out, out_type, n_tokens, dim, out_stride)},
+                            {span(table, table_type, vocab, dim, table_stride), span(tokens, n_tokens)}));
         if (n_tokens == 0) return HGB_OK;
         HGB_HIP(c, hipSetDevice(c->device));
         ProfScope ps(c, HGB_KERNEL_EMBED);
@@ -291,10 +314,14 @@ hgb_status hgb_embed_backward(hgb_ctx* c, const void* grad, int32_t grad_type, i
         if (!is_pair(out_type, grad_type))
             return fail(c, HGB_E_UNSUPPORTED, "embed_backward: grad has out's type, or 16 bits beside a 32-bit out");
         if (n_tokens > 0 && !tokens) return fail(c, HGB_E_INVALID, "embed_backward: tokens is null");
-        HGB_TRY(check_apart(c, "embed_backward", span(out, out_type, vocab, dim, out_stride),
-                            span(grad, grad_type, n_tokens, dim, grad_stride)));
+        HGB_TRY(check_words(c, "embed_backward", {tokens}));
         const EmbedPlan p = plan_embed(n_tokens, vocab, dim);
-        if (n_tokens > 0) HGB_TRY(check_workspace(c, "embed_backward", workspace, workspace_bytes, p.bytes));
+        const Span to = span(out, out_type, vocab, dim, out_stride), from = span(grad, grad_type, n_tokens, dim, grad_stride);
+        HGB_TRY(check_apart(c, "embed_backward", {to}, {from, span(tokens, n_tokens)}));
+        if (n_tokens > 0) {
+            HGB_TRY(check_workspace(c, "embed_backward", workspace, workspace_bytes, p.bytes));
+            HGB_TRY(check_apart(c, "embed_backward", {to, Span{(const char*)workspace, p.bytes}}, {from, span(tokens, n_tokens)}));
+        }
         HGB_HIP(c, hipSetDevice(c->device));
         ProfScope ps(c, HGB_KERNEL_EMBED);
         ZeroFill z;
@@ -350,7 +377,10 @@ hgb_status hgb_layer_norm(hgb_ctx* c, const void* x, int32_t type, int64_t x_str
         if (!(eps >= 0.0f) || std::isinf(eps)) return fail(c, HGB_E_INVALID, "layer_norm: eps must be finite and not negative");
         if (n_rows == 0) return HGB_OK;
         if (!mean || !rstd) return fail(c, HGB_E_INVALID, "layer_norm: mean or rstd is null");
-        HGB_TRY(check_apart(c, "layer_norm", span(y, type, n_rows, dim, y_stride), span(x, type, n_rows, dim, x_stride)));
+        HGB_TRY(check_words(c, "layer_norm", {mean, rstd}));
+        HGB_TRY(check_apart(c, "layer_norm", {span(y, type, n_rows, dim, y_stride), span(mean, n_rows), span(rstd, n_rows)},
+                            {span(x, type, n_rows, dim, x_stride), span(weight, param_type, 1, dim, dim),
+                             span(bias, param_type, 1, dim, dim)}));
         HGB_HIP(c, hipSetDevice(c->device));
         ProfScope ps(c, HGB_KERNEL_NORM);
         return by_type(type, [&](auto* t) -> hgb_status {
@@ -398,10 +428,20 @@ hgb_status hgb_layer_norm_backward(hgb_ctx* c, const void* grad, int64_t grad_st
         if (param_type != type && param_type != HGB_F32)
             return fail(c, HGB_E_UNSUPPORTED, "%s: the parameters have x's type, or 32 bits", verb);
         if (n_rows > 0 && (!mean || !rstd)) return fail(c, HGB_E_INVALID, "%s: mean or rstd is null", verb);
-        HGB_TRY(check_apart(c, verb, span(dx, type, n_rows, dim, dx_stride), span(x, type, n_rows, dim, x_stride)));
-        HGB_TRY(check_apart(c, verb, span(dx, type, n_rows, dim, dx_stride), span(grad, type, n_rows, dim, grad_stride)));
+        HGB_TRY(check_words(c, verb, {mean, rstd}));
         const bool params = dweight || dbias;
-        if (params) HGB_TRY(check_workspace(c, verb, workspace, workspace_bytes, norm_workspace(n_rows, dim)));
+        const auto apart = [&](int64_t scratch) {
+            return check_apart(c, verb,
+                               {span(dx, type, n_rows, dim, dx_stride), span(dweight, param_type, 1, dim, dim),
+                                span(dbias, param_type, 1, dim, dim), Span{(const char*)workspace, scratch}},
+                               {span(x, type, n_rows, dim, x_stride), span(grad, type, n_rows, dim, grad_stride),
+                                span(mean, n_rows), span(rstd, n_rows), span(weight, param_type, 1, dim, dim)});
+        };
+        HGB_TRY(apart(0));
+        if (params) {
+            HGB_TRY(check_workspace(c, verb, workspace, workspace_bytes, norm_workspace(n_rows, dim)));
+            HGB_TRY(apart(norm_workspace(n_rows, dim)));
+        }
         HGB_HIP(c, hipSetDevice(c->device));
         ProfScope ps(c, HGB_KERNEL_NORM);
         const NormPlan p = plan_norm(dim);
@@ -478,6 +518,11 @@ hgb_status hgb_route(hgb_ctx* c, const int32_t* experts, int64_t n_rows, int32_t
         if (!offsets) return fail(c, HGB_E_INVALID, "route: offsets is null");
         const int64_t n = n_rows * top;
         HGB_TRY(check_workspace(c, "route", workspace, workspace_bytes, route_workspace(n, n_experts)));
+        HGB_TRY(check_words(c, "route", {experts, order, position, offsets}));
+        HGB_TRY(check_apart(c, "route",
+                            {span(order, n), span(position, n), span(offsets, (int64_t)n_experts + 1),
+                             Span{(const char*)workspace, route_workspace(n, n_experts)}},
+                            {span(experts, n)}));
         HGB_HIP(c, hipSetDevice(c->device));
         ProfScope ps(c, HGB_KERNEL_ROUTE);
         SortIn in{experts, nullptr, n, n_experts, -1, kVecErrExpert, c->dev_words + kWordVectors};
@@ -497,8 +542,10 @@ hgb_status hgb_route_gather(hgb_ctx* c, const void* x, int32_t type, int64_t x_s
         HGB_TRY(check_rows(c, "route_gather", "out", out, type, n_rows, dim, out_stride));
         if (n_rows == 0) return HGB_OK;
         if (!offsets) return fail(c, HGB_E_INVALID, "route_gather: offsets is null");
-        HGB_TRY(check_apart(c, "route_gather", span(out, type, n_rows * top, dim, out_stride),
-                            span(x, type, n_rows, dim, x_stride)));
+        HGB_TRY(check_words(c, "route_gather", {position, offsets}));
+        HGB_TRY(check_apart(c, "route_gather", {span(out, type, n_rows * top, dim, out_stride)},
+                            {span(x, type, n_rows, dim, x_stride), span(position, n_rows * top),
+                             span(offsets, (int64_t)n_experts + 1)}));
         HGB_HIP(c, hipSetDevice(c->device));
         ProfScope ps(c, HGB_KERNEL_ROUTE);
         return by_type(type, [&](auto* t) -> hgb_status {
@@ -522,7 +569,9 @@ static hgb_status combine(hgb_ctx* c, const char* verb, const void* y, int32_t t
     HGB_TRY(check_rows(c, verb, "the sorted rows", y, type, n_rows, dim, y_stride));
     HGB_TRY(check_rows(c, verb, "out", out, type, n_rows, dim, out_stride));
     if (n_rows == 0) return HGB_OK;
-    HGB_TRY(check_apart(c, verb, span(out, type, n_rows, dim, out_stride), span(y, type, n_rows * top, dim, y_stride)));
+    HGB_TRY(check_words(c, verb, {position, weight}));
+    HGB_TRY(check_apart(c, verb, {span(out, type, n_rows, dim, out_stride)},
+                        {span(y, type, n_rows * top, dim, y_stride), span(position, n_rows * top), span(weight, n_rows * top)}));
     HGB_HIP(c, hipSetDevice(c->device));
     ProfScope ps(c, HGB_KERNEL_ROUTE);
     return by_type(type, [&](auto* t) -> hgb_status {
@@ -567,9 +616,11 @@ hgb_status hgb_route_combine_backward(hgb_ctx* c, const void* grad, int32_t type
         HGB_TRY(check_rows(c, verb, "their gradient", dy, type, n_rows, dim, dy_stride));
         if (n_rows == 0) return HGB_OK;
         if (!offsets) return fail(c, HGB_E_INVALID, "%s: offsets is null", verb);
-        const Span to = span(dy, type, n_rows * top, dim, dy_stride);
-        HGB_TRY(check_apart(c, verb, to, span(grad, type, n_rows, dim, grad_stride)));
-        if (dweight) HGB_TRY(check_apart(c, verb, to, span(y, type, n_rows * top, dim, y_stride)));
+        HGB_TRY(check_words(c, verb, {position, offsets, weight, dweight}));
+        HGB_TRY(check_apart(c, verb, {span(dy, type, n_rows * top, dim, dy_stride), span(dweight, n_rows * top)},
+                            {span(grad, type, n_rows, dim, grad_stride),
+                             span(dweight ? y : nullptr, type, n_rows * top, dim, y_stride), span(position, n_rows * top),
+                             span(offsets, (int64_t)n_experts + 1), span(weight, n_rows * top)}));
         HGB_HIP(c, hipSetDevice(c->device));
         ProfScope ps(c, HGB_KERNEL_ROUTE);
         return by_type(type, [&](auto* t) -> hgb_status {

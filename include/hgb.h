@@ -477,8 +477,8 @@ hgb_status hgb_grow_level(hgb_ctx* ctx, const int64_t* parent_hist_dev, const hg
  *     verb refuses).  Its contents mean nothing before and after the call, and
  *     calls that may overlap need one each.  The verbs allocate nothing and
  *     wait for nothing, so they can be captured into a graph.
- *   - An output that overlaps an input is refused (HGB_E_INVALID); outputs may
- *     not overlap each other.
+ *   - An output that overlaps an input or another output is refused
+ *     (HGB_E_INVALID); the workspace counts as an output.
  *   - Zero rows or tokens are valid and leave only what the verb defines for
  *     them.
  */

@@ -160,6 +160,25 @@ static void refusals()
     is(hgb_route_gather_backward(&c, f, F, 4, 2, 2, 4, nullptr, f + 32, 4), HGB_E_INVALID, "position");
     is(hgb_route_combine_backward(&c, f, F, 4, f + 8, 4, 2, 2, 4, i, nullptr, 3, f, f + 24, 4, f + 60), HGB_E_INVALID, "offsets");
     is(hgb_route_combine_backward(&c, f, F, 4, f + 8, 4, 2, 2, 4, i, i, 3, f, f + 8, 4, f + 60), HGB_E_INVALID, "overlaps");
+    // every pointer's alignment, and every output against every input and the other outputs
+    int32_t* odd = (int32_t*)((char*)i + 2);
+    is(hgb_embed(&c, f, F, 4, 3, 4, odd, 5, -1, 1, f + 32, F, 4), HGB_E_INVALID, "aligned");
+    is(hgb_embed(&c, f, F, 4, 3, 4, (int32_t*)(f + 36), 5, -1, 1, f + 32, F, 4), HGB_E_INVALID, "overlaps");
+    is(hgb_embed_backward(&c, f, F, 4, 5, 4, i, -1, 1, 3, f + 32, F, 4, f + 40, 1 << 20), HGB_E_INVALID, "overlaps");
+    is(hgb_layer_norm(&c, f, F, 4, 2, 4, f + 8, nullptr, F, 1e-5f, f + 9, 4, f + 50, f + 52), HGB_E_INVALID, "overlaps");
+    is(hgb_layer_norm(&c, f, F, 4, 2, 4, nullptr, nullptr, F, 1e-5f, f + 16, 4, f + 50, f + 51), HGB_E_INVALID, "another");
+    is(hgb_layer_norm(&c, f, F, 4, 2, 4, nullptr, nullptr, F, 1e-5f, f + 16, 4, (float*)odd, f + 51), HGB_E_INVALID, "aligned");
+    is(hgb_layer_norm_backward(&c, f, 4, f + 8, 4, F, 2, 4, f + 50, f + 52, nullptr, F, f + 16, 4, f + 40, f + 41, ws, 4096),
+       HGB_E_INVALID, "another");
+    is(hgb_layer_norm_backward(&c, f, 4, f + 8, 4, F, 2, 4, f + 50, f + 52, nullptr, F, f + 16, 4, f + 40, f + 44, f + 48, 4096),
+       HGB_E_INVALID, "overlaps");
+    is(hgb_route(&c, i, 4, 2, 3, i + 4, i + 16, i + 24, nullptr, 0), HGB_E_INVALID, "overlaps");
+    is(hgb_route(&c, i, 4, 2, 3, i + 8, i + 12, i + 24, nullptr, 0), HGB_E_INVALID, "another");
+    is(hgb_route(&c, odd, 4, 2, 3, i + 8, i + 16, i + 24, nullptr, 0), HGB_E_INVALID, "aligned");
+    is(hgb_route_gather(&c, f, F, 4, 2, 2, 4, odd, i, 3, f + 8, 4), HGB_E_INVALID, "aligned");
+    is(hgb_route_gather(&c, f, F, 4, 2, 2, 4, (int32_t*)(f + 20), i, 3, f + 8, 4), HGB_E_INVALID, "overlaps");
+    is(hgb_route_combine(&c, f, F, 4, 2, 2, 4, i, f + 33, f + 32, 4), HGB_E_INVALID, "overlaps");
+    is(hgb_route_combine_backward(&c, f, F, 4, f + 8, 4, 2, 2, 4, i, i + 8, 3, f, f + 24, 4, f + 39), HGB_E_INVALID, "another");
     CHECK(hgb_embed(nullptr, f, F, 4, 3, 4, i, 5, -1, 1, f, F, 4) == HGB_E_INVALID);
     CHECK(hgb_route(nullptr, i, 4, 2, 3, i, i, i, nullptr, 0) == HGB_E_INVALID);
 }
