@@ -29,12 +29,14 @@ struct Vals {
 // `left` of the values lie in the row, the others are zeros.  WHOLE: all do or
 // none, which spares the code for a part: a row's last vector then ends where
 // the row does and shares values with the one before it (both store the same).
-template <int V, bool WHOLE = false, typename T>
+// STREAM: past the caches, for rows that a large call reads once.
+template <int V, bool WHOLE = false, bool STREAM = false, typename T>
 __device__ inline typename Vals<T, V>::type load_raw(const T* p, int64_t left)
 {
-    typename Vals<T, V>::type v{};
+    typedef typename Vals<T, V>::type Vec;
+    Vec v{};
     if (WHOLE ? left > 0 : left >= V) {
-        v = *(const typename Vals<T, V>::type*)p;
+        v = STREAM ? __builtin_nontemporal_load((const Vec*)p) : *(const Vec*)p;
     } else if (!WHOLE) {
 #pragma unroll
         for (int k = 0; k < V; ++k) v[k] = k < left ? p[k] : (T)0.0f;
@@ -557,13 +559,14 @@ __global__ __launch_bounds__(256) void k_zero_rows(ZeroFill z) { zero_fill(z, bl
 // chunk's partial rows: row 0 a run that began before the chunk, row 1 one
 // that begins in it and goes on.  The order of the sums depends on the tokens
 // alone.  Bound by the gradient's rows, 128 bytes each in the measured case, in
-// the tokens' order: 3,670,016 rows of 64 bf16 values in 113 us, 4.2 TB/s (the
-// same reads in row order: 105; a large copy: 4.9 TB/s).
+// the tokens' order: 3,670,016 rows of 64 bf16 values in 108 us, 4.5 TB/s (through
+// the caches 114; a large copy: 4.9 TB/s).
 template <typename T, typename U>
 __global__ __launch_bounds__(256) void k_embed_sum(const uint2* __restrict__ pairs, int64_t n, const T* __restrict__ grad,
                                                    int64_t grad_stride, int64_t dim, int64_t vocab, float scale,
                                                    U* __restrict__ out, int64_t out_stride, float* __restrict__ part,
-                                                   int64_t part_stride, int chunk, int64_t chunks, RowMap m)
+                                                   int64_t part_stride, int chunk, int64_t chunks, RowMap m,
+                                                   bool stream)
 {
     constexpr int V = kVals<T, U>;
     const RowPlace at = row_place<V>(m, chunks, (int)dim);
@@ -573,9 +576,9 @@ __global__ __launch_bounds__(256) void k_embed_sum(const uint2* __restrict__ pai
     const uint32_t prev = begin > 0 ? pairs[begin - 1].x : none, next = end < n ? pairs[end].x : none;
     // STEP rows in flight; fewer where a row is shorter than a vector and its
     // values are loaded one by one
-    auto walk = [&](auto step) {
+    auto walk = [&](auto step, auto past) {
         constexpr int STEP = decltype(step)::value;
-        constexpr bool WHOLE = STEP == 8;
+        constexpr bool WHOLE = STEP == 8, STREAM = decltype(past)::value;
         uint32_t cur = pairs[begin].x;
         bool head = cur == prev;
         float acc[V];
@@ -602,7 +605,7 @@ __global__ __launch_bounds__(256) void k_embed_sum(const uint2* __restrict__ pai
             // a dropped token's row is not read: its sum, which no one stores, takes row 0
 #pragma unroll
             for (int u = 0; u < STEP; ++u)
-                v[u] = load_raw<V, WHOLE>(grad + (kv[u].x < (uint32_t)vocab ? (uint64_t)kv[u].y : 0) * (uint64_t)grad_stride + c, dim);
+                v[u] = load_raw<V, WHOLE, STREAM>(grad + (kv[u].x < (uint32_t)vocab ? (uint64_t)kv[u].y : 0) * (uint64_t)grad_stride + c, dim);
 #pragma unroll
             for (int u = 0; u < STEP; ++u) ahead[u] = pairs[j + STEP + u < end ? j + STEP + u : end - 1];
 #pragma unroll
@@ -621,8 +624,9 @@ __global__ __launch_bounds__(256) void k_embed_sum(const uint2* __restrict__ pai
         }
         flush(cur == next);
     };
-    if (dim >= V) walk(std::integral_constant<int, 8>());
-    else walk(std::integral_constant<int, 4>());
+    if (dim < V) walk(std::integral_constant<int, 4>(), std::false_type());
+    else if (stream) walk(std::integral_constant<int, 8>(), std::true_type());
+    else walk(std::integral_constant<int, 8>(), std::false_type());
 }
 
 // Runs that cross chunk borders: the partial row of the chunk where the run
@@ -1183,7 +1187,7 @@ __global__ __launch_bounds__(256) void k_norm_join(const float* __restrict__ par
 
 // Rows to their slots' places, a vector a thread.  It also zeroes the places of
 // its number range that lie past the last routed slot.  Bound by bytes: 32,768
-// rows of 1,024 bf16 values, four places each, in 65 us, 5.2 TB/s.
+// rows of 1,024 bf16 values, four places each, in 62 us, 5.4 TB/s.
 template <typename T>
 __global__ __launch_bounds__(256) void k_route_gather(const T* __restrict__ x, int64_t x_stride, int64_t rows, int top,
                                                       int dim, const int32_t* __restrict__ position,
@@ -1210,7 +1214,7 @@ __global__ __launch_bounds__(256) void k_route_gather(const T* __restrict__ x, i
 
 // out[r] = sum over k of weight[r][k] * y[position[r][k]], in the order of k,
 // a vector a thread, four rows of y in flight.  Bound by bytes: 32,768 rows of
-// 1,024 bf16 values, four each, in 61 us, 5.5 TB/s.
+// 1,024 bf16 values, four each, in 55 us, 6.1 TB/s (y through the caches: 59).
 template <typename T>
 __global__ __launch_bounds__(256) void k_route_combine(const T* __restrict__ y, int64_t y_stride, int64_t rows, int top,
                                                        int dim, const int32_t* __restrict__ position,
@@ -1221,8 +1225,8 @@ __global__ __launch_bounds__(256) void k_route_combine(const T* __restrict__ y, 
     const RowPlace p = row_place<V>(m, rows, dim);
     if (!p.in) return;
     const int64_t slots = rows * top, first = p.r * top;
-    auto sum = [&](auto whole) {
-        constexpr bool WHOLE = decltype(whole)::value;
+    auto sum = [&](auto whole, auto past) {
+        constexpr bool WHOLE = decltype(whole)::value, STREAM = decltype(past)::value;
         float acc[V];
 #pragma unroll
         for (int k = 0; k < V; ++k) acc[k] = 0.0f;
@@ -1234,17 +1238,18 @@ __global__ __launch_bounds__(256) void k_route_combine(const T* __restrict__ y, 
                 const int64_t at = k + u < top ? position[first + k + u] : -1;
                 const bool live = at >= 0 && at < slots;
                 w[u] = live && weight ? weight[first + k + u] : live;
-                v[u] = live ? load_raw<V, WHOLE>(y + at * y_stride + p.c, dim) : typename Vals<T, V>::type{};
+                v[u] = live ? load_raw<V, WHOLE, STREAM>(y + at * y_stride + p.c, dim) : typename Vals<T, V>::type{};
             }
 #pragma unroll
             for (int u = 0; u < STEP; ++u)
 #pragma unroll
                 for (int i = 0; i < V; ++i) acc[i] = fmaf(w[u], (float)v[u][i], acc[i]);
         }
-        store_vals<V, WHOLE>(acc, out + p.r * out_stride + p.c, dim, stream);
+        store_vals<V, WHOLE>(acc, out + p.r * out_stride + p.c, dim, STREAM);
     };
-    if (dim >= V) sum(std::true_type());
-    else sum(std::false_type());
+    if (dim < V) sum(std::false_type(), std::false_type());
+    else if (stream) sum(std::true_type(), std::true_type());
+    else sum(std::true_type(), std::false_type());
 }
 
 // dy[position[r][k]] = weight[r][k] * grad[r]; dweight[r][k] = <grad[r], y[position[r][k]]>.
@@ -1252,8 +1257,8 @@ __global__ __launch_bounds__(256) void k_route_combine(const T* __restrict__ y, 
 // vectors of each row in flight; a row's slots are neighbours, so that its
 // gradient comes from the cache after the first.  Places past the last routed
 // slot are zeroed as in k_route_gather.  Bound by bytes: 32,768 rows of 1,024
-// bf16 values, four slots each, in 106 us, 5.7 TB/s (a wave a row: 116, and 3
-// times as long for 186 rows of 3,304 values).
+// bf16 values, four slots each, in 94 us, 6.4 TB/s (y through the caches 106, and
+// a wave a row 116; 7 and 45 for 186 rows of 3,304 values, six slots each).
 template <typename T, bool WAVE>
 __global__ __launch_bounds__(256) void k_route_combine_grad(const T* __restrict__ grad, int64_t grad_stride,
                                                             const T* __restrict__ y, int64_t y_stride, int64_t rows,
@@ -1278,8 +1283,8 @@ __global__ __launch_bounds__(256) void k_route_combine_grad(const T* __restrict_
     T* zero = dy + (int64_t)s * dy_stride;
     typedef typename Vals<T, V>::type Vec;
     float dot = 0.0f;
-    auto slot = [&](auto whole) {
-        constexpr bool WHOLE = decltype(whole)::value;
+    auto slot = [&](auto whole, auto past) {
+        constexpr bool WHOLE = decltype(whole)::value, STREAM = decltype(past)::value;
         for (int first = lane * V; first < dim; first += (STEP * V) << log_group) {
             Vec g[STEP], v[STEP];
             int c[STEP];
@@ -1288,7 +1293,7 @@ __global__ __launch_bounds__(256) void k_route_combine_grad(const T* __restrict_
                 const int from = first + ((u * V) << log_group);
                 c[u] = WHOLE ? min(from, dim - V) : from;
                 g[u] = load_raw<V, WHOLE>(g_row + c[u], live ? dim - from : 0);
-                v[u] = load_raw<V, WHOLE>(y_row + c[u], live && dweight ? dim - from : 0);
+                v[u] = load_raw<V, WHOLE, STREAM>(y_row + c[u], live && dweight ? dim - from : 0);
             }
 #pragma unroll
             for (int u = 0; u < STEP; ++u) {
@@ -1300,13 +1305,14 @@ __global__ __launch_bounds__(256) void k_route_combine_grad(const T* __restrict_
                     if (c[u] + i >= from) dot = fmaf((float)g[u][i], (float)v[u][i], dot);
                     out[i] = (float)g[u][i] * w;
                 }
-                if (live) store_vals<V, WHOLE>(out, to + c[u], dim - from, stream);
-                if (s >= used) store_raw<V, WHOLE>(Vec{}, zero + c[u], dim - from, stream);
+                if (live) store_vals<V, WHOLE>(out, to + c[u], dim - from, STREAM);
+                if (s >= used) store_raw<V, WHOLE>(Vec{}, zero + c[u], dim - from, STREAM);
             }
         }
     };
-    if (dim >= V) slot(std::true_type());
-    else slot(std::false_type());
+    if (dim < V) slot(std::false_type(), std::false_type());
+    else if (stream) slot(std::true_type(), std::true_type());
+    else slot(std::true_type(), std::false_type());
     if (dweight) {
         dot = group_sum(dot, log_group);
         if (lane == 0) dweight[s] = dot;

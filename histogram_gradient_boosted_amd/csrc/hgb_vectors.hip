@@ -154,14 +154,15 @@ void by_shape(const NormPlan& p, int64_t dim, int V, F&& f)
     else with(std::integral_constant<int, 32>());
 }
 
-// Whether an output's rows are stored past the caches, in a call that reads
-// and writes `bytes`: where these exceed three quarters of the 256 MB of the
+// Whether a call that reads and writes `bytes` stores its rows past the caches
+// (and loads past them what it reads once: the embedding gradient's rows, the
+// sorted rows of the routing).  Above three quarters of the 256 MB of the
 // memory-side cache, what is left there of the output must be written out
-// beside a later kernel's reads.  In us, past the caches and not, bf16: embed of 3,670,016
-// tokens 81 and 152, then layer_norm of the same values 301 and 334 together;
-// of 1,835,008 tokens 129 and 173 together; of 917,504 tokens (a call of 118
-// MB) 71 and 64 together, so not below; route_gather and route_combine of
-// 32,768 rows of 1,024, four experts each, 136 and 158.
+// beside a later kernel's reads.  In us, past the caches and not, bf16: embed of
+// 3,670,016 tokens 81 and 152, then layer_norm of the same values 301 and 334
+// together; of 1,835,008 tokens 129 and 173 together; of 917,504 tokens (a call
+// of 118 MB) 71 and 64 together, so not below.  route_gather and route_combine
+// of 32,768 rows of 1,024, four experts each, 116 and 158.
 bool streams(int64_t bytes) { return bytes >= (int64_t)192 << 20; }
 
 int log2_of(int p) { return 31 - __builtin_clz((unsigned)p); }
@@ -348,7 +349,7 @@ hgb_status hgb_embed_backward(hgb_ctx* c, const void* grad, int32_t grad_type, i
             const RowMap m = plan_rows(dim, kVals<T, U>);
             k_embed_sum<T, U><<<(unsigned)row_blocks(m, p.chunks), 256, 0, c->stream>>>(
                 pairs, n_tokens, (const T*)grad, grad_stride, dim, vocab, scale, (U*)out, out_stride, part, p.part_stride, p.chunk,
-                p.chunks, m);
+                p.chunks, m, z.stream);
             HGB_LAUNCHED(c, "k_embed_sum");
             if (p.chunks > 1) {
                 const dim3 jgrid((unsigned)vec_ceil(p.chunks, kJoinChunks), (unsigned)vec_ceil(dim, 64));
