@@ -557,16 +557,20 @@ __global__ __launch_bounds__(256) void k_zero_rows(ZeroFill z) { zero_fill(z, bl
 // row's vectors walk one chunk of sorted positions; a run that lies in its chunk is
 // finished there, and a run that crosses a border leaves its part in the
 // chunk's partial rows: row 0 a run that began before the chunk, row 1 one
-// that begins in it and goes on.  The order of the sums depends on the tokens
-// alone.  Bound by the gradient's rows, 128 bytes each in the measured case, in
-// the tokens' order: 3,670,016 rows of 64 bf16 values in 108 us, 4.5 TB/s (through
-// the caches 114; a large copy: 4.9 TB/s).
+// that begins in it and goes on.  ends[chunk] tells k_embed_join: the key of a
+// run that begins in the chunk and goes on, kChunkWhole where one run fills the
+// chunk and goes on at both ends, else kChunkNone.  The order of the sums
+// depends on the tokens alone.  Bound by the gradient's rows, 128 bytes each in the measured case, in
+// the tokens' order: 3,670,016 rows of 64 bf16 values in 104 us, 4.7 TB/s (with a
+// quarter of the waves 108, those through the caches 114; a large copy: 4.9 TB/s).
+constexpr uint32_t kChunkNone = 0xffffffffu, kChunkWhole = 0xfffffffeu;   // no key is that large
+
 template <typename T, typename U>
 __global__ __launch_bounds__(256) void k_embed_sum(const uint2* __restrict__ pairs, int64_t n, const T* __restrict__ grad,
                                                    int64_t grad_stride, int64_t dim, int64_t vocab, float scale,
                                                    U* __restrict__ out, int64_t out_stride, float* __restrict__ part,
-                                                   int64_t part_stride, int chunk, int64_t chunks, RowMap m,
-                                                   bool stream)
+                                                   int64_t part_stride, uint32_t* __restrict__ ends, int chunk,
+                                                   int64_t chunks, RowMap m, bool stream)
 {
     constexpr int V = kVals<T, U>;
     const RowPlace at = row_place<V>(m, chunks, (int)dim);
@@ -623,106 +627,104 @@ __global__ __launch_bounds__(256) void k_embed_sum(const uint2* __restrict__ pai
             }
         }
         flush(cur == next);
+        if (c == 0) ends[id] = cur != next || cur >= (uint32_t)vocab ? kChunkNone : head ? kChunkWhole : cur;
     };
     if (dim < V) walk(std::integral_constant<int, 4>(), std::false_type());
     else if (stream) walk(std::integral_constant<int, 8>(), std::true_type());
     else walk(std::integral_constant<int, 8>(), std::false_type());
 }
 
-// Runs that cross chunk borders: the partial row of the chunk where the run
-// begins plus row 0 of each chunk it goes on in.  A block takes kJoinChunks
-// chunks and 64 columns: a wave sums a short run, the whole block a long one,
-// joined in a fixed order.  Bound by its chain of loads that wait for one
-// another.
-constexpr int kJoinThreads = 256;
-constexpr int kJoinChunks = kJoinThreads / 64;
-constexpr int kJoinLong = 32;
+// Runs that cross chunk borders: the partial row 1 of the chunk where the run
+// begins plus row 0 of each chunk it goes on in.  A block takes `own` chunks (up
+// to 64, which it sees) and 64 columns: the lanes of a partial row's columns sum a short run, the whole block
+// a long one, joined in a fixed order.  Bound by its chain of loads that wait for
+// one another: 5.5 us for 626 chunks, 8.5 for 57,344.  (A wave a chunk that looks
+// for its run among the keys took 5.3 and 19.)
+constexpr int kJoinChunks = 64;
+constexpr int kJoinLong = 16;
 
 template <typename U>
-__global__ __launch_bounds__(kJoinThreads) void k_embed_join(const uint2* __restrict__ pairs, int64_t n, int64_t dim,
-                                                             int64_t vocab, float scale, U* __restrict__ out,
-                                                             int64_t out_stride, const float* __restrict__ part,
-                                                             int64_t part_stride, int chunk, int64_t chunks, int log_cols)
+__global__ __launch_bounds__(256) void k_embed_join(const uint32_t* __restrict__ ends, int dim, float scale,
+                                                    U* __restrict__ out, int64_t out_stride, const float* __restrict__ part,
+                                                    int64_t part_stride, int chunks, int own, int log_cols)
 {
-    __shared__ int64_t last[kJoinChunks];   // the run's last chunk; -1: no run to join here
+    __shared__ int first[kJoinChunks], last[kJoinChunks], count;   // of the runs that begin here
     __shared__ uint32_t key[kJoinChunks];
-    __shared__ float4 sums[kJoinChunks][16];
+    __shared__ float4 sums[4][16];
     const int w = threadIdx.x >> 6, lane = threadIdx.x & 63;
-    const int64_t id = (int64_t)blockIdx.x * kJoinChunks + w;
-    // each wave looks for the run of its chunk, 64 chunks at a glance
-    {
-        int64_t e = -1;
-        uint32_t k = 0;
-        if (id + 1 < chunks) {
-            const int64_t begin = id * chunk, end = begin + chunk;
-            const uint32_t front = pairs[begin].x, after = pairs[end].x, prev = begin > 0 ? pairs[begin - 1].x : ~0u;
-            const int64_t glance = id + 2 + lane;   // does not wait for the key
-            uint32_t seen = glance < chunks ? pairs[glance * chunk].x : ~0u;
-            k = pairs[end - 1].x;
-            const bool whole = front == k && prev == k;   // the run began before this chunk
-            if (after == k && !whole && k < (uint32_t)vocab) {
-                e = id + 1;   // a chunk that begins with the run
-                uint64_t other = ~__ballot(seen == k);
-                while (other == 0) {
-                    e += 64;
-                    const int64_t at = e + 1 + lane;
-                    seen = at < chunks ? pairs[at * chunk].x : ~0u;
-                    other = ~__ballot(seen == k);
-                }
-                e += __ffsll((unsigned long long)other) - 1;
+    if (w == 0) {
+        const int base = blockIdx.x * own, id = base + lane;
+        const uint32_t e = id < chunks ? ends[id] : kChunkNone;
+        const bool begins = e < kChunkWhole && lane < own;
+        const uint64_t begin = __ballot(begins), whole = __ballot(e == kChunkWhole);
+        // a run ends in the first chunk after it that is not whole
+        const uint64_t after = lane < 63 ? whole >> (lane + 1) : 0;
+        const int len = __ffsll((unsigned long long)~after) - 1;   // whole chunks that follow
+        int more = 0;
+        if (__any(begins && lane + len == 63)) {   // beyond what the block sees, 256 at a glance
+            for (int n = 256; n == 256; more += n) {
+                const int at = base + kJoinChunks + more + lane * 4;
+                n = 0;
+#pragma unroll
+                for (int k = 0; k < 4; ++k) n += n == k && at + k < chunks && ends[at + k] == kChunkWhole;
+                const uint64_t part_full = ~__ballot(n == 4);
+                const int full = part_full ? __ffsll((unsigned long long)part_full) - 1 : 64;   // lanes before the first with another
+                n = full == 64 ? 256 : full * 4 + __shfl(n, full, 64);
             }
         }
-        if (lane == 0) {
-            last[w] = e;
-            key[w] = k;
+        if (begins) {
+            const int at = __builtin_amdgcn_mbcnt_hi((uint32_t)(begin >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)begin, 0));
+            first[at] = id;
+            last[at] = id + len + 1 + (lane + len == 63 ? more : 0);
+            key[at] = e;
         }
+        if (lane == 0) count = __popcll(begin);
     }
     __syncthreads();
-    // 2^log_cols lanes hold a row's columns, four each; the others take further rows
-    const int cols = 1 << log_cols, row = lane >> log_cols, rows = 64 >> log_cols;
-    const int64_t c = (int64_t)blockIdx.y * 64 + (lane & (cols - 1)) * 4;
+    // 2^log_cols lanes hold a row's columns, four each
+    const int cols = 1 << log_cols, group = threadIdx.x >> log_cols, groups = 256 >> log_cols;
+    const int c = blockIdx.y * 64 + (lane & (cols - 1)) * 4;
     const bool in = c < dim;   // part rows are padded to four floats
-    auto sum = [&](int64_t first, int64_t e, int from, int step) {
+    auto sum = [&](int from, int to, int step, int begin) {
         float4 a = make_float4(0, 0, 0, 0);
         if (in)
 #pragma unroll 8
-            for (int64_t k = first + from; k <= e; k += step) {
-                const float4 v = *(const float4*)(part + (k * 2 + (k == first ? 1 : 0)) * part_stride + c);
+            for (int k = from; k <= to; k += step) {
+                const float4 v = *(const float4*)(part + ((int64_t)k * 2 + (k == begin ? 1 : 0)) * part_stride + c);
                 a.x += v.x;
                 a.y += v.y;
                 a.z += v.z;
                 a.w += v.w;
             }
+        return a;
+    };
+    auto store = [&](const float4& a, uint32_t k) {
+        const float r[4] = {a.x * scale, a.y * scale, a.z * scale, a.w * scale};
+        if (in) store_vals<4>(r, out + (int64_t)k * out_stride + c, dim - c);
+    };
+    for (int i = group; i < count; i += groups)
+        if (last[i] - first[i] <= kJoinLong) store(sum(first[i], last[i], 1, first[i]), key[i]);
+    for (int i = 0; i < count; ++i) {
+        if (last[i] - first[i] <= kJoinLong) continue;
+        float4 a = sum(first[i] + group, last[i], groups, first[i]);
         for (int d = cols; d < 64; d *= 2) {
             a.x += __shfl_xor(a.x, d, 64);
             a.y += __shfl_xor(a.y, d, 64);
             a.z += __shfl_xor(a.z, d, 64);
             a.w += __shfl_xor(a.w, d, 64);
         }
-        return a;
-    };
-    auto store = [&](const float4& a, uint32_t k) {
-        const float r[4] = {a.x * scale, a.y * scale, a.z * scale, a.w * scale};
-        if (lane < cols && in) store_vals<4>(r, out + (int64_t)k * out_stride + c, dim - c);
-    };
-    if (last[w] >= 0 && last[w] - id <= kJoinLong) store(sum(id, last[w], row, rows), key[w]);
-    for (int s = 0; s < kJoinChunks; ++s) {
-        const int64_t first = (int64_t)blockIdx.x * kJoinChunks + s;
-        if (last[s] - first <= kJoinLong) continue;
-        const float4 a = sum(first, last[s], w * rows + row, kJoinChunks * rows);
         __syncthreads();
         if (lane < cols) sums[w][lane] = a;
         __syncthreads();
-        if (w == 0) {
-            float4 t = make_float4(0, 0, 0, 0);
-            for (int k = 0; k < kJoinChunks; ++k) {
-                const float4 v = sums[k][lane & (cols - 1)];
-                t.x += v.x;
-                t.y += v.y;
-                t.z += v.z;
-                t.w += v.w;
+        if ((int)threadIdx.x < cols) {
+            float4 t = sums[0][lane];
+            for (int k = 1; k < 4; ++k) {
+                t.x += sums[k][lane].x;
+                t.y += sums[k][lane].y;
+                t.z += sums[k][lane].z;
+                t.w += sums[k][lane].w;
             }
-            store(t, key[s]);
+            store(t, key[i]);
         }
     }
 }

@@ -117,18 +117,20 @@ inline RowMap plan_rows(int64_t dim, int V)
 inline int64_t row_blocks(const RowMap& m, int64_t rows) { return m.slices > 1 ? rows * m.slices : vec_ceil(rows, m.per); }
 
 // The embedding's gradient: the sort, then chunks of sorted positions.
-// Workspace: counts | pairs A | pairs B | partial sums (two rows a chunk).
+// Workspace: counts | pairs A | pairs B | partial sums (two rows a chunk) |
+// how each chunk ends.
 struct EmbedPlan {
     SortPlan sort;
     int chunk = 1;             // sorted positions a group of lanes sums
     int64_t chunks = 0;
     int64_t part_stride = 0;   // floats of a partial row
-    int64_t off_a = 0, off_b = 0, off_part = 0, bytes = 0;
+    int64_t off_a = 0, off_b = 0, off_part = 0, off_ends = 0, bytes = 0;
 };
 
 constexpr int kEmbedChunk = 256;         // largest chunk
 constexpr int kEmbedFew = 32;
-constexpr int64_t kEmbedWaves = 2048;    // chunks are halved until this many waves run (8 a CU), below 16 a quarter
+constexpr int64_t kEmbedWaves = 8192;    // chunks are halved until this many waves run (32 a CU), below
+                                        // 32 tokens a quarter, below 16 a sixteenth
 
 inline EmbedPlan plan_embed(int64_t n, int64_t vocab, int64_t dim)
 {
@@ -143,15 +145,17 @@ inline EmbedPlan plan_embed(int64_t n, int64_t vocab, int64_t dim)
         while (p.chunk > least && vec_ceil(n, p.chunk) * vecs / 64 < waves) p.chunk /= 2;
     };
     if (n > kEmbedFew) {
-        fewer(16, kEmbedWaves);
-        fewer(8, kEmbedWaves / 4);
+        fewer(32, kEmbedWaves);
+        fewer(16, kEmbedWaves / 4);
+        fewer(8, kEmbedWaves / 16);
     }
     p.chunks = vec_ceil(n, p.chunk);
     p.part_stride = vec_up(dim, 4);
     p.off_a = p.sort.count ? vec_up((int64_t)p.sort.blocks * p.sort.row * 4, 256) : 0;
     p.off_b = p.off_a + vec_up(n * 8, 256);
     p.off_part = p.off_b + (p.sort.small ? 0 : vec_up(n * 8, 256));
-    p.bytes = p.off_part + vec_up(p.chunks * 2 * p.part_stride * 4, 256);
+    p.off_ends = p.off_part + vec_up(p.chunks * 2 * p.part_stride * 4, 256);
+    p.bytes = p.off_ends + vec_up(p.chunks * 4, 256);
     return p;
 }
 

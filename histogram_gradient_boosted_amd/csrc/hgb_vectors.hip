@@ -346,16 +346,19 @@ hgb_status hgb_embed_backward(hgb_ctx* c, const void* grad, int32_t grad_type, i
             using U = std::remove_pointer_t<decltype(u)>;
             using T = std::remove_pointer_t<decltype(t)>;
             float* part = (float*)(ws + p.off_part);
+            uint32_t* ends = (uint32_t*)(ws + p.off_ends);
             const RowMap m = plan_rows(dim, kVals<T, U>);
             k_embed_sum<T, U><<<(unsigned)row_blocks(m, p.chunks), 256, 0, c->stream>>>(
-                pairs, n_tokens, (const T*)grad, grad_stride, dim, vocab, scale, (U*)out, out_stride, part, p.part_stride, p.chunk,
-                p.chunks, m, z.stream);
+                pairs, n_tokens, (const T*)grad, grad_stride, dim, vocab, scale, (U*)out, out_stride, part, p.part_stride, ends,
+                p.chunk, p.chunks, m, z.stream);
             HGB_LAUNCHED(c, "k_embed_sum");
             if (p.chunks > 1) {
-                const dim3 jgrid((unsigned)vec_ceil(p.chunks, kJoinChunks), (unsigned)vec_ceil(dim, 64));
-                k_embed_join<U><<<jgrid, kJoinThreads, 0, c->stream>>>(pairs, n_tokens, dim, vocab, scale, (U*)out, out_stride, part,
-                                                                       p.part_stride, p.chunk, p.chunks,
-                                                                       log2_of(std::min(16, vec_pow2(vec_ceil(dim, 4)))));
+                // two blocks a CU before a block takes more chunks
+                const int64_t slices = vec_ceil(dim, 64);
+                const int own = vec_pow2(std::min<int64_t>(kJoinChunks, std::max<int64_t>(4, p.chunks * slices / (2 * c->n_cu))));
+                k_embed_join<U><<<dim3((unsigned)vec_ceil(p.chunks, own), (unsigned)slices), 256, 0, c->stream>>>(
+                    ends, (int)dim, scale, (U*)out, out_stride, part, p.part_stride, (int)p.chunks, own,
+                    log2_of(std::min(16, vec_pow2(vec_ceil(dim, 4)))));
                 HGB_LAUNCHED(c, "k_embed_join");
             }
             return HGB_OK;
