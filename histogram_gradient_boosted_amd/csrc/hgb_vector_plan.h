@@ -48,7 +48,8 @@ constexpr int kSortMaxBlocks = 512;
 struct SortPlan {
     int64_t n = 0;
     int passes = 0;
-    int bits = 0;        // of every digit
+    int key_bits = 0;    // of a key
+    int bits = 0;        // of every digit (the last may have fewer: pass())
     int radix = 0;       // digits' values: 2^bits
     int row = 4;         // words of a share's counts: the radix, at least a 16-byte load
     bool small = false;
@@ -56,6 +57,19 @@ struct SortPlan {
     int items = 1;       // keys a thread holds of a tile: 1, 4 or kSortItems
     int blocks = 1;
     int tiles = 1;
+
+    void digits(int b)
+    {
+        bits = b;
+        radix = 1 << b;
+        row = std::max(radix, 4);
+    }
+    SortPlan pass(int k) const   // as pass k takes it, whose digits begin at bit k * bits
+    {
+        SortPlan p = *this;
+        p.digits(std::min(bits, key_bits - k * bits));
+        return p;
+    }
 };
 
 inline SortPlan plan_sort(int64_t n, int64_t limit, bool one_pass)
@@ -73,12 +87,10 @@ inline SortPlan plan_sort(int64_t n, int64_t limit, bool one_pass)
         p.blocks = (int)vec_ceil(tiles, p.tiles);
         p.count = p.blocks > kSortSelf;
     }
-    const int bits = vec_bits(limit);
+    p.key_bits = vec_bits(limit);
     const int most = one_pass || p.blocks <= kSortFew ? kSortBits : kSortManyBits;
-    p.passes = (int)vec_ceil(bits, most);
-    p.bits = (int)vec_ceil(bits, p.passes);
-    p.radix = 1 << p.bits;
-    p.row = std::max(p.radix, 4);
+    p.passes = (int)vec_ceil(p.key_bits, most);
+    p.digits((int)vec_ceil(p.key_bits, p.passes));
     return p;
 }
 

@@ -250,10 +250,10 @@ hgb_status launch_sort(hgb_ctx* c, SortIn in, SortOut out, const SortPlan& p, co
         const ZeroFill one = part(launch), two = p.count ? part(launch + 1) : one;
         if (a) out.to = pass & 1 ? b : a;
         if (pass == 0) {
-            HGB_TRY(launch_pass<true>(c, in, out, p, shift, counts, one, two));
+            HGB_TRY(launch_pass<true>(c, in, out, p.pass(pass), shift, counts, one, two));
         } else {
             in.from = pass & 1 ? a : b;
-            HGB_TRY(launch_pass<false>(c, in, out, p, shift, counts, one, two));
+            HGB_TRY(launch_pass<false>(c, in, out, p.pass(pass), shift, counts, one, two));
         }
     }
     if (sorted) *sorted = out.to;

@@ -37,6 +37,14 @@ static void plans()
                 CHECK((int64_t)p.bits * p.passes >= vec_bits(limit) && p.bits <= kSortBits);
                 CHECK(p.radix == 1 << p.bits && p.radix <= kSortThreads);
                 CHECK(p.small == (n <= kSortSmall));
+                int bits = 0;
+                for (int k = 0; k < p.passes; ++k) {
+                    const SortPlan q = p.pass(k);
+                    CHECK(q.bits >= 1 && q.bits <= p.bits && q.radix == 1 << q.bits && q.row >= q.radix && q.row <= p.row);
+                    CHECK(k * p.bits == bits);   // its digits begin where the last one's end
+                    bits += q.bits;
+                }
+                CHECK(bits == vec_bits(limit));
                 CHECK(p.items == 1 || p.items == 4 || p.items == kSortItems);
                 const int64_t tile = (int64_t)p.items * kSortThreads;
                 // the blocks' shares cover every key, and none starts past the last
