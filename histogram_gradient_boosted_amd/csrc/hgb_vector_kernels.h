@@ -853,6 +853,16 @@ __device__ inline void load_param(float (&r)[V], const void* p, int type, int64_
     }
 }
 
+// V values of a parameter's gradient.
+template <int V, bool WHOLE>
+__device__ inline void store_param(const float (&r)[V], void* p, int type, int64_t c, int64_t left)
+{
+    if (!p) return;
+    if (type == 0) store_vals<V, WHOLE>(r, (float*)p + c, left);
+    else if (type == 1) store_vals<V, WHOLE>(r, (__bf16*)p + c, left);
+    else store_vals<V, WHOLE>(r, (_Float16*)p + c, left);
+}
+
 // mean = sum x / dim, rstd = 1 / sqrt(sum (x - mean)^2 / dim + eps), y = (x -
 // mean) rstd weight + bias.  Bound by bytes: the row stays in registers between
 // its three uses, so x is read once, and the parameters stay there from row to
@@ -925,7 +935,8 @@ __global__ __launch_bounds__(norm_threads(WPR)) void k_norm(
 // dx by rows, and the parameters' gradients over the block's rows in the same
 // pass: a lane keeps the sums of its columns in registers, the block's waves
 // join theirs through LDS at the end (a fixed tree), and part
-// [blocks][2][dim] holds the blocks' sums for k_norm_join.  Bound by bytes,
+// [blocks][2][dim] holds the blocks' sums for k_norm_join.  A block alone stores
+// the gradients itself.  Bound by bytes,
 // each read and written once.  32,768 rows of 1,792 bf16 values: 74 us, 4.8
 // TB/s, and 5 us for k_norm_join.  On the way: 298 us as passes of their own
 // for dx and for the sums, 120 in one pass, 94 with the next row ahead but both
@@ -934,7 +945,8 @@ template <typename T, int NV, int WPR, int TAIL>
 __global__ __launch_bounds__(norm_grad_threads(NV, WPR)) void k_norm_grad(
     const T* __restrict__ grad, int64_t grad_stride, const T* __restrict__ x, int64_t x_stride, int64_t rows, int dim,
     const float* __restrict__ mean, const float* __restrict__ rstd, const void* __restrict__ weight, int wtype,
-    T* __restrict__ dx, int64_t dx_stride, float* __restrict__ part, int log_group, bool stream)
+    T* __restrict__ dx, int64_t dx_stride, float* __restrict__ part, void* __restrict__ dweight, void* __restrict__ dbias,
+    int log_group, bool stream)
 {
     using S = NormShape<T, NV, WPR>;
     constexpr int V = S::V, K = S::K, THREADS = norm_grad_threads(NV, WPR), WAVES = THREADS / 64;
@@ -1074,6 +1086,11 @@ __global__ __launch_bounds__(norm_grad_threads(NV, WPR)) void k_norm_grad(
 #pragma unroll
     for (int k = 0; k < K; ++k) {
         const NormRun<S, TAIL> run(k, span, lane, dim);
+        if (gridDim.x == 1) {
+            store_param<V, WHOLE>(dw[k], dweight, wtype, run.c, run.left);
+            store_param<V, WHOLE>(db[k], dbias, wtype, run.c, run.left);
+            continue;
+        }
         store_vals<V, WHOLE>(dw[k], to + run.c, run.left);
         store_vals<V, WHOLE>(db[k], to + dim + run.c, run.left);
     }
@@ -1189,7 +1206,7 @@ __global__ __launch_bounds__(256) void k_norm_join(const float* __restrict__ par
 
 // Rows to their slots' places, a vector a thread.  It also zeroes the places of
 // its number range that lie past the last routed slot.  Bound by bytes: 32,768
-// rows of 1,024 bf16 values, four places each, in 62 us, 5.4 TB/s.
+// rows of 1,024 bf16 values, four places each, in 51 us, 6.5 TB/s.
 template <typename T>
 __global__ __launch_bounds__(256) void k_route_gather(const T* __restrict__ x, int64_t x_stride, int64_t rows, int top,
                                                       int dim, const int32_t* __restrict__ position,

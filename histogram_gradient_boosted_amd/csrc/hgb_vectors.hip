@@ -469,14 +469,14 @@ hgb_status hgb_layer_norm_backward(hgb_ctx* c, const void* grad, int64_t grad_st
                     constexpr int NV = decltype(values)::value, WPR = decltype(waves)::value;
                     k_norm_grad<T, NV, WPR, decltype(tail)::value><<<(unsigned)parts, norm_grad_threads(NV, WPR), 0, c->stream>>>(
                         g, grad_stride, (const T*)x, x_stride, n_rows, (int)dim, mean, rstd, weight, param_type, (T*)dx,
-                        dx_stride, params ? (float*)workspace : nullptr, p.log_group,
+                        dx_stride, params ? (float*)workspace : nullptr, dweight, dbias, p.log_group,
                         streams(3 * n_rows * dim * elem_size(type)));
                 });
                 HGB_LAUNCHED(c, "k_norm_grad");
             }
             return HGB_OK;
         }));
-        if (params) {
+        if (params && (parts > 1 || !p.values)) {
             k_norm_join<<<dim3((unsigned)vec_ceil(dim, 16), 2), 256, 0, c->stream>>>((const float*)workspace, parts, dim, dweight,
                                                                                     dbias, param_type);
             HGB_LAUNCHED(c, "k_norm_join");
