@@ -86,28 +86,19 @@ __device__ inline void store_vals(const float (&r)[V], T* p, int64_t left, bool 
 // of its vector (the last vector is moved back to end with the row) and
 // whether it has one.
 struct RowPlace {
-    int64_t r;
+    uint32_t r;
     int c;
     bool in;
 };
 
 template <int V>
-__device__ inline RowPlace row_place(const RowMap& m, int64_t rows, int dim)
+__device__ inline RowPlace row_place(const RowMap& m, uint32_t rows, int dim)
 {
-    const int t = threadIdx.x;
+    const int t = threadIdx.x, q = (t * m.magic) >> 16, j = (int)blockIdx.y * 256 + t - q * m.vecs;
     RowPlace p;
-    int j;
-    if (m.slices > 1) {
-        p.r = blockIdx.x / (uint32_t)m.slices;
-        j = (int)(blockIdx.x % (uint32_t)m.slices) * 256 + t;
-        p.in = j < m.vecs;
-    } else {
-        const int q = (t * m.magic) >> 16;
-        j = t - q * m.vecs;
-        p.r = (int64_t)blockIdx.x * m.per + q;
-        p.in = q < m.per && p.r < rows;
-    }
+    p.r = blockIdx.x * (uint32_t)m.per + (uint32_t)q;
     p.c = dim < V ? 0 : min(j * V, dim - V);
+    p.in = q < m.per && j < m.vecs && p.r < rows;
     return p;
 }
 
@@ -538,7 +529,7 @@ __global__ __launch_bounds__(256) void k_embed(const T* __restrict__ table, int6
     const bool live = t != pad && (uint32_t)t < (uint32_t)vocab;
     if (!live && t != pad && at.c == 0) atomicOr(err, kVecErrToken);
     const T* from = table + (uint64_t)(live ? (uint32_t)t : 0) * (uint64_t)table_stride + at.c;
-    U* to = out + (uint64_t)(uint32_t)at.r * (uint64_t)out_stride + at.c;
+    U* to = out + (uint64_t)at.r * (uint64_t)out_stride + at.c;
     auto copy = [&](auto whole) {
         constexpr bool WHOLE = decltype(whole)::value;
         float v[V];
@@ -573,7 +564,7 @@ __global__ __launch_bounds__(256) void k_embed_sum(const uint2* __restrict__ pai
                                                    int64_t chunks, RowMap m, bool stream)
 {
     constexpr int V = kVals<T, U>;
-    const RowPlace at = row_place<V>(m, chunks, (int)dim);
+    const RowPlace at = row_place<V>(m, (uint32_t)chunks, (int)dim);
     if (!at.in) return;
     const int64_t id = at.r, c = at.c, begin = id * chunk, end = begin + chunk < n ? begin + chunk : n;
     const uint32_t none = 0xffffffffu;
@@ -1214,9 +1205,9 @@ __global__ __launch_bounds__(256) void k_route_gather(const T* __restrict__ x, i
                                                       int64_t out_stride, RowMap m, bool stream)
 {
     constexpr int V = kVals<T>;
-    const RowPlace p = row_place<V>(m, rows, dim);
+    const RowPlace p = row_place<V>(m, (uint32_t)rows, dim);
     if (!p.in) return;
-    const int64_t slots = rows * top, used = *routed, first = p.r * top;
+    const int64_t slots = rows * top, used = *routed, first = (int64_t)p.r * top;
     auto copy = [&](auto whole) {
         constexpr bool WHOLE = decltype(whole)::value;
         const typename Vals<T, V>::type v = load_raw<V, WHOLE>(x + p.r * x_stride + p.c, dim);
@@ -1241,9 +1232,9 @@ __global__ __launch_bounds__(256) void k_route_combine(const T* __restrict__ y, 
                                                        int64_t out_stride, RowMap m, bool stream)
 {
     constexpr int V = kVals<T>, STEP = 4;
-    const RowPlace p = row_place<V>(m, rows, dim);
+    const RowPlace p = row_place<V>(m, (uint32_t)rows, dim);
     if (!p.in) return;
-    const int64_t slots = rows * top, first = p.r * top;
+    const int64_t slots = rows * top, first = (int64_t)p.r * top;
     auto sum = [&](auto whole, auto past) {
         constexpr bool WHOLE = decltype(whole)::value, STREAM = decltype(past)::value;
         float acc[V];

@@ -103,9 +103,10 @@ constexpr int scatter_pair_words(int items) { return items > 1 ? 2 * items * kSo
 constexpr int small_pair_words(const SortPlan& p, int items, int threads) { return p.passes > 1 ? 2 * items * threads : 0; }
 
 // One vector of V values a thread, for rows of `dim`: 256 threads take `per`
-// whole rows where a row has at most 256 vectors, else one of its `slices`
-// (the idle threads are fewer than with groups of 2^k lanes: at most a third,
-// and a tenth for rows of up to 25 vectors, against a half).
+// whole rows where a row has at most 256 vectors, else one of its `slices` (the
+// grid's y: no division, and no branch that would part the kernel's loads of
+// its arguments).  The idle threads are fewer than with groups of 2^k lanes: at
+// most a third, and a tenth for rows of up to 25 vectors, against a half.
 struct RowMap {
     int vecs = 1;
     int per = 1;
@@ -117,16 +118,13 @@ inline RowMap plan_rows(int64_t dim, int V)
 {
     RowMap m;
     m.vecs = (int)vec_ceil(dim, V);
-    if (m.vecs <= 256) {
-        m.per = 256 / m.vecs;
-        m.magic = 65536 / m.vecs + 1;
-    } else {
-        m.slices = (int)vec_ceil(m.vecs, 256);
-    }
+    m.per = std::max(1, 256 / m.vecs);
+    m.slices = (int)vec_ceil(m.vecs, 256);
+    m.magic = m.vecs <= 256 ? 65536 / m.vecs + 1 : 0;
     return m;
 }
 
-inline int64_t row_blocks(const RowMap& m, int64_t rows) { return m.slices > 1 ? rows * m.slices : vec_ceil(rows, m.per); }
+inline int64_t row_blocks(const RowMap& m, int64_t rows) { return vec_ceil(rows, m.per); }
 
 // The embedding's gradient: the sort, then chunks of sorted positions.
 // Workspace: counts | pairs A | pairs B | partial sums (two rows a chunk) |

@@ -165,6 +165,8 @@ void by_shape(const NormPlan& p, int64_t dim, int V, F&& f)
 // of 32,768 rows of 1,024, four experts each, 116 and 158.
 bool streams(int64_t bytes) { return bytes >= (int64_t)192 << 20; }
 
+dim3 row_grid(const RowMap& m, int64_t rows) { return dim3((unsigned)row_blocks(m, rows), (unsigned)m.slices); }
+
 int log2_of(int p) { return 31 - __builtin_clz((unsigned)p); }
 
 hgb_status raise_lds(hgb_ctx* c, const void* fn, size_t bytes)
@@ -287,7 +289,7 @@ hgb_status hgb_embed(hgb_ctx* c, const void* table, int32_t table_type, int64_t 
             using U = std::remove_pointer_t<decltype(u)>;
             const RowMap m = plan_rows(dim, kVals<T, U>);
             const int64_t bytes = dim * (n_tokens * (int64_t)sizeof(U) + std::min(n_tokens, vocab) * (int64_t)sizeof(T));
-            k_embed<T, U><<<(unsigned)row_blocks(m, n_tokens), 256, 0, c->stream>>>(
+            k_embed<T, U><<<row_grid(m, n_tokens), 256, 0, c->stream>>>(
                 (const T*)table, table_stride, (int)vocab, (int)dim, tokens, (int)n_tokens, pad, scale, (U*)out, out_stride, m,
                 streams(bytes), c->dev_words + kWordVectors);
             HGB_LAUNCHED(c, "k_embed");
@@ -348,7 +350,7 @@ hgb_status hgb_embed_backward(hgb_ctx* c, const void* grad, int32_t grad_type, i
             float* part = (float*)(ws + p.off_part);
             uint32_t* ends = (uint32_t*)(ws + p.off_ends);
             const RowMap m = plan_rows(dim, kVals<T, U>);
-            k_embed_sum<T, U><<<(unsigned)row_blocks(m, p.chunks), 256, 0, c->stream>>>(
+            k_embed_sum<T, U><<<row_grid(m, p.chunks), 256, 0, c->stream>>>(
                 pairs, n_tokens, (const T*)grad, grad_stride, dim, vocab, scale, (U*)out, out_stride, part, p.part_stride, ends,
                 p.chunk, p.chunks, m, z.stream);
             HGB_LAUNCHED(c, "k_embed_sum");
@@ -555,7 +557,7 @@ hgb_status hgb_route_gather(hgb_ctx* c, const void* x, int32_t type, int64_t x_s
         return by_type(type, [&](auto* t) -> hgb_status {
             using T = std::remove_pointer_t<decltype(t)>;
             const RowMap m = plan_rows(dim, kVals<T>);
-            k_route_gather<T><<<(unsigned)row_blocks(m, n_rows), 256, 0, c->stream>>>(
+            k_route_gather<T><<<row_grid(m, n_rows), 256, 0, c->stream>>>(
                 (const T*)x, x_stride, n_rows, top, (int)dim, position, offsets + n_experts, (T*)out, out_stride, m,
                 streams(n_rows * (top + 1) * dim * elem_size(type)));
             HGB_LAUNCHED(c, "k_route_gather");
@@ -581,7 +583,7 @@ static hgb_status combine(hgb_ctx* c, const char* verb, const void* y, int32_t t
     return by_type(type, [&](auto* t) -> hgb_status {
         using T = std::remove_pointer_t<decltype(t)>;
         const RowMap m = plan_rows(dim, kVals<T>);
-        k_route_combine<T><<<(unsigned)row_blocks(m, n_rows), 256, 0, c->stream>>>(
+        k_route_combine<T><<<row_grid(m, n_rows), 256, 0, c->stream>>>(
             (const T*)y, y_stride, n_rows, top, (int)dim, position, weight, (T*)out, out_stride, m,
             streams(n_rows * (top + 1) * dim * elem_size(type)));
         HGB_LAUNCHED(c, "k_route_combine");
