@@ -383,12 +383,12 @@ __global__ __launch_bounds__(kSortThreads) void k_sort_count(SortIn in, SortPlan
 // shares' counts, at most kSortMaxBlocks rows of them and read from L2, or by
 // counting all keys itself) instead of a scan in a launch of its own, then
 // ranks its tiles in order.  Blocks past p.blocks write the zeros.  3,670,016
-// keys by 128 digits: 28 us, of which 5 for the counts, 6 for the ranks, 4 to
+// keys by 128 digits: 27 us, of which 5 for the counts, 6 for the ranks, 4 to
 // pass through LDS and out (38 us with the pairs stored from their lanes and
 // the counts read a word at a time).
 template <bool FIRST, int ITEMS>
 __global__ __launch_bounds__(kSortThreads, 8) void k_sort_scatter(SortIn in, SortOut out, SortPlan p, int shift,
-                                                               const uint32_t* counts, ZeroFill z)
+                                                                  const uint32_t* counts, ZeroFill z)
 {
     if ((int)blockIdx.x >= p.blocks) {
         zero_fill(z, blockIdx.x - p.blocks, gridDim.x - p.blocks);
