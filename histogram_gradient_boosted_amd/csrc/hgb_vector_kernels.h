@@ -600,7 +600,8 @@ __global__ __launch_bounds__(256) void k_embed_sum(const uint2* __restrict__ pai
             // a dropped token's row is not read: its sum, which no one stores, takes row 0
 #pragma unroll
             for (int u = 0; u < STEP; ++u)
-                v[u] = load_raw<V, WHOLE, STREAM>(grad + (kv[u].x < (uint32_t)vocab ? (uint64_t)kv[u].y : 0) * (uint64_t)grad_stride + c, dim);
+                v[u] = load_raw<V, WHOLE, STREAM>(
+                    grad + (kv[u].x < (uint32_t)vocab ? (uint64_t)kv[u].y : 0) * (uint64_t)grad_stride + c, dim);
 #pragma unroll
             for (int u = 0; u < STEP; ++u) ahead[u] = pairs[j + STEP + u < end ? j + STEP + u : end - 1];
 #pragma unroll
@@ -627,10 +628,10 @@ __global__ __launch_bounds__(256) void k_embed_sum(const uint2* __restrict__ pai
 
 // Runs that cross chunk borders: the partial row 1 of the chunk where the run
 // begins plus row 0 of each chunk it goes on in.  A block takes `own` chunks (up
-// to 64, which it sees) and 64 columns: the lanes of a partial row's columns sum a short run, the whole block
-// a long one, joined in a fixed order.  Bound by its chain of loads that wait for
-// one another: 5.5 us for 626 chunks, 8.5 for 57,344.  (A wave a chunk that looks
-// for its run among the keys took 5.3 and 19.)
+// to 64, which it sees) and 64 columns: the lanes of a partial row's columns sum
+// a short run, the whole block a long one, joined in a fixed order.  Bound by its
+// chain of loads that wait for one another: 5.5 us for 626 chunks, 8.5 for
+// 57,344.  (A wave a chunk that looks for its run among the keys took 5.3 and 19.)
 constexpr int kJoinChunks = 64;
 constexpr int kJoinLong = 16;
 
