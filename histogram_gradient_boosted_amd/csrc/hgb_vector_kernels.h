@@ -82,6 +82,9 @@ __device__ inline void store_vals(const float (&r)[V], T* p, int64_t left, bool 
     store_raw<V, WHOLE>(v, p, left, stream);
 }
 
+// A block's number in a grid of span_blocks.
+__device__ inline uint32_t block_number() { return (blockIdx.z << kGridLog) + blockIdx.x; }
+
 // A thread's place among rows of `dim` (plan_rows): its row, the first column
 // of its vector (the last vector is moved back to end with the row) and
 // whether it has one.
@@ -96,7 +99,7 @@ __device__ inline RowPlace row_place(const RowMap& m, uint32_t rows, int dim)
 {
     const int t = threadIdx.x, q = (t * m.magic) >> 16, j = (int)blockIdx.y * 256 + t - q * m.vecs;
     RowPlace p;
-    p.r = blockIdx.x * (uint32_t)m.per + (uint32_t)q;
+    p.r = block_number() * (uint32_t)m.per + (uint32_t)q;
     p.c = dim < V ? 0 : min(j * V, dim - V);
     p.in = q < m.per && j < m.vecs && p.r < rows;
     return p;
@@ -1283,7 +1286,7 @@ __global__ __launch_bounds__(256) void k_route_combine_grad(const T* __restrict_
     if (WAVE) log_group = 6;
     const int lane = threadIdx.x & ((1 << log_group) - 1), group = threadIdx.x >> log_group;
     const uint32_t slots = (uint32_t)(rows * top);
-    const uint32_t s = blockIdx.x * (256u >> log_group) + (WAVE ? __builtin_amdgcn_readfirstlane(group) : group);
+    const uint32_t s = block_number() * (256u >> log_group) + (WAVE ? __builtin_amdgcn_readfirstlane(group) : group);
     if (s >= slots) return;
     const uint32_t r = s / (uint32_t)top, used = (uint32_t)*routed, at = (uint32_t)position[s];
     const bool live = at < slots;   // -1 is not

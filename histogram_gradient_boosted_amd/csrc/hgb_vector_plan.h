@@ -126,6 +126,22 @@ inline RowMap plan_rows(int64_t dim, int V)
 
 inline int64_t row_blocks(const RowMap& m, int64_t rows) { return vec_ceil(rows, m.per); }
 
+// A dimension of a grid holds fewer than 2^32 threads.  Blocks of 256 threads
+// beyond kGridBlocks go on in the grid's z: block b is (b % kGridBlocks, b /
+// kGridBlocks), and a part-filled last layer's blocks find no work.
+constexpr int kGridLog = 23;
+constexpr int64_t kGridBlocks = (int64_t)1 << kGridLog;
+struct GridSpan {
+    unsigned x = 1, z = 1;
+};
+inline GridSpan span_blocks(int64_t blocks)
+{
+    GridSpan g;
+    g.x = (unsigned)std::min(blocks, kGridBlocks);
+    g.z = (unsigned)vec_ceil(blocks, kGridBlocks);
+    return g;
+}
+
 // The embedding's gradient: the sort, then chunks of sorted positions.
 // Workspace: counts | pairs A | pairs B | partial sums (two rows a chunk) |
 // how each chunk ends.

@@ -165,7 +165,11 @@ void by_shape(const NormPlan& p, int64_t dim, int V, F&& f)
 // of 32,768 rows of 1,024, four experts each, 116 and 158.
 bool streams(int64_t bytes) { return bytes >= (int64_t)192 << 20; }
 
-dim3 row_grid(const RowMap& m, int64_t rows) { return dim3((unsigned)row_blocks(m, rows), (unsigned)m.slices); }
+dim3 row_grid(const RowMap& m, int64_t rows)
+{
+    const GridSpan g = span_blocks(row_blocks(m, rows));
+    return dim3(g.x, (unsigned)m.slices, g.z);
+}
 
 int log2_of(int p) { return 31 - __builtin_clz((unsigned)p); }
 
@@ -635,7 +639,8 @@ hgb_status hgb_route_combine_backward(hgb_ctx* c, const void* grad, int32_t type
             const int lg = log2_of(vec_pow2(std::min<int64_t>(vecs, 64)));
             const bool stream = streams(n_rows * ((dweight ? 2 : 1) * top + 1) * dim * elem_size(type));
             auto* kernel = lg == 6 ? k_route_combine_grad<T, true> : k_route_combine_grad<T, false>;
-            kernel<<<(unsigned)vec_ceil(slots, 256 >> lg), 256, 0, c->stream>>>(
+            const GridSpan blocks = span_blocks(vec_ceil(slots, 256 >> lg));
+            kernel<<<dim3(blocks.x, 1, blocks.z), 256, 0, c->stream>>>(
                 (const T*)grad, grad_stride, (const T*)y, y_stride, n_rows, top, (int)dim, position, offsets + n_experts, weight,
                 (T*)dy, dy_stride, dweight, lg, stream);
             HGB_LAUNCHED(c, "k_route_combine_grad");

@@ -1,0 +1,134 @@
+// What the vector verbs ask of the runtime, on the host alone: the runtime's
+// launch functions are this program's, which hold every launch to the limits of
+// a launch and run nothing.  No buffer is touched: addresses are made up.
+// Usage: vector_launch_test grids
+#include "hgb_ctx.h"
+#include "hgb_vector_plan.h"
+
+#include <cstdint>
+#include <cstdio>
+#include <cstring>
+
+using namespace hgb;
+
+static int failures = 0, checks = 0, launches = 0;
+static char what[200];
+
+#define CHECK(cond, ...)                                  \
+    do {                                                  \
+        ++checks;                                         \
+        if (!(cond) && ++failures <= 20) {                \
+            std::printf("%s: %s: ", what, #cond);         \
+            std::printf(__VA_ARGS__);                     \
+            std::printf("\n");                            \
+        }                                                 \
+    } while (0)
+
+extern "C" {
+
+hipError_t hipSetDevice(int) { return hipSuccess; }
+hipError_t hipGetLastError(void) { return hipSuccess; }
+hipError_t hipFuncSetAttribute(const void*, hipFuncAttribute, int) { return hipSuccess; }
+
+// <<<grid, block, lds, stream>>>
+struct Shape {
+    dim3 grid, block;
+    size_t lds;
+    hipStream_t stream;
+} shape;
+
+hipError_t __hipPushCallConfiguration(dim3 grid, dim3 block, size_t lds, hipStream_t stream)
+{
+    shape = {grid, block, lds, stream};
+    return hipSuccess;
+}
+
+hipError_t __hipPopCallConfiguration(dim3* grid, dim3* block, size_t* lds, hipStream_t* stream)
+{
+    *grid = shape.grid;
+    *block = shape.block;
+    *lds = shape.lds;
+    *stream = shape.stream;
+    return hipSuccess;
+}
+
+hipError_t hipLaunchKernel(const void*, dim3 grid, dim3 block, void**, size_t, hipStream_t)
+{
+    ++launches;
+    const uint64_t most = (uint64_t)1 << 32;
+    CHECK(grid.x > 0 && grid.y > 0 && grid.z > 0, "%u x %u x %u blocks", grid.x, grid.y, grid.z);
+    CHECK(block.x * block.y * block.z <= 1024, "%u threads", block.x * block.y * block.z);
+    CHECK((uint64_t)grid.x * block.x < most, "%u blocks of %u in x", grid.x, block.x);
+    CHECK((uint64_t)grid.y * block.y < 65536, "%u blocks in y", grid.y);
+    CHECK((uint64_t)grid.z * block.z < 65536, "%u blocks in z", grid.z);
+    return hipSuccess;
+}
+
+}  // extern "C"
+
+static char* at(int k) { return (char*)((uint64_t)(k + 1) << 57); }
+
+// every verb at every size that its checks accept
+static void grids()
+{
+    hgb_ctx c;   // no device behind it
+    c.dev_words = (uint32_t*)4096;
+    float* mean = (float*)at(10);
+    int32_t *tok = (int32_t*)at(11), *pos = (int32_t*)at(12), *off = (int32_t*)at(13);
+    void *ws = at(14), *a = at(1), *b = at(3), *d = at(5);
+    float *w = (float*)at(15), *dw = (float*)at(16);
+    const int64_t ns[] = {0, 1, 7, 4097, 1000000, 16777215, 16777216, 33554433, 67108864, 268435456, 1073741824, 2147483647};
+    const int64_t dims[] = {1, 3, 8, 33, 64, 129, 257, 513, 1024, 1025, 1040, 2049, 5001, 16385, 1 << 20};
+    auto ok = [&](hgb_status s) { CHECK(s == HGB_OK, "status %d, %s", s, c.err.c_str()); };
+    for (int32_t type : {HGB_F32, HGB_BF16})
+        for (int64_t dim : dims)
+            for (int64_t n : ns) {
+                std::snprintf(what, sizeof what, "type %d, %lld rows of %lld", type, (long long)n, (long long)dim);
+                ok(hgb_embed(&c, a, type, dim, 1000, dim, tok, n, -1, 1, b, type, dim));
+                ok(hgb_embed_backward(&c, a, type, dim, n, dim, tok, -1, 1, 1000, b, type, dim, ws, (int64_t)1 << 56));
+                if (n > 0)
+                    ok(hgb_embed_backward(&c, a, type, dim, 1000, dim, tok, -1, 1, std::min(n, kVecMaxVocab), b, type, dim, ws,
+                                          (int64_t)1 << 56));
+                ok(hgb_layer_norm(&c, a, type, dim, n, dim, w, dw, HGB_F32, 1e-5f, b, dim, mean, (float*)tok));
+                ok(hgb_layer_norm_backward(&c, a, dim, b, dim, type, n, dim, mean, (float*)tok, w, HGB_F32, d, dim, dw, (float*)pos,
+                                           ws, (int64_t)1 << 56));
+                for (int32_t top : {1, 2, 7, 64}) {
+                    const int64_t rows = n / top;
+                    ok(hgb_route(&c, tok, rows, top, 700, (int32_t*)b, pos, off, ws, (int64_t)1 << 56));
+                    ok(hgb_route_gather(&c, a, type, dim, rows, top, dim, pos, off, 700, b, dim));
+                    ok(hgb_route_gather_backward(&c, a, type, dim, rows, top, dim, pos, b, dim));
+                    ok(hgb_route_combine(&c, a, type, dim, rows, top, dim, pos, w, b, dim));
+                    ok(hgb_route_combine_backward(&c, a, type, dim, b, dim, rows, top, dim, pos, off, 700, w, d, dim, dw));
+                }
+            }
+}
+
+// the blocks' numbers cover the work, and a number times what a block takes stays below 2^32
+static void spans()
+{
+    const int64_t ns[] = {1, 255, 256, 16777216, 16777217, 67108865, 1073741823, 2147483646, 2147483647};
+    auto check = [&](int64_t blocks, int64_t each) {
+        std::snprintf(what, sizeof what, "%lld blocks of %lld", (long long)blocks, (long long)each);
+        const GridSpan g = span_blocks(blocks);
+        CHECK((int64_t)g.x * 256 < (int64_t)1 << 32 && g.z < 65536, "%u x %u", g.x, g.z);
+        CHECK(g.z == 1 ? g.x == blocks : g.x == kGridBlocks, "%u x %u", g.x, g.z);
+        CHECK((int64_t)g.x * g.z >= blocks && (int64_t)g.x * (g.z - 1) < blocks, "%u x %u", g.x, g.z);
+        CHECK(((int64_t)g.x * g.z - 1) * each + each - 1 < (int64_t)1 << 32, "%u x %u", g.x, g.z);
+    };
+    for (int64_t n : ns) {
+        for (int V : {4, 8})
+            for (int64_t dim = 1; dim < 3000; ++dim) check(row_blocks(plan_rows(dim, V), n), plan_rows(dim, V).per);
+        for (int lg = 0; lg <= 6; ++lg) check(vec_ceil(n, 256 >> lg), 256 >> lg);   // slots by groups of lanes
+    }
+}
+
+int main(int argc, char** argv)
+{
+    if (argc > 1 && !std::strcmp(argv[1], "grids")) {
+        spans();
+        grids();
+    }
+    CHECK(launches > 0, "nothing was launched");
+    std::printf(failures ? "%d of %d checks failed\n" : "%d of %d failed: all checks passed\n", failures, checks);
+    return failures != 0;
+}
