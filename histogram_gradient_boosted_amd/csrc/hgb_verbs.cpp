@@ -97,6 +97,8 @@ const Tensor& tensor(const Call& c, PyObject* o, const char* name)
 {
     if (THPVariable_Check(o)) {
         const Tensor& t = THPVariable_Unpack(o);
+        // what lies in memory is not what such a view holds
+        if (t.is_neg()) throw Refused("%s is a negated view: give its resolve_neg()", name);
         if (t.is_cuda() && t.get_device() == c.device) return t;
     }
     throw Refused("%s must be a CUDA tensor on device %d", name, c.device);

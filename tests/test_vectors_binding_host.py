@@ -1,0 +1,36 @@
+"""What the binding of the vector verbs refuses before any device call, on host
+tensors: these checks come before the one for the device."""
+import pytest
+import torch
+
+from histogram_gradient_boosted_amd import binding
+
+
+@pytest.fixture()
+def ctx():
+    c = binding.Context.__new__(binding.Context)   # no device: only the checks run
+    c._torch, c._lib, c.device = torch, binding.load(), 0
+    return c
+
+
+def calls(ctx, x):
+    """Every verb, given x ([4, 8]) as its vectors."""
+    i = torch.zeros(4, 2, dtype=torch.int32)
+    r = binding.Route(i.reshape(-1), i, torch.zeros(4, dtype=torch.int32))
+    return (lambda: ctx.embed(x, i), lambda: ctx.embed_backward(x, i[:, 0], 5), lambda: ctx.layer_norm(x),
+            lambda: ctx.layer_norm_backward(x, x, x[:, 0], x[:, 0]), lambda: ctx.route_gather(x, r),
+            lambda: ctx.route_combine(x, r), lambda: ctx.route_gather_backward(x, r),
+            lambda: ctx.route_combine_backward(x, x, r))
+
+
+def test_views_that_torch_would_negate_are_refused(ctx):
+    """conj().imag is a view whose values are those in memory with the other sign."""
+    z = torch.ones(4, 1, dtype=torch.complex64)
+    x = z.conj().imag
+    assert x.is_neg() and float(x[0, 0]) == 0
+    for call in calls(ctx, x):
+        with pytest.raises(ValueError, match="resolve_neg"):
+            call()
+    for call in calls(ctx, x.resolve_neg()):
+        with pytest.raises(ValueError, match="CUDA tensor"):
+            call()
