@@ -503,7 +503,7 @@ class Context:
 
     def layer_norm_backward(self, grad, x, mean, rstd, weight=None, bias: bool = True, out=None):
         """Gradients of layer_norm: (dx, dweight, dbias), dweight None without a
-        weight and dbias None where `bias` is false.  The parameters' gradients
+        weight and dbias None where `bias` (a truth value, not the tensor) is false.  The parameters' gradients
         have the weight's type (float32 without one)."""
         return self._verb("layer_norm_backward", grad, x, mean, rstd, weight, bias, out)
 

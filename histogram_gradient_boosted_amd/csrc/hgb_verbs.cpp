@@ -93,6 +93,17 @@ float real(PyObject* o, const char* name)
     return (float)v;
 }
 
+// A yes or no; a tensor's would be a wait for the device.
+bool truth(PyObject* o, const char* name)
+{
+    const int v = THPVariable_Check(o) ? -1 : PyObject_IsTrue(o);
+    if (v < 0) {
+        PyErr_Clear();
+        throw Refused("%s must be a truth value", name);
+    }
+    return v != 0;
+}
+
 const Tensor& tensor(const Call& c, PyObject* o, const char* name)
 {
     if (THPVariable_Check(o)) {
@@ -323,6 +334,7 @@ PyObject* layer_norm(const Call& c)
 // layer_norm_backward(grad, x, mean, rstd, weight, bias, out)
 PyObject* layer_norm_backward(const Call& c)
 {
+    const bool bias = truth(c.args[5], "bias");
     const Rows grad = rows(c, c.args[0], "grad"), x = rows(c, c.args[1], "x");
     same(x.t.scalar_type(), grad.t.scalar_type(), "x");
     shaped(x, grad.n, grad.dim, "x");
@@ -331,7 +343,6 @@ PyObject* layer_norm_backward(const Call& c)
     if (mean.numel() < x.n || rstd.numel() < x.n)
         throw Refused("mean and rstd must hold %lld values", (long long)x.n);
     const Tensor weight = param(c, c.args[4], "weight", x);
-    const bool bias = PyObject_IsTrue(c.args[5]) == 1;
     Out out(c, c.args[6], x.t.scalar_type(), true, x.n, x.dim);
     const int64_t bytes = weight.defined() || bias ? hgb_layer_norm_backward_workspace(x.n, x.dim) : 0;
     if (bytes < 0) return status(kTooLarge);

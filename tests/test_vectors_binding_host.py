@@ -34,3 +34,17 @@ def test_views_that_torch_would_negate_are_refused(ctx):
     for call in calls(ctx, x.resolve_neg()):
         with pytest.raises(ValueError, match="CUDA tensor"):
             call()
+
+
+def test_layer_norm_backward_takes_a_truth_value_for_bias(ctx):
+    """layer_norm has the bias itself at that name; here a tensor, or what has no truth value, is refused first."""
+    import numpy as np
+    x = torch.zeros(4, 8)
+    for bias in (torch.ones(8), torch.zeros(1), torch.ones(1)):
+        with pytest.raises(ValueError, match="bias"):
+            ctx.layer_norm_backward(x, x, x[:, 0], x[:, 0], None, bias)
+    with pytest.raises(ValueError, match="bias"):
+        ctx.layer_norm_backward(x, x, x[:, 0], x[:, 0], None, np.ones(8))
+    for bias in (True, False, 1, None):
+        with pytest.raises(ValueError, match="CUDA tensor"):
+            ctx.layer_norm_backward(x, x, x[:, 0], x[:, 0], None, bias)
