@@ -454,7 +454,9 @@ class Context:
                                               float(gamma), op), "find_splits")
 
     # -- the vector verbs ---------------------------------------------------
-    # Tensors must be on the context's device.  The checks, outputs and
+    # Tensors must be on the context's device.  Nothing is recorded for autograd
+    # (the _backward verbs are the gradients), so a tensor that requires a
+    # gradient is refused while torch records.  The checks, outputs and
     # workspaces are csrc/hgb_verbs.cpp's.  A call made on another stream than
     # the context's is ordered after that (the current) stream's work, and the
     # current stream after the call.

@@ -13,6 +13,7 @@
 #include <Python.h>
 
 #include <ATen/ATen.h>
+#include <c10/core/GradMode.h>
 #include <c10/core/impl/VirtualGuardImpl.h>
 #include <torch/csrc/Dtype.h>
 #include <torch/csrc/Exceptions.h>
@@ -108,6 +109,10 @@ const Tensor& tensor(const Call& c, PyObject* o, const char* name)
 {
     if (THPVariable_Check(o)) {
         const Tensor& t = THPVariable_Unpack(o);
+        // the verbs record nothing for autograd: the result would have no gradient, without a word
+        if (t.requires_grad() && c10::GradMode::is_enabled())
+            throw Refused("%s requires a gradient, which the verbs do not record: call them under torch.no_grad(), and "
+                          "their _backward for gradients", name);
         // what lies in memory is not what such a view holds
         if (t.is_neg()) throw Refused("%s is a negated view: give its resolve_neg()", name);
         if (t.is_cuda() && t.get_device() == c.device) return t;

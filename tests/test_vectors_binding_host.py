@@ -48,3 +48,18 @@ def test_layer_norm_backward_takes_a_truth_value_for_bias(ctx):
     for bias in (True, False, 1, None):
         with pytest.raises(ValueError, match="CUDA tensor"):
             ctx.layer_norm_backward(x, x, x[:, 0], x[:, 0], None, bias)
+
+
+def test_tensors_whose_gradient_would_be_lost_are_refused(ctx):
+    """The verbs record nothing for autograd, so a result would have no gradient and not say so."""
+    x = torch.zeros(4, 8, requires_grad=True)
+    for call in calls(ctx, x):
+        with pytest.raises(ValueError, match="requires a gradient"):
+            call()
+    with torch.no_grad():
+        for call in calls(ctx, x):
+            with pytest.raises(ValueError, match="CUDA tensor"):
+                call()
+    for call in calls(ctx, x.detach()):
+        with pytest.raises(ValueError, match="CUDA tensor"):
+            call()
