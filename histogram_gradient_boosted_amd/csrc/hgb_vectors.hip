@@ -14,6 +14,7 @@
 
 #include <cmath>
 #include <initializer_list>
+#include <numeric>
 #include <type_traits>
 
 using namespace hgb;
@@ -36,23 +37,39 @@ hgb_status check_rows(hgb_ctx* c, const char* verb, const char* name, const void
     return HGB_OK;
 }
 
-// The bytes of a matrix argument, from its first element to past its last.
+// The bytes of an argument: `rows` runs of `width`, `step` apart.
 struct Span {
     const char* begin;
-    int64_t bytes;
+    int64_t width;
+    int64_t rows = 1, step = 0;
 };
 
 Span span(const void* p, int32_t type, int64_t rows, int64_t dim, int64_t stride)
 {
-    return {(const char*)p, p && rows > 0 ? ((rows - 1) * stride + dim) * elem_size(type) : 0};
+    const int64_t size = elem_size(type);
+    if (!p || rows < 1) return {(const char*)p, 0};
+    if (rows == 1 || stride == dim) return {(const char*)p, rows * dim * size};
+    return {(const char*)p, dim * size, rows, stride * size};
 }
 
 Span span(const int32_t* p, int64_t n) { return {(const char*)p, p ? n * 4 : 0}; }
 Span span(const float* p, int64_t n) { return {(const char*)p, p ? n * 4 : 0}; }
 
+// Whether two arguments share a byte.  Where both extents meet, their rows may
+// still lie side by side: with g the greatest divisor of both steps, every row
+// of a is at begin(a) modulo g and every row of b at begin(b), so that they are
+// apart if one row of each is, on a ring of g bytes.  That finds every overlap,
+// and nothing else where the steps are equal or one argument is a single run.
 bool overlap(const Span& a, const Span& b)
 {
-    return a.bytes > 0 && b.bytes > 0 && a.begin < b.begin + b.bytes && b.begin < a.begin + a.bytes;
+    if (a.width < 1 || b.width < 1) return false;
+    const auto extent = [](const Span& s) { return (__int128)(s.rows - 1) * s.step + s.width; };
+    const __int128 ahead = (__int128)(intptr_t)b.begin - (intptr_t)a.begin;   // of a's first byte
+    if (ahead >= extent(a) || -ahead >= extent(b)) return false;
+    const int64_t g = a.rows == 1 ? b.step : b.rows == 1 ? a.step : std::gcd(a.step, b.step);
+    if (g == 0) return true;
+    const int64_t at = (int64_t)((ahead % g + g) % g);
+    return at < a.width || at + b.width > g;
 }
 
 // No output overlaps an input or another output; a workspace counts as an output.

@@ -477,8 +477,11 @@ hgb_status hgb_grow_level(hgb_ctx* ctx, const int64_t* parent_hist_dev, const hg
  *     verb refuses).  Its contents mean nothing before and after the call, and
  *     calls that may overlap need one each.  The verbs allocate nothing and
  *     wait for nothing, so they can be captured into a graph.
- *   - An output that overlaps an input or another output is refused
- *     (HGB_E_INVALID); the workspace counts as an output.
+ *   - An output that shares a byte with an input or another output is refused
+ *     (HGB_E_INVALID); the workspace counts as an output.  Rows of several
+ *     arguments may lie side by side in one buffer, with the same stride or
+ *     with strides whose greatest common divisor has room for a row of each;
+ *     with other strides, arguments whose extents meet are refused.
  *   - Zero rows or tokens are valid and leave only what the verb defines for
  *     them.
  */

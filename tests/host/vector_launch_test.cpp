@@ -1,7 +1,7 @@
 // What the vector verbs ask of the runtime, on the host alone: the runtime's
 // launch functions are this program's, which hold every launch to the limits of
 // a launch and run nothing.  No buffer is touched: addresses are made up.
-// Usage: vector_launch_test grids
+// Usage: vector_launch_test grids | apart
 #include "hgb_ctx.h"
 #include "hgb_vector_plan.h"
 
@@ -122,12 +122,70 @@ static void spans()
     }
 }
 
+// arguments side by side in one buffer share no byte and are taken; those that share one are not
+static void apart()
+{
+    hgb_ctx c;
+    c.dev_words = (uint32_t*)4096;
+    float* buf = (float*)at(1);
+    float *mean = (float*)at(10), *rstd = (float*)at(11), *ws = (float*)at(14);
+    int32_t *tok = (int32_t*)at(12), *pos = (int32_t*)at(13), *off = (int32_t*)at(15);
+    const int32_t F = HGB_F32, B = HGB_BF16;
+    auto is = [&](const char* name, hgb_status got, bool taken) {
+        std::snprintf(what, sizeof what, "%s", name);
+        CHECK(got == (taken ? HGB_OK : HGB_E_INVALID), "status %d, %s", got, c.err.c_str());
+        CHECK(taken || std::strstr(c.err.c_str(), "overlaps"), "%s", c.err.c_str());
+    };
+    auto norm = [&](float* x, int64_t xs, float* y, int64_t ys, int64_t n, int64_t dim) {
+        return hgb_layer_norm(&c, x, F, xs, n, dim, nullptr, nullptr, F, 1e-5f, y, ys, mean, rstd);
+    };
+    is("halves", norm(buf, 16, buf + 8, 16, 5, 8), true);
+    is("halves, the output first", norm(buf + 8, 16, buf, 16, 5, 8), true);
+    is("one value shared", norm(buf, 16, buf + 7, 16, 5, 8), false);
+    is("one value shared with the next row", norm(buf, 16, buf + 9, 16, 5, 8), false);
+    is("rows further on", norm(buf, 16, buf + 16 * 3 + 8, 16, 5, 8), true);
+    is("rows further on, shared", norm(buf, 16, buf + 16 * 3, 16, 5, 8), false);
+    is("behind the last row", norm(buf, 16, buf + 16 * 4 + 8, 16, 5, 8), true);
+    is("the last row shared", norm(buf, 16, buf + 16 * 4 + 7, 16, 5, 8), false);
+    is("one row between others", norm(buf, 16, buf + 8, 8, 1, 8), true);
+    is("one row behind the other", norm(buf, 16, buf + 8, 99, 1, 8), true);
+    is("strides of 32 and 16", norm(buf, 32, buf + 8, 16, 5, 8), true);
+    is("strides of 32 and 16, shared", norm(buf, 32, buf + 4, 16, 5, 8), false);
+    is("strides without room for both", norm(buf, 16, buf + 8, 17, 5, 8), false);
+    is("far apart", norm(buf, 16, buf + 1000, 17, 5, 8), true);
+    is("statistics in the rows' gap", hgb_layer_norm(&c, buf, F, 64, 5, 8, nullptr, nullptr, F, 1e-5f, buf + 16, 64, buf + 32, buf + 37), true);
+    is("statistics across a row", hgb_layer_norm(&c, buf, F, 64, 5, 8, nullptr, nullptr, F, 1e-5f, buf + 16, 64, buf + 60, buf + 37), false);
+    is("a table beside the output", hgb_embed(&c, buf, F, 24, 100, 8, tok, 50, -1, 1, buf + 8, B, 48), true);
+    is("a table under the output", hgb_embed(&c, buf, F, 24, 100, 8, tok, 50, -1, 1, buf + 7, B, 48), false);
+    is("the table's gradient beside the rows'",
+       hgb_embed_backward(&c, buf, F, 20, 50, 8, tok, -1, 1, 30, buf + 12, F, 20, ws, 1 << 20), true);
+    is("the table's gradient over the rows'",
+       hgb_embed_backward(&c, buf, F, 20, 50, 8, tok, -1, 1, 30, buf + 13, F, 20, ws, 1 << 20), false);
+    is("dx beside x and grad", hgb_layer_norm_backward(&c, buf, 24, buf + 8, 24, F, 5, 8, mean, rstd, nullptr, F, buf + 16, 24, nullptr,
+                                                       nullptr, nullptr, 0), true);
+    is("dx into grad's next row", hgb_layer_norm_backward(&c, buf, 24, buf + 8, 24, F, 5, 8, mean, rstd, nullptr, F, buf + 17, 24, nullptr,
+                                                          nullptr, nullptr, 0), false);
+    is("sorted rows beside the rows", hgb_route_gather(&c, buf, F, 16, 6, 2, 8, pos, off, 4, buf + 8, 16), true);
+    is("sorted rows over the rows", hgb_route_gather(&c, buf, F, 16, 6, 2, 8, pos, off, 4, buf + 4, 16), false);
+    is("answers beside the sums", hgb_route_combine(&c, buf, F, 16, 6, 2, 8, pos, nullptr, buf + 8, 16), true);
+    is("answers' gradient beside the answers",
+       hgb_route_combine_backward(&c, buf, F, 24, buf + 8, 24, 6, 2, 8, pos, off, 4, mean, buf + 16, 24, rstd), true);
+    // extents that do not fit 64 bits
+    is("a solid output in the gap of the largest extent",
+       hgb_embed(&c, at(0), F, (int64_t)1 << 40, kVecMaxVocab, 8, tok, 50, -1, 1, at(0) + 32, F, 8), true);
+    is("a solid output over its first row",
+       hgb_embed(&c, at(0), F, (int64_t)1 << 40, kVecMaxVocab, 8, tok, 50, -1, 1, at(0) + 28, F, 8), false);
+    is("the largest extents, side by side",
+       hgb_embed(&c, at(0), F, (int64_t)1 << 40, kVecMaxVocab, 8, tok, 50, -1, 1, at(0) + 32, F, (int64_t)1 << 40), true);
+}
+
 int main(int argc, char** argv)
 {
     if (argc > 1 && !std::strcmp(argv[1], "grids")) {
         spans();
         grids();
     }
+    if (argc > 1 && !std::strcmp(argv[1], "apart")) apart();
     CHECK(launches > 0, "nothing was launched");
     std::printf(failures ? "%d of %d checks failed\n" : "%d of %d failed: all checks passed\n", failures, checks);
     return failures != 0;

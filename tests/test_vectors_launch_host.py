@@ -32,3 +32,7 @@ def run(program, what):
 
 def test_every_accepted_size_fits_a_launch(program):
     run(program, "grids")
+
+
+def test_arguments_side_by_side_in_one_buffer_are_taken(program):
+    run(program, "apart")
