@@ -811,7 +811,7 @@ static hgb_status take_flags(hgb_ctx* c)
     return HGB_OK;
 }
 
-// The same for the vector verbs' word.  A failed row index is reported first.
+// The same for the vector verbs' word.
 static hgb_status take_vector_flags(hgb_ctx* c)
 {
     const uint32_t flags = c->host_words[kWordVectors];
@@ -819,9 +819,9 @@ static hgb_status take_vector_flags(hgb_ctx* c)
     k_clear_u32<<<1, 64, 0, c->stream>>>(c->dev_words + kWordVectors, 1);
     HGB_LAUNCHED(c, "k_clear_u32");
     HGB_HIP(c, hipStreamSynchronize(c->stream));
-    if (!c->err.empty()) return HGB_E_INVALID;
-    if (flags & kVecErrToken) return fail(c, HGB_E_INVALID, "a token outside [0, vocab) was taken as padding");
-    return fail(c, HGB_E_INVALID, "an expert outside [0, n_experts) was dropped");
+    const bool token = flags & kVecErrToken, expert = flags & kVecErrExpert;
+    return fail(c, HGB_E_INVALID, "%s%s%s", token ? "a token outside [0, vocab) was taken as padding" : "",
+                token && expert ? ", and " : "", expert ? "an expert outside [0, n_experts) was dropped" : "");
 }
 
 hgb_status hgb_sync(hgb_ctx* c)
@@ -836,14 +836,13 @@ hgb_status hgb_sync(hgb_ctx* c)
     st = resolve_scales(c);
     if (st != HGB_OK) return st;
     st = take_flags(c);
-    const hgb_status vt = take_vector_flags(c);
-    if (st == HGB_OK) st = vt;
     if (c->deferred != HGB_OK) {   // reported once, before a skipped row index
         const hgb_status d = c->deferred;
         c->deferred = HGB_OK;
         return fail(c, d, "%s", c->deferred_msg.c_str());
     }
-    return st;
+    // last, and left to the next sync where this one reports something else
+    return st != HGB_OK ? st : take_vector_flags(c);
 }
 
 hgb_status hgb_set_async_begin(hgb_ctx* c, int enable)

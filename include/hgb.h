@@ -100,9 +100,10 @@ const char* hgb_last_error(const hgb_ctx* ctx);
  * context lifecycle": the host reads results once the level's work is done).
  * Returns HGB_E_NONFINITE if a tree started asynchronously since the previous
  * hgb_sync had a non-finite value (hgb_set_async_begin), else HGB_E_INVALID
- * if a kernel met a row index outside [0, n), or a vector verb a token or
- * expert out of range, since the previous hgb_sync (those entries were
- * skipped), HGB_E_DEVICE on a runtime error, else HGB_OK. */
+ * if a kernel met a row index outside [0, n) since the previous hgb_sync (those
+ * entries were skipped), else HGB_E_INVALID if a vector verb met a token or
+ * expert out of range (skipped too) since the last hgb_sync that reported that
+ * or returned HGB_OK, HGB_E_DEVICE on a runtime error, else HGB_OK. */
 hgb_status hgb_sync(hgb_ctx* ctx);
 
 /*

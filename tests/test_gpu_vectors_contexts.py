@@ -1,0 +1,94 @@
+"""The vector verbs on contexts: what a sync reports when several things went
+wrong before it, and contexts side by side."""
+import sys
+
+import numpy as np
+import pytest
+
+from histogram_gradient_boosted_amd import synth
+
+pytestmark = pytest.mark.gpu
+
+
+def say(*a):
+    print("[gpu-vectors-contexts]", *a, flush=True)
+    sys.stdout.flush()
+
+
+@pytest.fixture(scope="module")
+def torch():
+    import torch as _torch
+    from histogram_gradient_boosted_amd import binding
+    if not _torch.cuda.is_available() or not binding.available():
+        pytest.skip("no HIP device")
+    return _torch
+
+
+@pytest.fixture(scope="module")
+def hgb(torch):
+    from histogram_gradient_boosted_amd import binding
+    return binding
+
+
+@pytest.fixture()
+def ctx(hgb):
+    c = hgb.Context(0)
+    yield c
+    c.close()
+
+
+def bad_token(torch, ctx):
+    ctx.embed(torch.ones(3, 4, device="cuda"), torch.tensor([0, 3], dtype=torch.int32, device="cuda"))
+
+
+def bad_expert(torch, ctx):
+    ctx.route(torch.tensor([[0], [3]], dtype=torch.int32, device="cuda"), 3)
+
+
+def reports(hgb, ctx, *words):
+    """The next sync fails with these words in its message."""
+    with pytest.raises(hgb.HGBError) as e:
+        ctx.sync()
+    for w in words:
+        assert w in str(e.value), str(e.value)
+    return e.value.status
+
+
+def test_a_sync_reports_tokens_and_experts(torch, hgb, ctx):
+    bad_token(torch, ctx)
+    bad_expert(torch, ctx)
+    assert reports(hgb, ctx, "token", "expert") == hgb.HGB_E_INVALID
+    ctx.sync()
+    bad_token(torch, ctx)
+    assert reports(hgb, ctx, "token") == hgb.HGB_E_INVALID
+    bad_expert(torch, ctx)
+    assert reports(hgb, ctx, "expert") == hgb.HGB_E_INVALID
+    ctx.sync()
+
+
+@pytest.mark.parametrize("bad", [bad_token, bad_expert])
+def test_a_row_index_is_reported_and_then_the_token(torch, hgb, ctx, bad):
+    w = synth.random_small(65, 1000, 4, 64, False, 0)
+    ctx.upload_bins(w.bins, w.n_bins, w.has_missing)
+    ctx.begin_tree(torch.from_numpy(w.grad).cuda(), torch.from_numpy(w.hess).cuda())
+    hist = torch.empty((1, 4, 64, 2), dtype=torch.int64, device="cuda")
+    rows = torch.tensor([0, 1, 1000, 2], dtype=torch.int32, device="cuda")
+    ctx.build_level(hist, rows, np.array([0, 4], np.int32))
+    bad(torch, ctx)
+    assert reports(hgb, ctx, "row index") == hgb.HGB_E_INVALID
+    assert reports(hgb, ctx, bad.__name__[4:]) == hgb.HGB_E_INVALID
+    ctx.sync()
+
+
+@pytest.mark.parametrize("bad", [bad_token, bad_expert])
+def test_a_tree_that_is_not_finite_is_reported_and_then_the_token(torch, hgb, ctx, bad):
+    w = synth.random_small(66, 1000, 4, 64, False, 0)
+    ctx.set_async_begin(True)
+    ctx.upload_bins(w.bins, w.n_bins, w.has_missing)
+    g = torch.from_numpy(w.grad).cuda()
+    g[7] = float("nan")
+    ctx.begin_tree(g, torch.from_numpy(w.hess).cuda())
+    bad(torch, ctx)
+    assert reports(hgb, ctx) == hgb.HGB_E_NONFINITE
+    assert reports(hgb, ctx, bad.__name__[4:]) == hgb.HGB_E_INVALID
+    ctx.sync()
