@@ -270,23 +270,6 @@ PlanCtx plan_ctx(const hgb_ctx* c)
     return pc;
 }
 
-template <typename K>
-hgb_status set_lds(hgb_ctx* c, K kernel, size_t bytes)
-{
-    // once per kernel and size: the attribute persists for the process
-    const void* fn = (const void*)kernel;
-    for (auto& e : c->lds_set)
-        if (e.first == fn) {
-            if (e.second >= bytes) return HGB_OK;
-            HGB_HIP(c, hipFuncSetAttribute(fn, hipFuncAttributeMaxDynamicSharedMemorySize, (int)bytes));
-            e.second = bytes;
-            return HGB_OK;
-        }
-    HGB_HIP(c, hipFuncSetAttribute(fn, hipFuncAttributeMaxDynamicSharedMemorySize, (int)bytes));
-    c->lds_set.emplace_back(fn, bytes);
-    return HGB_OK;
-}
-
 struct FillArgs {
     const int2* gh;
     const int32_t* row_index;
@@ -312,7 +295,7 @@ hgb_status launch_fill_acc(hgb_ctx* c, const FillPlan& p, const FillArgs& a)
     hgb_status st = HGB_OK;
 #define HGB_LAUNCH(kern, ...)                                                            \
     do {                                                                                 \
-        st = set_lds(c, kern, p.lds_bytes);                                              \
+        st = raise_lds(c, kern);                                                         \
         if (st != HGB_OK) return st;                                                     \
         kern<<<grid, p.threads, p.lds_bytes, c->stream>>>(__VA_ARGS__);                  \
     } while (0)
@@ -922,8 +905,8 @@ hgb_status hgb_upload_bins(hgb_ctx* c, const void* bins, int bin_bytes, int on_d
         HGB_HIP(c, hipMemsetAsync(counts, 0, sizeof(uint32_t) * n_counts, c->stream));
         const dim3 cgrid((unsigned)((n_rows + kCountChunk - 1) / kCountChunk), (unsigned)n_features);
         const size_t clds = sizeof(uint32_t) * (size_t)S * kCountCopies;
-        hgb_status st = bin_bytes == 1 ? set_lds(c, k_slot_counts<uint8_t>, clds)
-                                       : set_lds(c, k_slot_counts<uint16_t>, clds);
+        hgb_status st = bin_bytes == 1 ? raise_lds(c, k_slot_counts<uint8_t>)
+                                       : raise_lds(c, k_slot_counts<uint16_t>);
         if (st != HGB_OK) {
             (void)hipFree(counts);
             return st;

@@ -141,8 +141,8 @@ struct hgb_ctx {
     // optional per-kernel timing
     bool prof = false;
     std::vector<hipEvent_t> ev_pool;
-    // kernels whose dynamic-LDS limit has been raised, and to what
-    std::vector<std::pair<const void*, size_t>> lds_set;
+    // kernels whose dynamic-LDS limit has been raised (raise_lds)
+    std::vector<const void*> lds_set;
     std::vector<std::pair<hipEvent_t, hipEvent_t>> ev_pending[HGB_KERNEL_COUNT];
     double prof_ms[HGB_KERNEL_COUNT] = {};
     int64_t prof_launches[HGB_KERNEL_COUNT] = {};
@@ -175,6 +175,22 @@ inline hgb_status fail(hgb_ctx* c, hgb_status st, const char* fmt, ...)
             return fail((c), HGB_E_DEVICE, "launch of %s failed: %s", what,                \
                         hipGetErrorString(e_));                                            \
     } while (0)
+
+// Lets a kernel (without LDS arrays of its own) be launched with all the LDS of
+// a CU.  The limit is the kernel's in the process, so every context sets it to
+// the same: one that set what its own launch needs could lower another's.
+constexpr int kLdsBytes = 160 * 1024;
+
+template <typename K>
+hgb_status raise_lds(hgb_ctx* c, K kernel)
+{
+    const void* fn = (const void*)kernel;
+    for (const void* f : c->lds_set)
+        if (f == fn) return HGB_OK;
+    HGB_HIP(c, hipFuncSetAttribute(fn, hipFuncAttributeMaxDynamicSharedMemorySize, kLdsBytes));
+    c->lds_set.push_back(fn);
+    return HGB_OK;
+}
 
 inline hipEvent_t pool_event(hgb_ctx* c)
 {

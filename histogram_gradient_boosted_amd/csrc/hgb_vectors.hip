@@ -190,21 +190,6 @@ dim3 row_grid(const RowMap& m, int64_t rows)
 
 int log2_of(int p) { return 31 - __builtin_clz((unsigned)p); }
 
-hgb_status raise_lds(hgb_ctx* c, const void* fn, size_t bytes)
-{
-    if (bytes <= 65536) return HGB_OK;
-    for (auto& e : c->lds_set)
-        if (e.first == fn) {
-            if (e.second >= bytes) return HGB_OK;
-            HGB_HIP(c, hipFuncSetAttribute(fn, hipFuncAttributeMaxDynamicSharedMemorySize, (int)bytes));
-            e.second = bytes;
-            return HGB_OK;
-        }
-    HGB_HIP(c, hipFuncSetAttribute(fn, hipFuncAttributeMaxDynamicSharedMemorySize, (int)bytes));
-    c->lds_set.emplace_back(fn, bytes);
-    return HGB_OK;
-}
-
 // Blocks for a zero fill of `bytes`: a wave's 16-byte stores 16 times over, at most two blocks a CU.
 int zero_blocks(const hgb_ctx* c, int64_t bytes, int threads)
 {
@@ -216,7 +201,7 @@ hgb_status launch_sort_small(hgb_ctx* c, const SortIn& in, const SortOut& out, c
 {
     const int threads = (int)std::max<int64_t>(std::max<int64_t>(64, p.radix), vec_up(vec_ceil(in.n, ITEMS), 64));
     const size_t lds = 4 * ((size_t)small_pair_words(p, ITEMS, threads) + (size_t)(threads / 64) * p.radix + p.radix + 16);
-    HGB_TRY(raise_lds(c, (const void*)k_sort_small<ITEMS>, lds));
+    if (lds > 65536) HGB_TRY(raise_lds(c, k_sort_small<ITEMS>));
     k_sort_small<ITEMS><<<1 + zero_blocks(c, z.rows * z.cols * z.elem, threads), threads, lds, c->stream>>>(in, out, p, z);
     HGB_LAUNCHED(c, "k_sort_small");
     return HGB_OK;
@@ -227,7 +212,7 @@ hgb_status launch_scatter(hgb_ctx* c, const SortIn& in, const SortOut& out, cons
                           const uint32_t* counts, const ZeroFill& z)
 {
     const size_t lds = 4 * (scatter_pair_words(ITEMS) + (size_t)(kSortThreads / 64) * p.radix + 2 * (size_t)p.radix + 16);
-    HGB_TRY(raise_lds(c, (const void*)k_sort_scatter<FIRST, ITEMS>, lds));
+    if (lds > 65536) HGB_TRY(raise_lds(c, k_sort_scatter<FIRST, ITEMS>));
     k_sort_scatter<FIRST, ITEMS><<<p.blocks + zero_blocks(c, z.rows * z.cols * z.elem, kSortThreads), kSortThreads, lds,
                                    c->stream>>>(in, out, p, shift, counts, z);
     HGB_LAUNCHED(c, "k_sort_scatter");

@@ -1,13 +1,14 @@
 // What the vector verbs ask of the runtime, on the host alone: the runtime's
 // launch functions are this program's, which hold every launch to the limits of
 // a launch and run nothing.  No buffer is touched: addresses are made up.
-// Usage: vector_launch_test grids | apart
+// Usage: vector_launch_test grids | apart | contexts
 #include "hgb_ctx.h"
 #include "hgb_vector_plan.h"
 
 #include <cstdint>
 #include <cstdio>
 #include <cstring>
+#include <map>
 
 using namespace hgb;
 
@@ -28,7 +29,16 @@ extern "C" {
 
 hipError_t hipSetDevice(int) { return hipSuccess; }
 hipError_t hipGetLastError(void) { return hipSuccess; }
-hipError_t hipFuncSetAttribute(const void*, hipFuncAttribute, int) { return hipSuccess; }
+
+// a kernel's limit of dynamic LDS: one for the process, whoever sets it
+static std::map<const void*, int> limits;
+
+hipError_t hipFuncSetAttribute(const void* fn, hipFuncAttribute which, int value)
+{
+    if (which != hipFuncAttributeMaxDynamicSharedMemorySize || value < 0 || value > 163840) return hipErrorInvalidValue;
+    limits[fn] = value;
+    return hipSuccess;
+}
 
 // <<<grid, block, lds, stream>>>
 struct Shape {
@@ -52,9 +62,12 @@ hipError_t __hipPopCallConfiguration(dim3* grid, dim3* block, size_t* lds, hipSt
     return hipSuccess;
 }
 
-hipError_t hipLaunchKernel(const void*, dim3 grid, dim3 block, void**, size_t, hipStream_t)
+hipError_t hipLaunchKernel(const void* fn, dim3 grid, dim3 block, void**, size_t lds, hipStream_t)
 {
     ++launches;
+    const auto limit = limits.find(fn);
+    const int most_lds = limit == limits.end() ? 65536 : limit->second;
+    CHECK(lds <= (size_t)most_lds, "%zu bytes of LDS, limit %d", lds, most_lds);
     const uint64_t most = (uint64_t)1 << 32;
     CHECK(grid.x > 0 && grid.y > 0 && grid.z > 0, "%u x %u x %u blocks", grid.x, grid.y, grid.z);
     CHECK(block.x * block.y * block.z <= 1024, "%u threads", block.x * block.y * block.z);
@@ -179,6 +192,21 @@ static void apart()
        hgb_embed(&c, at(0), F, (int64_t)1 << 40, kVecMaxVocab, 8, tok, 50, -1, 1, at(0) + 32, F, (int64_t)1 << 40), true);
 }
 
+// two contexts turn by turn, whose sorts take more and less LDS of one kernel
+static void contexts()
+{
+    hgb_ctx a, b;
+    a.dev_words = b.dev_words = (uint32_t*)4096;
+    for (int64_t n : {3000, 300000, 1100000, 5000000})
+        for (int experts : {1023, 200, 1023}) {
+            std::snprintf(what, sizeof what, "%lld slots of %d experts", (long long)n, experts);
+            for (hgb_ctx* c : {&a, &b, &a})
+                CHECK(hgb_route(c, (int32_t*)at(1), n, 1, c == &a ? experts : 1223 - experts, (int32_t*)at(2), (int32_t*)at(3),
+                                (int32_t*)at(4), at(5), (int64_t)1 << 56) == HGB_OK,
+                      "%s", c->err.c_str());
+        }
+}
+
 int main(int argc, char** argv)
 {
     if (argc > 1 && !std::strcmp(argv[1], "grids")) {
@@ -186,6 +214,7 @@ int main(int argc, char** argv)
         grids();
     }
     if (argc > 1 && !std::strcmp(argv[1], "apart")) apart();
+    if (argc > 1 && !std::strcmp(argv[1], "contexts")) contexts();
     CHECK(launches > 0, "nothing was launched");
     std::printf(failures ? "%d of %d checks failed\n" : "%d of %d failed: all checks passed\n", failures, checks);
     return failures != 0;

@@ -92,3 +92,19 @@ def test_a_tree_that_is_not_finite_is_reported_and_then_the_token(torch, hgb, ct
     assert reports(hgb, ctx) == hgb.HGB_E_NONFINITE
     assert reports(hgb, ctx, bad.__name__[4:]) == hgb.HGB_E_INVALID
     ctx.sync()
+
+
+def test_two_contexts_sort_by_digits_of_different_widths(torch, hgb):
+    """Turn by turn, sorts whose kernels take 139 and 83 KB of LDS."""
+    a, b = hgb.Context(0), hgb.Context(0)
+    n = 1_100_000
+    g = torch.Generator(device="cuda").manual_seed(1)
+    e = torch.randint(0, 200, (n, 1), generator=g, device="cuda", dtype=torch.int32)
+    want = torch.sort(e.view(-1), stable=True).indices.int()
+    for c, experts in ((a, 1023), (b, 200), (a, 1023), (b, 1023), (a, 200)):
+        say("experts", experts)
+        assert torch.equal(c.route(e, experts).order, want)
+    a.sync()
+    b.sync()
+    a.close()
+    b.close()

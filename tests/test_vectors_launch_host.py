@@ -36,3 +36,7 @@ def test_every_accepted_size_fits_a_launch(program):
 
 def test_arguments_side_by_side_in_one_buffer_are_taken(program):
     run(program, "apart")
+
+
+def test_contexts_do_not_lower_each_other_s_lds(program):
+    run(program, "contexts")
