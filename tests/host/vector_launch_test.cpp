@@ -131,6 +131,15 @@ static void spans()
     for (int64_t n : ns) {
         for (int V : {4, 8})
             for (int64_t dim = 1; dim < 3000; ++dim) check(row_blocks(plan_rows(dim, V), n), plan_rows(dim, V).per);
+        // the embedding gradient's chunk ends have their place in its workspace
+        for (int64_t dim : {1, 7, 64, 129, 1040, 1 << 20})
+            for (int64_t vocab : {(int64_t)1, (int64_t)7196, kVecMaxVocab}) {
+                const EmbedPlan p = plan_embed(n, vocab, dim);
+                std::snprintf(what, sizeof what, "%lld tokens of %lld, vocab %lld", (long long)n, (long long)dim, (long long)vocab);
+                CHECK(p.off_ends >= p.off_part + p.chunks * 2 * p.part_stride * 4 && p.off_ends % 4 == 0, "ends at %lld", (long long)p.off_ends);
+                CHECK(p.bytes >= p.off_ends + p.chunks * 4, "%lld bytes", (long long)p.bytes);
+                CHECK(p.chunks * p.chunk >= n && p.chunks <= 2147483647, "%lld chunks", (long long)p.chunks);
+            }
         for (int lg = 0; lg <= 6; ++lg) check(vec_ceil(n, 256 >> lg), 256 >> lg);   // slots by groups of lanes
     }
 }
