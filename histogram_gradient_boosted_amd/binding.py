@@ -220,7 +220,7 @@ class Context:
     def close(self):
         if getattr(self, "_h", None):
             self._lib.hgb_destroy(self._h)
-            self._h = self._handle = None
+            self._h, self._handle = None, 0
 
     def __del__(self):
         try:

@@ -108,3 +108,18 @@ def test_two_contexts_sort_by_digits_of_different_widths(torch, hgb):
     b.sync()
     a.close()
     b.close()
+
+
+def test_a_closed_context_is_refused_as_a_null_one(torch, hgb):
+    ctx = hgb.Context(0)
+    x, i = torch.zeros(4, 8, device="cuda"), torch.zeros(4, 2, dtype=torch.int32, device="cuda")
+    r = ctx.route(i, 3)
+    y = ctx.route_gather(x, r)
+    _, mean, rstd = ctx.layer_norm(x)
+    ctx.close()
+    for call in (lambda: ctx.embed(x, i), lambda: ctx.embed_backward(x, i[:, 0].contiguous(), 5), lambda: ctx.layer_norm(x),
+                 lambda: ctx.layer_norm_backward(x, x, mean, rstd), lambda: ctx.route(i, 3), lambda: ctx.route_gather(x, r),
+                 lambda: ctx.route_combine(y, r), lambda: ctx.route_gather_backward(y, r),
+                 lambda: ctx.route_combine_backward(x, y, r), ctx.sync):
+        with pytest.raises(hgb.HGBError, match="null context"):
+            call()
