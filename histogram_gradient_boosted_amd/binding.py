@@ -40,14 +40,16 @@ EXPORTED = ("hgb_available", "hgb_create", "hgb_destroy", "hgb_last_error", "hgb
             "hgb_embed", "hgb_embed_backward", "hgb_embed_backward_workspace",
             "hgb_layer_norm", "hgb_layer_norm_backward", "hgb_layer_norm_backward_workspace",
             "hgb_route", "hgb_route_workspace", "hgb_route_gather", "hgb_route_gather_backward",
-            "hgb_route_combine", "hgb_route_combine_backward")
+            "hgb_route_combine", "hgb_route_combine_backward",
+            "hgb_gate", "hgb_gate_backward", "hgb_head_workspace", "hgb_head_backward_workspace",
+            "hgb_cross_entropy", "hgb_cross_entropy_backward", "hgb_distill", "hgb_distill_backward")
 
 # hgb_objective
 OBJECTIVES = {"squared": 0, "logistic": 1, "poisson": 2}
 
 KERNELS = {"quantize": 0, "gather": 1, "zero": 2, "fill": 3, "subtract": 4, "split": 5,
            "partition": 6, "fill_root": 7, "fill_level": 8, "merge": 9, "embed": 10, "norm": 11,
-           "route": 12}
+           "route": 12, "gate": 13, "head": 14}
 
 
 class HGBError(RuntimeError):
@@ -533,3 +535,49 @@ class Context:
         """Gradients of route_combine: (dy [rows * top, dim], dweights [rows, top],
         None without weights)."""
         return self._verb("route_combine_backward", grad, y, route.position, route.offsets, weights, out)
+
+    def gate(self, logits, top: int, score: str = "softmax", bias=None, groups: int = 1, keep: int = 1, best: int = 2,
+             renormalise: bool = True, scale: float = 1.0):
+        """The `top` experts of each row of logits [rows, experts] and their
+        shares: (int32, float32 [rows, top]), as route and route_combine take
+        them.  The largest scores ("softmax" or "sigmoid") plus bias (float32
+        [experts], for the choice alone) are chosen, out of the `keep` of `groups` equal
+        runs of experts whose `best` largest are largest in sum.  share: scale
+        times the score, over the chosen scores' sum with renormalise.  An
+        expert of logit or bias -inf is masked; a row with too few left has
+        expert -1 and share 0 behind them."""
+        return self._verb("gate", logits, top, score, bias, groups, keep, best, renormalise, scale)
+
+    def gate_backward(self, grad, logits, experts, score: str = "softmax", renormalise: bool = True, scale: float = 1.0,
+                      out=None):
+        """The gradient of gate's logits ([rows, experts], of their type) from
+        the shares' (float32 [rows, top]), for the experts that gate chose."""
+        return self._verb("gate_backward", grad, logits, experts, score, renormalise, scale, out)
+
+    def cross_entropy(self, x, table, targets, scale: float = 1.0, pad: int = -1):
+        """The loss of x's rows ([..., dim]) under a softmax over the rows of
+        table ([vocab, dim], x's type): (loss, lse), float32 [...], with
+        lse = log of the sum of exp(scale * <x, table[v]>) and loss = lse minus
+        the target's logit.  The target `pad` gives loss 0; so does one out of
+        range, which the next sync() reports.  The logits are never stored."""
+        return self._verb("cross_entropy", x, table, targets, scale, pad)
+
+    def cross_entropy_backward(self, grad, x, table, targets, lse, scale: float = 1.0, pad: int = -1, dtype=None, out=None):
+        """Gradients of cross_entropy: (dx, dtable), from the losses' gradients
+        `grad` (float32).  dtable: [vocab, dim] of `dtype` (x's type, or
+        float32); out: where dx goes."""
+        return self._verb("cross_entropy_backward", grad, x, table, targets, lse, scale, pad, dtype, out)
+
+    def distill(self, x, table, tokens, teacher, temperature: float = 1.0):
+        """The loss of x's rows against a teacher's top logits: tokens (int32)
+        and teacher (float32 or x's type), both [..., top].  With T the
+        temperature, T^2 times the divergence of softmax(x table^T / T), over
+        all tokens, from softmax(teacher / T), over the given ones:
+        (loss, lse, picked), float32, picked [..., top] the logits (over T) at the
+        tokens.  A slot of token -1 or logit -inf is left out (one out of range
+        too, and the next sync() reports it); a row of none has loss 0."""
+        return self._verb("distill", x, table, tokens, teacher, temperature)
+
+    def distill_backward(self, grad, x, table, tokens, teacher, lse, picked, temperature: float = 1.0, dtype=None, out=None):
+        """Gradients of distill: (dx, dtable), as cross_entropy_backward gives them."""
+        return self._verb("distill_backward", grad, x, table, tokens, teacher, lse, picked, temperature, dtype, out)

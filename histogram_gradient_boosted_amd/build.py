@@ -5,13 +5,15 @@ from __future__ import annotations
 import os
 import subprocess
 import sys
+import tempfile
+from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libhgb.so")
-SOURCES = [os.path.join(CSRC, "hgb.hip"), os.path.join(CSRC, "hgb_vectors.hip")]
+SOURCES = [os.path.join(CSRC, name) for name in ("hgb.hip", "hgb_vectors.hip", "hgb_vector_gate.hip", "hgb_vector_head.hip")]
 # the vector verbs on torch tensors, host code over the C ABI
 VERBS_LIB = os.path.join(PKG, "_verbs.so")
 VERBS_SOURCE = os.path.join(CSRC, "hgb_verbs.cpp")
@@ -20,11 +22,14 @@ PROBE_LIB = os.path.join(PKG, "liblds_rate.so")
 PROBE_SOURCES = [os.path.join(CSRC, "lds_rate.hip")]
 HEADERS = [os.path.join(CSRC, "hgb_kernels.h"), os.path.join(CSRC, "hgb_layout.h"), os.path.join(CSRC, "hgb_plan.h"),
            os.path.join(CSRC, "hgb_ctx.h"), os.path.join(CSRC, "hgb_vector_kernels.h"),
-           os.path.join(CSRC, "hgb_vector_plan.h"), os.path.join(INCLUDE, "hgb.h")]
+           os.path.join(CSRC, "hgb_vector_plan.h"), os.path.join(CSRC, "hgb_vector_rows.h"),
+           os.path.join(CSRC, "hgb_vector_checks.h"), os.path.join(CSRC, "hgb_vector_gate_kernels.h"),
+           os.path.join(CSRC, "hgb_vector_head_kernels.h"), os.path.join(CSRC, "hgb_vector_head_plan.h"),
+           os.path.join(INCLUDE, "hgb.h")]
 ARCH = "gfx950"
 
 HIPCC_FLAGS = [
-    f"--offload-arch={ARCH}", "-O3", "-std=c++17", "-fPIC", "-shared",
+    f"--offload-arch={ARCH}", "-O3", "-std=c++17", "-fPIC",
     # the split scan's fp64 gain is evaluated exactly as written
     "-ffp-contract=off",
     # no packed fp32 instructions in generated code
@@ -35,12 +40,20 @@ HIPCC_FLAGS = [
 
 
 def _compile(lib: str, sources, verbose: bool) -> None:
+    """Each source by itself, side by side, then the library from their objects."""
     hipcc = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
-    tmp = lib + ".tmp"
-    cmd = [hipcc, *HIPCC_FLAGS, "-o", tmp, *sources]
-    if verbose:
-        print(" ".join(cmd), flush=True)
-    subprocess.run(cmd, check=True)
+
+    def run(*args):
+        cmd = [hipcc, *HIPCC_FLAGS, *args]
+        if verbose:
+            print(" ".join(cmd), flush=True)
+        subprocess.run(cmd, check=True)
+
+    with tempfile.TemporaryDirectory() as folder, ThreadPoolExecutor(len(sources)) as pool:
+        objects = [os.path.join(folder, f"{i}.o") for i in range(len(sources))]
+        list(pool.map(lambda at: run("-c", "-o", *at), zip(objects, sources)))
+        tmp = lib + ".tmp"
+        run("-shared", "-o", tmp, *objects)
     os.replace(tmp, lib)
 
 

@@ -802,9 +802,11 @@ static hgb_status take_vector_flags(hgb_ctx* c)
     k_clear_u32<<<1, 64, 0, c->stream>>>(c->dev_words + kWordVectors, 1);
     HGB_LAUNCHED(c, "k_clear_u32");
     HGB_HIP(c, hipStreamSynchronize(c->stream));
-    const bool token = flags & kVecErrToken, expert = flags & kVecErrExpert;
-    return fail(c, HGB_E_INVALID, "%s%s%s", token ? "a token outside [0, vocab) was taken as padding" : "",
-                token && expert ? ", and " : "", expert ? "an expert outside [0, n_experts) was dropped" : "");
+    const bool token = flags & kVecErrToken, expert = flags & kVecErrExpert, score = flags & kVecErrScore;
+    return fail(c, HGB_E_INVALID, "%s%s%s%s%s", token ? "a token outside [0, vocab) was taken as padding" : "",
+                token && expert ? ", and " : "", expert ? "an expert outside [0, n_experts) was dropped" : "",
+                (token || expert) && score ? ", and " : "",
+                score ? "an expert whose logit or bias is NaN or +infinity was masked" : "");
 }
 
 hgb_status hgb_sync(hgb_ctx* c)

@@ -26,11 +26,12 @@ constexpr int kStages = 16;
 constexpr int kEpochEvents = 4;
 constexpr int kEpochUses = 6;
 // The device and pinned host word in which the vector verbs' kernels flag a
-// token or an expert out of range (apart from word 2, which partition_level
-// reads and clears).
+// token or an expert out of range, or a gate's logit that is NaN or +infinity
+// (apart from word 2, which partition_level reads and clears).
 constexpr int kWordVectors = 12;
 constexpr uint32_t kVecErrToken = 1u;
 constexpr uint32_t kVecErrExpert = 2u;
+constexpr uint32_t kVecErrScore = 4u;
 
 struct Stage {
     void* host = nullptr;   // pinned

@@ -21,6 +21,7 @@
 
 #include <cstdarg>
 #include <cstdio>
+#include <cstring>
 #include <exception>
 
 #include "hgb.h"
@@ -441,6 +442,181 @@ PyObject* route_combine_backward(const Call& c)
     return s == HGB_OK ? tuple({out.r.t, dw}) : status(s);
 }
 
+int32_t score_of(PyObject* o)
+{
+    const char* name = PyUnicode_Check(o) ? PyUnicode_AsUTF8(o) : nullptr;
+    if (name && !strcmp(name, "softmax")) return HGB_SOFTMAX;
+    if (name && !strcmp(name, "sigmoid")) return HGB_SIGMOID;
+    PyErr_Clear();
+    throw Refused("score must be \"softmax\" or \"sigmoid\"");
+}
+
+// gate(logits, top, score, bias, groups, keep, best, renormalise, scale)
+PyObject* gate(const Call& c)
+{
+    const Rows z = rows(c, c.args[0], "logits");
+    if (z.t.dim() != 2) throw Refused("logits must be two-dimensional");
+    const int32_t top = whole32(c.args[1], "top"), score = score_of(c.args[2]);
+    Tensor bias;
+    if (given(c.args[3])) {
+        bias = plain(c, c.args[3], "bias", at::kFloat);
+        if (bias.dim() != 1 || bias.size(0) != z.dim) throw Refused("bias must have shape [%lld]", (long long)z.dim);
+    }
+    const int32_t groups = whole32(c.args[4], "groups"), keep = whole32(c.args[5], "keep"), best = whole32(c.args[6], "best");
+    const bool renormalise = truth(c.args[7], "renormalise");
+    const float scale = real(c.args[8], "scale");
+    if (z.dim > INT32_MAX) return status(kTooLarge);
+    if (c.elsewhere()) return status(kElsewhere);
+    const int64_t slots = top > 0 ? top : 0;   // refused below
+    const Tensor experts = c.make({z.n, slots}, at::kInt), share = c.make({z.n, slots}, at::kFloat);
+    const hgb_status s = hgb_gate(c.ctx, z.p, z.type, z.stride, z.n, (int32_t)z.dim, score, (const float*)ptr(bias), groups, keep, best,
+                                  top, renormalise, scale, (int32_t*)experts.data_ptr(), (float*)share.data_ptr());
+    return s == HGB_OK ? tuple({experts, share}) : status(s);
+}
+
+// gate_backward(grad, logits, experts, score, renormalise, scale, out)
+PyObject* gate_backward(const Call& c)
+{
+    const Rows z = rows(c, c.args[1], "logits");
+    if (z.t.dim() != 2) throw Refused("logits must be two-dimensional");
+    const Tensor& grad = plain(c, c.args[0], "grad", at::kFloat);
+    const Tensor& experts = plain(c, c.args[2], "experts", at::kInt);
+    if (experts.dim() != 2 || experts.size(0) != z.n) throw Refused("experts must have shape [%lld, top]", (long long)z.n);
+    if (grad.sizes() != experts.sizes()) throw Refused("grad must have the experts' shape");
+    const int32_t score = score_of(c.args[3]);
+    const bool renormalise = truth(c.args[4], "renormalise");
+    const float scale = real(c.args[5], "scale");
+    Out out(c, c.args[6], z.t.scalar_type(), true, z.n, z.dim);
+    if (z.dim > INT32_MAX || experts.size(1) > INT32_MAX) return status(kTooLarge);
+    if (c.elsewhere()) return status(kElsewhere);
+    out.allocate(c, z.t.sizes());
+    const hgb_status s = hgb_gate_backward(c.ctx, (const float*)grad.data_ptr(), z.p, z.type, z.stride, z.n, (int32_t)z.dim, score,
+                                           (const int32_t*)experts.data_ptr(), (int32_t)experts.size(1), renormalise, scale, out.r.p,
+                                           out.r.stride);
+    return s == HGB_OK ? wrap(out.r.t) : status(s);
+}
+
+// A loss's rows, table and tokens.
+struct HeadRows {
+    Rows x, table;
+    const Tensor& token;
+    HeadRows(const Call& c, PyObject* x_, PyObject* table_, PyObject* token_, const char* name, bool slots)
+        : x(rows(c, x_, "x")), table(rows(c, table_, "table")), token(plain(c, token_, name, at::kInt))
+    {
+        if (table.t.dim() != 2) throw Refused("table must be two-dimensional");
+        same(table.t.scalar_type(), x.t.scalar_type(), "table");
+        if (table.dim != x.dim) throw Refused("table has rows of %lld values, needs %lld", (long long)table.dim, (long long)x.dim);
+        const int64_t dims = x.t.dim() - (slots ? 0 : 1);
+        if (token.dim() != dims || token.sizes().slice(0, x.t.dim() - 1) != lead())
+            throw Refused(slots ? "%s must have x's shape, with the slots last" : "%s must have x's shape, without its last dimension", name);
+        if (slots && token.size(-1) > INT32_MAX) throw Refused("%s has too many slots", name);
+    }
+    at::IntArrayRef lead() const { return x.t.sizes().slice(0, x.t.dim() - 1); }
+    const int32_t* tokens() const { return (const int32_t*)token.data_ptr(); }
+    // a float for each row
+    const Tensor& each(const Call& c, PyObject* o, const char* name) const
+    {
+        const Tensor& t = plain(c, o, name, at::kFloat);
+        if (t.sizes() != lead()) throw Refused("%s must have x's shape, without its last dimension", name);
+        return t;
+    }
+    int64_t bytes() const { return hgb_head_workspace(x.p, x.stride, table.p, table.stride, x.type, x.n, table.n, x.dim); }
+    int64_t grad_bytes(int type) const
+    {
+        return hgb_head_backward_workspace(x.p, x.stride, table.p, table.stride, x.type, type, x.n, table.n, x.dim);
+    }
+};
+
+// A teacher's logits, one for each token.
+struct Teacher {
+    const Tensor& t;
+    int type;
+    Teacher(const Call& c, PyObject* o, const HeadRows& h) : t(tensor(c, o, "teacher")), type(code(t.scalar_type(), "teacher"))
+    {
+        if (t.scalar_type() != at::kFloat) same(t.scalar_type(), h.x.t.scalar_type(), "teacher");
+        if (!t.is_contiguous()) throw Refused("teacher must be contiguous");
+        if (t.sizes() != h.token.sizes()) throw Refused("teacher must have the tokens' shape");
+    }
+};
+
+// cross_entropy(x, table, targets, scale, pad)
+PyObject* cross_entropy(const Call& c)
+{
+    const HeadRows h(c, c.args[0], c.args[1], c.args[2], "targets", false);
+    const float scale = real(c.args[3], "scale");
+    const int32_t pad = whole32(c.args[4], "pad");
+    const int64_t bytes = h.bytes();
+    if (bytes < 0) return status(kTooLarge);
+    if (c.elsewhere()) return status(kElsewhere);
+    const Tensor loss = c.make(h.lead(), at::kFloat), lse = c.make(h.lead(), at::kFloat), ws = c.workspace(bytes);
+    const hgb_status s = hgb_cross_entropy(c.ctx, h.x.p, h.x.type, h.x.stride, h.x.n, h.x.dim, h.table.p, h.table.stride, h.table.n,
+                                           h.tokens(), pad, scale, (float*)loss.data_ptr(), (float*)lse.data_ptr(), ptr(ws), bytes);
+    return s == HGB_OK ? tuple({loss, lse}) : status(s);
+}
+
+// cross_entropy_backward(grad, x, table, targets, lse, scale, pad, dtype, out)
+PyObject* cross_entropy_backward(const Call& c)
+{
+    const HeadRows h(c, c.args[1], c.args[2], c.args[3], "targets", false);
+    const Tensor &grad = h.each(c, c.args[0], "grad"), &lse = h.each(c, c.args[4], "lse");
+    const float scale = real(c.args[5], "scale");
+    const int32_t pad = whole32(c.args[6], "pad");
+    Out dtable(c, Py_None, dtype(c.args[7], h.x.t.scalar_type()), false, h.table.n, h.x.dim);
+    Out out(c, c.args[8], h.x.t.scalar_type(), true, h.x.n, h.x.dim);
+    const int64_t bytes = h.grad_bytes(dtable.r.type);
+    if (bytes < 0) return status(kTooLarge);
+    if (c.elsewhere()) return status(kElsewhere);
+    dtable.allocate(c, {h.table.n, h.x.dim});
+    out.allocate(c, h.x.t.sizes());
+    const Tensor ws = c.workspace(bytes);
+    const hgb_status s = hgb_cross_entropy_backward(
+        c.ctx, (const float*)grad.data_ptr(), h.x.p, h.x.type, h.x.stride, h.x.n, h.x.dim, h.table.p, h.table.stride, h.table.n,
+        h.tokens(), pad, scale, (const float*)lse.data_ptr(), out.r.p, out.r.stride, dtable.r.p, dtable.r.type, dtable.r.stride, ptr(ws),
+        bytes);
+    return s == HGB_OK ? tuple({out.r.t, dtable.r.t}) : status(s);
+}
+
+// distill(x, table, tokens, teacher, temperature)
+PyObject* distill(const Call& c)
+{
+    const HeadRows h(c, c.args[0], c.args[1], c.args[2], "tokens", true);
+    const Teacher teacher(c, c.args[3], h);
+    const float heat = real(c.args[4], "temperature");
+    const int64_t bytes = h.bytes();
+    if (bytes < 0) return status(kTooLarge);
+    if (c.elsewhere()) return status(kElsewhere);
+    const Tensor loss = c.make(h.lead(), at::kFloat), lse = c.make(h.lead(), at::kFloat), picked = c.make(h.token.sizes(), at::kFloat);
+    const Tensor ws = c.workspace(bytes);
+    const hgb_status s = hgb_distill(c.ctx, h.x.p, h.x.type, h.x.stride, h.x.n, h.x.dim, h.table.p, h.table.stride, h.table.n, h.tokens(),
+                                     teacher.t.data_ptr(), teacher.type, (int32_t)h.token.size(-1), heat, (float*)loss.data_ptr(),
+                                     (float*)lse.data_ptr(), (float*)picked.data_ptr(), ptr(ws), bytes);
+    return s == HGB_OK ? tuple({loss, lse, picked}) : status(s);
+}
+
+// distill_backward(grad, x, table, tokens, teacher, lse, picked, temperature, dtype, out)
+PyObject* distill_backward(const Call& c)
+{
+    const HeadRows h(c, c.args[1], c.args[2], c.args[3], "tokens", true);
+    const Teacher teacher(c, c.args[4], h);
+    const Tensor &grad = h.each(c, c.args[0], "grad"), &lse = h.each(c, c.args[5], "lse");
+    const Tensor& picked = plain(c, c.args[6], "picked", at::kFloat);
+    if (picked.sizes() != h.token.sizes()) throw Refused("picked must have the tokens' shape");
+    const float heat = real(c.args[7], "temperature");
+    Out dtable(c, Py_None, dtype(c.args[8], h.x.t.scalar_type()), false, h.table.n, h.x.dim);
+    Out out(c, c.args[9], h.x.t.scalar_type(), true, h.x.n, h.x.dim);
+    const int64_t bytes = h.grad_bytes(dtable.r.type);
+    if (bytes < 0) return status(kTooLarge);
+    if (c.elsewhere()) return status(kElsewhere);
+    dtable.allocate(c, {h.table.n, h.x.dim});
+    out.allocate(c, h.x.t.sizes());
+    const Tensor ws = c.workspace(bytes);
+    const hgb_status s = hgb_distill_backward(
+        c.ctx, (const float*)grad.data_ptr(), h.x.p, h.x.type, h.x.stride, h.x.n, h.x.dim, h.table.p, h.table.stride, h.table.n,
+        h.tokens(), teacher.t.data_ptr(), teacher.type, (int32_t)h.token.size(-1), heat, (const float*)lse.data_ptr(),
+        (const float*)picked.data_ptr(), out.r.p, out.r.stride, dtable.r.p, dtable.r.type, dtable.r.stride, ptr(ws), bytes);
+    return s == HGB_OK ? tuple({out.r.t, dtable.r.t}) : status(s);
+}
+
 // The Python function of a verb: (handle, device, stream id, its COUNT arguments).
 template <PyObject* (*F)(const Call&), int COUNT>
 PyObject* verb(PyObject*, PyObject* const* args, Py_ssize_t count)
@@ -474,6 +650,12 @@ PyMethodDef methods[] = {
     method<route_gather_backward, 4>("route_gather_backward"),
     method<route_combine, 5>("route_combine"),
     method<route_combine_backward, 6>("route_combine_backward"),
+    method<gate, 9>("gate"),
+    method<gate_backward, 7>("gate_backward"),
+    method<cross_entropy, 5>("cross_entropy"),
+    method<cross_entropy_backward, 9>("cross_entropy_backward"),
+    method<distill, 5>("distill"),
+    method<distill_backward, 10>("distill_backward"),
     {nullptr, nullptr, 0, nullptr},
 };
 

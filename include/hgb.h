@@ -461,9 +461,11 @@ hgb_status hgb_grow_level(hgb_ctx* ctx, const int64_t* parent_hist_dev, const hg
  * The vector verbs: learned vectors beside the trees.  A binned row is a list
  * of tokens (a bin of a feature, or the leaf a tree sends the row to); a model
  * on top of them looks up a vector for each token (hgb_embed), normalises the
- * rows (hgb_layer_norm) and sends each row to some of its experts, a tree's
- * leaves for instance, and back (hgb_route and the verbs after it).  Each has
- * its gradient.  No page describes them; the definitions stand here.
+ * rows (hgb_layer_norm), picks each row's experts (hgb_gate), sends each row to
+ * its experts, a tree's leaves for instance, and back (hgb_route and the verbs
+ * after it), and answers with a softmax over all tokens, learning from the
+ * row's own next one (hgb_cross_entropy) or from a teacher's (hgb_distill).
+ * Each has its gradient.  No page describes them; the definitions stand here.
  *
  * Conventions, besides those at the top:
  *   - A context needs no upload_bins or begin_tree for them.
@@ -619,6 +621,152 @@ hgb_status hgb_route_combine_backward(hgb_ctx* ctx, const void* grad_dev, int32_
                                       const float* weight_dev, void* dy_dev, int64_t dy_stride, float* dweight_dev);
 
 /*
+ * The experts of each row and their shares, from the row's logits z.  The
+ * score of expert e is s = softmax(z)[e] or 1 / (1 + exp(-z[e])), its key
+ * s + bias[e].  Where groups > 1, the experts are `groups` equal runs; a group
+ * is worth the sum of its `best` largest keys, and only the experts of the
+ * `keep` groups worth most are eligible.  The row's experts are the `top`
+ * eligible ones with the largest keys, largest first; ties, between groups
+ * too, go to the lower index.  Keys closer than the error of 32 bits are
+ * compared in 64.
+ *   share = scale * s, or with renormalise scale * s / the sum of the chosen s
+ *
+ * An expert whose logit or bias is -infinity is masked: its key is -infinity
+ * (also in its group's worth), it is never chosen, and its softmax is 0 where
+ * the logit is.  So is one whose logit or bias is NaN or +infinity, which the
+ * next hgb_sync reports.  Where fewer than `top` experts are left, the slots
+ * behind them get expert -1 (dropped by hgb_route) and share 0.
+ *
+ * logits_dev: [n_rows][n_experts], rows `stride` apart, type `type`.
+ * score:      an hgb_score.  bias_dev: float [n_experts], or NULL for zeros.
+ * experts_dev, share_dev: int32 and float [n_rows][top].
+ * Errors: HGB_E_INVALID for null or misaligned pointers, n_rows outside
+ *         [0, 2^31), n_rows * top above 2^31 - 1, an unknown score, groups that
+ *         do not divide n_experts, keep outside [1, groups], best other than 1
+ *         or 2 or above a group's experts, top below one or above the eligible
+ *         experts, a scale that is not finite; HGB_E_UNSUPPORTED for n_experts
+ *         above 1,023 or top above 64.
+ */
+typedef enum {
+    HGB_SOFTMAX = 0,
+    HGB_SIGMOID = 1
+} hgb_score;
+
+hgb_status hgb_gate(hgb_ctx* ctx, const void* logits_dev, int32_t type, int64_t stride, int64_t n_rows, int32_t n_experts,
+                    int32_t score, const float* bias_dev, int32_t groups, int32_t keep, int32_t best, int32_t top,
+                    int32_t renormalise, float scale, int32_t* experts_dev, float* share_dev);
+
+/*
+ * The logits' gradient from the shares': which experts are chosen counts as
+ * given (the bias has no gradient).  All of dlogits is written: zeros for
+ * masked experts, and for those not chosen, except where the shares are the
+ * softmax itself (renormalise 0), which every logit changes.
+ *
+ * grad_dev:    float [n_rows][top], of the shares.
+ * experts_dev: int32 [n_rows][top], as hgb_gate wrote them; the slots of -1
+ *              are left out, and so are those of any other value outside
+ *              [0, n_experts), which the next hgb_sync reports.  An expert that
+ *              is named twice in a row counts twice.
+ * logits_dev, dlogits_dev: [n_rows][n_experts] of type `type`.
+ * Errors: as for hgb_gate.
+ */
+hgb_status hgb_gate_backward(hgb_ctx* ctx, const float* grad_dev, const void* logits_dev, int32_t type, int64_t stride,
+                             int64_t n_rows, int32_t n_experts, int32_t score, const int32_t* experts_dev, int32_t top,
+                             int32_t renormalise, float scale, void* dlogits_dev, int64_t dlogits_stride);
+
+/*
+ * The cross entropy of each row's target under a softmax over the vocabulary:
+ *   z[i][v] = scale * <x[i], table[v]>,  lse[i] = log of the sum of exp(z[i][v])
+ *   loss[i] = lse[i] - z[i][target[i]]
+ * The logits z are not kept: a block of kernels' tile of them lives in
+ * registers.  Products are of the inputs' type, sums of 32-bit floats.
+ *
+ * x_dev:       [n_rows][dim], rows x_stride apart; table_dev: [vocab][dim],
+ *              rows table_stride apart, both of type `type`.
+ * targets_dev: int32 [n_rows].  A row whose target is `pad` has loss 0 and no
+ *              gradient; so has one with any other target outside [0, vocab),
+ *              which the next hgb_sync reports.
+ * loss_dev, lse_dev: float [n_rows]; lse is written for every row.
+ * workspace:   hgb_head_workspace bytes.  Rows of x or table that do not all
+ *              start at 16 bytes, or end inside 16, are copied there first.
+ * A row with a logit that is NaN or +infinity has no finite loss.
+ * Errors: HGB_E_INVALID for null or misaligned pointers, n_rows below 0, vocab
+ *         or dim below 1, strides below dim, a scale that is not finite, a
+ *         workspace too small; HGB_E_UNSUPPORTED for n_rows or vocab above
+ *         2^24 or dim above 32,768.
+ */
+hgb_status hgb_cross_entropy(hgb_ctx* ctx, const void* x_dev, int32_t type, int64_t x_stride, int64_t n_rows, int64_t dim,
+                             const void* table_dev, int64_t table_stride, int64_t vocab, const int32_t* targets_dev,
+                             int32_t pad, float scale, float* loss_dev, float* lse_dev, void* workspace_dev,
+                             int64_t workspace_bytes);
+
+/* Of hgb_cross_entropy and hgb_distill called with these arguments, and of
+ * their gradients; -1 for sizes that they refuse. */
+int64_t hgb_head_workspace(const void* x_dev, int64_t x_stride, const void* table_dev, int64_t table_stride, int32_t type,
+                           int64_t n_rows, int64_t vocab, int64_t dim);
+int64_t hgb_head_backward_workspace(const void* x_dev, int64_t x_stride, const void* table_dev, int64_t table_stride,
+                                    int32_t type, int32_t dtable_type, int64_t n_rows, int64_t vocab, int64_t dim);
+
+/*
+ * Gradients of the sum of grad[i] * loss[i].  With q = exp(z - lse) and 1 at
+ * the target,
+ *   dz[i] = scale * grad[i] * (q[i] - 1),  dx = dz table,  dtable = dz^T x
+ * in pieces of the vocabulary: a piece of dz, computed again from x and table,
+ * is the most that the workspace holds of it.  dz is rounded to the inputs'
+ * type as a factor of the two products (beside a 32-bit dtable of 16-bit
+ * inputs, to twice its bits for dtable).  What x holds in rows without a
+ * gradient reaches nothing; dx is zero there.
+ *
+ * grad_dev:   float [n_rows].  lse_dev: as hgb_cross_entropy wrote it.
+ * dx_dev:     [n_rows][dim] of type `type`.
+ * dtable_dev: [vocab][dim] of type dtable_type, `type` or HGB_F32.
+ * Errors: as for hgb_cross_entropy; HGB_E_UNSUPPORTED for another dtable_type.
+ */
+hgb_status hgb_cross_entropy_backward(hgb_ctx* ctx, const float* grad_dev, const void* x_dev, int32_t type, int64_t x_stride,
+                                      int64_t n_rows, int64_t dim, const void* table_dev, int64_t table_stride,
+                                      int64_t vocab, const int32_t* targets_dev, int32_t pad, float scale,
+                                      const float* lse_dev, void* dx_dev, int64_t dx_stride, void* dtable_dev,
+                                      int32_t dtable_type, int64_t dtable_stride, void* workspace_dev,
+                                      int64_t workspace_bytes);
+
+/*
+ * Distillation from a teacher's top logits at temperature T:
+ *   z[i][v] = <x[i], table[v]> / T,  lse as above,  log q = z - lse
+ *   p[i][k] = softmax over the row's slots of teacher[i][k] / T
+ *   loss[i] = T^2 * the sum over k of p[i][k] (log p[i][k] - log q[i][tokens[i][k]])
+ *
+ * tokens_dev:  int32 [n_rows][top].  A slot of token -1 is left out; so is one
+ *              of any other token outside [0, vocab), which the next hgb_sync
+ *              reports, and one whose teacher logit is -infinity (p = 0).  A
+ *              row with no slot left has loss 0 and no gradient.  A token may
+ *              stand in several slots.
+ * teacher_dev: [n_rows][top] of type teacher_type, `type` or HGB_F32.
+ * picked_dev:  float [n_rows][top]; written: z at the slots' tokens, 0 for a
+ *              slot that is left out for its token.
+ * Errors: as for hgb_cross_entropy, and HGB_E_INVALID for a temperature that is
+ *         not positive and finite, top below 1; HGB_E_UNSUPPORTED for top above
+ *         256 or another teacher_type.
+ */
+hgb_status hgb_distill(hgb_ctx* ctx, const void* x_dev, int32_t type, int64_t x_stride, int64_t n_rows, int64_t dim,
+                       const void* table_dev, int64_t table_stride, int64_t vocab, const int32_t* tokens_dev,
+                       const void* teacher_dev, int32_t teacher_type, int32_t top, float temperature, float* loss_dev,
+                       float* lse_dev, float* picked_dev, void* workspace_dev, int64_t workspace_bytes);
+
+/*
+ * Its gradients, with P[i][v] = the sum of p[i][k] over the slots of token v:
+ *   dz[i] = T * grad[i] * (q[i] - P[i]),  dx = dz table,  dtable = dz^T x
+ * as hgb_cross_entropy_backward computes them.  The teacher has none.
+ * lse_dev, picked_dev: as hgb_distill wrote them.
+ * Errors: as for hgb_distill and hgb_cross_entropy_backward.
+ */
+hgb_status hgb_distill_backward(hgb_ctx* ctx, const float* grad_dev, const void* x_dev, int32_t type, int64_t x_stride,
+                                int64_t n_rows, int64_t dim, const void* table_dev, int64_t table_stride, int64_t vocab,
+                                const int32_t* tokens_dev, const void* teacher_dev, int32_t teacher_type, int32_t top,
+                                float temperature, const float* lse_dev, const float* picked_dev, void* dx_dev,
+                                int64_t dx_stride, void* dtable_dev, int32_t dtable_type, int64_t dtable_stride,
+                                void* workspace_dev, int64_t workspace_bytes);
+
+/*
  * Per-kernel device timing ([bonsai-10] "The kernel": the pages' backend
  * prints an upload / gpu / unpack breakdown when asked).  When enabled, every
  * launch is bracketed by HIP events on the context's stream.
@@ -638,7 +786,9 @@ typedef enum {
     HGB_KERNEL_EMBED = 10,     /* embed and embed_backward, each call */
     HGB_KERNEL_NORM = 11,      /* layer_norm and layer_norm_backward, each call */
     HGB_KERNEL_ROUTE = 12,     /* the route verbs, each call */
-    HGB_KERNEL_COUNT = 13
+    HGB_KERNEL_GATE = 13,      /* gate and gate_backward, each call */
+    HGB_KERNEL_HEAD = 14,      /* cross_entropy, distill and their gradients, each call */
+    HGB_KERNEL_COUNT = 15
 } hgb_kernel;
 
 /* Turn timing on (nonzero) or off, and reset the counters. */
