@@ -219,7 +219,7 @@ hgb_status run_backward(hgb_ctx* c, const Head& h, const HeadGrad& o, const Head
         z.k_steps = (int)vec_ceil(h.dim, STEP);
         z.planes = 1;
         z.first = (int)first;
-        z.scale = h.scale * kLog2e;
+        z.scale = h.scale;
         z.target = h.teacher ? nullptr : h.token;
         z.lse = o.lse;
         z.rate = rate;

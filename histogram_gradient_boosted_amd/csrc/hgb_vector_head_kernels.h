@@ -22,6 +22,9 @@ namespace hgb {
 constexpr float kLog2e = 1.44269504088896340736f;
 constexpr float kLn2 = 0.69314718055994530942f;
 
+// A value that all lanes have, for the compiler to keep as one.
+__device__ inline int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
+
 // A factor of a product, rows of 16-byte chunks.  Along the rows ("by k"
 // false): row m holds the values that are summed; by k: row k holds the value
 // k of every m.
@@ -43,7 +46,7 @@ struct ProductArgs {
     int first;           // row of x, or token, that C's first row or column stands for
 
     // z and dz
-    float scale;         // of the logits, times log2(e)
+    float scale;         // of the logits (kStats: times log2(e))
     int limit;           // C's columns beyond this are no tokens
     const int32_t* target;
     float2* part;        // [n_part][m]: maxima and sums
@@ -97,7 +100,7 @@ __device__ inline Acc mma(const Frag<float>::type& a, const Frag<float>::type& b
 
 // 64 lanes' 16 bytes each, from memory to consecutive places in LDS.  An
 // offset past the descriptor's bytes gives zeros.
-__device__ inline void load_lds(uint32_t lds, uint32_t offset, const Rsrc& r)
+__device__ __forceinline__ void load_lds(uint32_t lds, uint32_t offset, const Rsrc& r)
 {
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(lds), "v"(offset), "s"(r)
                  : "memory");
@@ -120,55 +123,79 @@ __device__ inline int by_k_place(int k, int chunk)
     return bytes >= 256 ? chunk ^ ((k & 3) << 2) : bytes == 128 ? chunk ^ (((k >> 1) & 1) << 2) : chunk;
 }
 
-// Loads a factor's tile of R rows (by k: columns), a step at a time.
+// Loads a factor's tile of R rows (by k: columns), a step at a time: a wave's N
+// loads of a step one by one, then next().  Past the last step zeros are loaded.
 template <typename T, int R, int WAVES, bool BY_K>
 struct Loader {
     static constexpr int N = R / 8 / WAVES;   // loads of a wave
-    static constexpr int STEP = kStepBytes / (int)sizeof(T);
+    static constexpr int SIZE = sizeof(T), STEP = kStepBytes / SIZE;
     uint32_t offset[N];
-    int tail[N];   // a chunk's first value of the step
+    int tail[2];       // along: the first value of the lane's chunk in the step, of even and odd loads
+    const char* base;  // of the step
+    int64_t left;      // bytes from there to the factor's end
+    int64_t step, back;   // bytes from a step to the next, and from a plane's last step to the next plane's first
+    int live;          // along: values of the rows from the step on
+    int cols, k, steps, to_go;
 
-    __device__ void init(const Factor& f, int64_t first, int wave, int lane)
+    // the steps [t0, t1) of all the planes'
+    __device__ __forceinline__ void init(const Factor& f, int64_t first, int wave, int lane, int k_steps, int64_t plane, int t0, int t1)
     {
 #pragma unroll
         for (int i = 0; i < N; ++i) {
             const int at = (wave * N + i) * 1024 + lane * 16;
             if (BY_K) {
-                constexpr int row_bytes = R * (int)sizeof(T);
-                const int k = at / row_bytes, chunk = by_k_place<T, R>(k, at % row_bytes / 16);
-                const int64_t col = first + chunk * (16 / (int)sizeof(T));
-                offset[i] = col < f.cols ? (uint32_t)(k * f.stride * (int)sizeof(T) + chunk * 16) : kNowhere;
-                tail[i] = 0;
+                constexpr int row_bytes = R * SIZE;
+                const int kk = at / row_bytes, chunk = by_k_place<T, R>(kk, at % row_bytes / 16);
+                const int64_t col = first + chunk * (16 / SIZE);
+                offset[i] = col < f.cols ? (uint32_t)(kk * f.stride * SIZE + chunk * 16) : kNowhere;
             } else {
                 const int row = at / kStepBytes, chunk = along_place(row, at % kStepBytes / 16);
-                offset[i] = (uint32_t)(row * f.stride * (int)sizeof(T) + chunk * 16);
-                tail[i] = chunk * (16 / (int)sizeof(T));
+                offset[i] = (uint32_t)(row * f.stride * SIZE + chunk * 16);
+                tail[i & 1] = chunk * (16 / SIZE);
+                static_assert(R / 8 % 2 == 0 && (N % 2 == 0 || N == 1), "chunks go by a load's parity");
             }
         }
+        steps = k_steps;
+        const int at_plane = uniform(t0 / k_steps);
+        k = t0 - at_plane * k_steps;
+        to_go = t1 - t0;
+        step = BY_K ? STEP * f.stride * SIZE : kStepBytes;
+        back = plane * SIZE - step * (k_steps - 1);
+        const int64_t row = BY_K ? (int64_t)k * STEP : first, col = BY_K ? first : (int64_t)k * STEP;
+        base = (const char*)f.p + (at_plane * plane + row * f.stride + col) * SIZE;
+        left = ((f.rows - 1 - row) * f.stride + f.cols - col) * SIZE;
+        cols = (int)f.cols;
+        live = cols - k * STEP;
     }
 
-    // step `k` of plane `plane`, to `lds` (of the wave's part)
-    __device__ void load(const Factor& f, int64_t first, int plane, int k, uint32_t lds) const
+    // the wave's load i to its place from `lds` on
+    __device__ __forceinline__ void load(int i, uint32_t lds) const
     {
-        const int64_t k0 = (int64_t)k * STEP;
-        const int64_t row = BY_K ? k0 : first, col = BY_K ? first : k0;
-        const char* base = (const char*)f.p + (plane * f.plane + row * f.stride + col) * (int)sizeof(T);
-        const int64_t left = ((f.rows - 1 - row) * f.stride + f.cols - col) * (int)sizeof(T);
-        const uint32_t bytes = (uint32_t)min(left, (int64_t)0x7ffffff0);
         const uint64_t b = (uint64_t)base;
-        const Rsrc r = {(int)(uint32_t)b, (int)((uint32_t)(b >> 32) & 0xffffu), (int)bytes, 0x00027000};
-        const int64_t live = f.cols - col;
-#pragma unroll
-        for (int i = 0; i < N; ++i) {
-            const uint32_t o = BY_K || tail[i] < live ? offset[i] : kNowhere;
-            load_lds(lds + i * 1024, o, r);
+        const uint32_t bytes = to_go > 0 ? (uint32_t)min(left, (int64_t)0x7ffffff0) : 0;
+        const Rsrc r = {uniform((int)(uint32_t)b), uniform((int)((uint32_t)(b >> 32) & 0xffffu)), uniform((int)bytes), 0x00027000};
+        load_lds(lds + i * 1024, BY_K || tail[i & 1] < live ? offset[i] : kNowhere, r);
+    }
+
+    __device__ __forceinline__ void next()
+    {
+        --to_go;
+        if (++k == steps) {
+            k = 0;
+            base += back;
+            left += step * (steps - 1);
+            live = cols;
+        } else {
+            base += step;
+            left -= step;
+            live -= STEP;
         }
     }
 };
 
 // Lane's part of 32 rows (columns) of a tile in LDS, sub-step s of the step.
 template <typename T, int R, bool BY_K>
-__device__ inline typename Frag<T>::type fragment(const char* tile, int block, int s, int lane)
+__device__ __forceinline__ typename Frag<T>::type fragment(const char* tile, int block, int s, int lane)
 {
     typename Frag<T>::type v;
     if (!BY_K) {
@@ -205,6 +232,37 @@ __device__ inline float swap_halves(float x)
     return __uint_as_float((threadIdx.x & 32) ? v[0] : v[1]);
 }
 
+// A wave's 32 rows of TN * 32 columns, as the matrix instructions leave them (a
+// lane has a row's values, four side by side), to memory by whole rows: through
+// the wave's own part of LDS, so that a store takes runs of 128 bytes and more.
+// Stored straight from the registers, 8 bytes here and there, the logits'
+// gradient of 8,192 x 32,768 took twice as long as its product.
+template <typename T, int TN>
+__device__ __forceinline__ void store_strip(const Acc (&acc)[TN], char* strip, int lane, int rows, T* out, int64_t stride)
+{
+    constexpr int V = 16 / sizeof(T), CHUNKS = TN * 32 / V, ROW = CHUNKS * 16;
+    auto place = [](int row, int chunk) { return row * ROW + (chunk ^ (CHUNKS >= 16 ? row & (CHUNKS - 1) : (row >> 1) & 7)) * 16; };
+    const int row = lane & 31, half = lane >> 5;
+    wave_order();
+#pragma unroll
+    for (int j = 0; j < TN; ++j)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            const int col = j * 32 + q * 8 + half * 4;
+            typedef T Four __attribute__((ext_vector_type(4)));
+            Four v;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v[e] = (T)acc[j][4 * q + e];
+            *(Four*)(strip + place(row, col / V) + col % V * (int)sizeof(T)) = v;
+        }
+    wave_order();
+#pragma unroll
+    for (int k = 0; k < 32 * CHUNKS / 64; ++k) {
+        const int at = k * 64 + lane, r = at / CHUNKS, chunk = at % CHUNKS;
+        if (r < rows) *(uint4*)(out + r * stride + chunk * V) = *(const uint4*)(strip + place(r, chunk));
+    }
+}
+
 // A block's tile of C.
 struct TilePlace {
     int m, n, split;
@@ -219,7 +277,7 @@ __device__ inline TilePlace tile_place(const ProductArgs& g)
     const uint32_t at = xcd * per + min(xcd, more) + blockIdx.x / 8;
     const uint32_t tile = at % tiles, width = 8 * (uint32_t)g.tiles_n, band = tile / width, first = band * 8;
     const uint32_t rows = min(8u, (uint32_t)g.tiles_m - first), in = tile % width;
-    return {(int)(first + in % rows), (int)(in / rows), (int)(at / tiles)};
+    return {uniform((int)(first + in % rows)), uniform((int)(in / rows)), uniform((int)(at / tiles))};
 }
 
 // One product: C = a b over the tiles.  A block of WM x WN waves makes a tile
@@ -233,25 +291,24 @@ __global__ __launch_bounds__(64 * WM * WN) void k_product(const ProductArgs g)
     constexpr int STAGE = (BM + BN) * kStepBytes;
     constexpr bool LANE_IS_ROW = WHAT == kStats || WHAT == kGrad;   // else a lane holds a column's values
     extern __shared__ __align__(16) char smem[];
-    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
     const int wm = wave / WN, wn = wave % WN;
     const TilePlace at = tile_place(g);
     const int64_t row0 = (int64_t)at.m * BM, col0 = (int64_t)at.n * BN;
     const int steps = g.k_steps * g.planes;
-    const int t0 = (int)((int64_t)steps * at.split / g.splits), t1 = (int)((int64_t)steps * (at.split + 1) / g.splits);
+    const int t0 = uniform((int)((int64_t)steps * at.split / g.splits)), t1 = uniform((int)((int64_t)steps * (at.split + 1) / g.splits));
 
     Loader<T, BM, WAVES, A_BY_K> la;
     Loader<T, BN, WAVES, B_BY_K> lb;
-    la.init(g.a, row0, wave, lane);
-    lb.init(g.b, col0, wave, lane);
+    la.init(g.a, row0, wave, lane, g.k_steps, g.a.plane, t0, t1);
+    lb.init(g.b, col0, wave, lane, g.k_steps, 0, t0, t1);
     const uint32_t lds = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) char*)smem;
     const uint32_t lds_a = lds + wave * (la.N * 1024), lds_b = lds + BM * kStepBytes + wave * (lb.N * 1024);
-    auto load = [&](int t) {
-        const uint32_t half = (t & 1) * STAGE;
-        const int plane = t / g.k_steps, k = t - plane * g.k_steps;
-        la.load(g.a, row0, plane, k, lds_a + half);
-        lb.load(g.b, col0, 0, k, lds_b + half);
+    auto load = [&](int i, uint32_t half) {   // one of a step's loads
+        if (i < la.N) la.load(i, lds_a + half);
+        else lb.load(i - la.N, lds_b + half);
     };
+    constexpr int LOADS = la.N + lb.N, FIRST = LOADS / 2;
 
     Acc acc[TM][TN];
 #pragma unroll
@@ -261,26 +318,68 @@ __global__ __launch_bounds__(64 * WM * WN) void k_product(const ProductArgs g)
 #pragma unroll
             for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.0f;
 
-    if (t0 < t1) load(t0);
+    // A step is four sub-steps; each sub-step's fragments are read while the
+    // one before is multiplied.  Before the last sub-step every wave has read
+    // its half of LDS and the other half's loads are in: one barrier a step,
+    // after which the half just read is filled for the step after the next.
+    // The loads take two sub-steps, the last of this step and the first of the
+    // next: 64 KB at 64 bytes a cycle are 1,024 cycles, two sub-steps' products.
+    // (All in the one: 1,120 against 1,097 us, 16,384 x 32,768 x 1,024.)
+    typename Frag<T>::type fa[2][TM], fb[2][TN];
+    auto read = [&](int i, int half, int s, int to) {   // one of a sub-step's fragments
+        const char* tile = smem + half * STAGE;
+        if (i < TM) fa[to][i] = fragment<T, BM, A_BY_K>(tile, wm * TM + i, s, lane);
+        else fb[to][i - TM] = fragment<T, BN, B_BY_K>(tile + BM * kStepBytes, wn * TN + i - TM, s, lane);
+    };
+    if (t0 < t1) {
+#pragma unroll
+        for (int i = 0; i < LOADS; ++i) load(i, 0);
+        la.next();
+        lb.next();
+#pragma unroll
+        for (int i = 0; i < FIRST; ++i) load(i, STAGE);
+        asm volatile("s_waitcnt vmcnt(%0)" ::"n"(FIRST) : "memory");
+        __builtin_amdgcn_s_barrier();
+        asm volatile("" ::: "memory");
+#pragma unroll
+        for (int i = 0; i < TM + TN; ++i) read(i, 0, 0, 0);
+    }
     for (int t = t0; t < t1; ++t) {
-        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-        __syncthreads();
-        if (t + 1 < t1) load(t + 1);
-        const char* ta = smem + (t & 1) * STAGE;
-        const char* tb = ta + BM * kStepBytes;
+        const int half = (t - t0) & 1;
 #pragma unroll
         for (int s = 0; s < 4; ++s) {
-            typename Frag<T>::type fa[TM], fb[TN];
+            if (s == 3) {
+                asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+                __builtin_amdgcn_s_barrier();
+                asm volatile("" ::: "memory");
+            }
+            // between the sub-step's products: the next one's fragments, and after the barrier the loads
+            constexpr int MMAS = TM * TN, READS = TM + TN;
 #pragma unroll
-            for (int i = 0; i < TM; ++i) fa[i] = fragment<T, BM, A_BY_K>(ta, wm * TM + i, s, lane);
+            for (int n = 0; n < MMAS; ++n) {
+                const int i = n / TN, j = n % TN;
+                acc[i][j] = LANE_IS_ROW ? mma(fb[s & 1][j], fa[s & 1][i], acc[i][j]) : mma(fa[s & 1][i], fb[s & 1][j], acc[i][j]);
 #pragma unroll
-            for (int j = 0; j < TN; ++j) fb[j] = fragment<T, BN, B_BY_K>(tb, wn * TN + j, s, lane);
+                for (int r = n * READS / MMAS; r < (n + 1) * READS / MMAS; ++r)
+                    read(r, s == 3 ? half ^ 1 : half, (s + 1) & 3, (s + 1) & 1);
+                if (s == 3) {
 #pragma unroll
-            for (int i = 0; i < TM; ++i)
+                    for (int l = n * FIRST / MMAS; l < (n + 1) * FIRST / MMAS; ++l) load(l, half * STAGE);
+                }
+                if (s == 0) {
 #pragma unroll
-                for (int j = 0; j < TN; ++j) acc[i][j] = LANE_IS_ROW ? mma(fb[j], fa[i], acc[i][j]) : mma(fa[i], fb[j], acc[i][j]);
+                    for (int l = n * (LOADS - FIRST) / MMAS; l < (n + 1) * (LOADS - FIRST) / MMAS; ++l)
+                        load(FIRST + l, (half ^ 1) * STAGE);
+                }
+                __builtin_amdgcn_sched_barrier(0);
+            }
+            if (s == 0) {
+                la.next();
+                lb.next();
+            }
         }
     }
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");   // LDS is written to no longer
 
     // Value r of a 32 x 32 block's lane: the lane's row (column) is lane % 32,
     // the other place 8 (r / 4) + 4 (lane / 32) + r % 4.
@@ -326,55 +425,60 @@ __global__ __launch_bounds__(64 * WM * WN) void k_product(const ProductArgs g)
         }
     } else if constexpr (WHAT == kGrad) {
         const float unit = g.unit[0];
+        __syncthreads();   // the tiles in LDS are read
+        char* strip = smem + wave * (32 * TN * 32 * (int)sizeof(T));
 #pragma unroll
         for (int i = 0; i < TM; ++i) {
             const int64_t row = m0 + i * 32 + (lane & 31);
             const bool live = row < g.m;
             const float rate = live ? g.rate[row] * unit : 0.0f;
-            const float lse = live ? g.lse[row] * kLog2e : 0.0f;
+            const float lse = live ? g.lse[row] : 0.0f;
             const int64_t target = live && g.target ? (int64_t)g.target[row] - g.first : -1;
 #pragma unroll
             for (int j = 0; j < TN; ++j)
 #pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    const int64_t col = n0 + j * 32 + 8 * q + half;
-                    float v[4];
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const float p = __builtin_amdgcn_exp2f(__builtin_fmaf(acc[i][j][4 * q + e], g.scale, -lse));
-                        const float d = rate * (col + e == target ? p - 1.0f : p);
-                        v[e] = rate != 0.0f && col + e < g.limit ? d : 0.0f;
-                    }
-                    if (live) {
-                        T* to = (T*)g.dz + row * g.dz_stride + col;
-                        store_vals<4>(v, to, 4);
-                        if (g.dz_plane) {
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) v[e] -= (float)(T)v[e];
-                            store_vals<4>(v, to + g.dz_plane, 4);
-                        }
-                    }
+                for (int r = 0; r < 16; ++r) {
+                    const int64_t col = n0 + j * 32 + 8 * (r / 4) + half + r % 4;
+                    const float p = __builtin_amdgcn_exp2f(__builtin_fmaf(acc[i][j][r], g.scale, -lse) * kLog2e);
+                    const float d = rate * (col == target ? p - 1.0f : p);
+                    acc[i][j][r] = rate != 0.0f && col < g.limit ? d : 0.0f;
                 }
+            T* to = (T*)g.dz + (m0 + i * 32) * g.dz_stride + n0;
+            store_strip<T, TN>(acc[i], strip, lane, (int)min((int64_t)32, g.m - m0 - i * 32), to, g.dz_stride);
+            if (g.dz_plane) {   // what the rounding left
+#pragma unroll
+                for (int j = 0; j < TN; ++j)
+#pragma unroll
+                    for (int r = 0; r < 16; ++r) acc[i][j][r] -= (float)(T)acc[i][j][r];
+                store_strip<T, TN>(acc[i], strip, lane, (int)min((int64_t)32, g.m - m0 - i * 32), to + g.dz_plane, g.dz_stride);
+            }
         }
     } else {
         const float factor = WHAT == kOut && g.factor ? g.factor[0] : 1.0f;
+        const int64_t col = n0 + (lane & 31);
+        const int cols = (int)min((int64_t)(TN * 32), g.n - col);   // of the lane's, 32 apart
+        auto store = [&](auto* out, int64_t stride, bool add) {
 #pragma unroll
-        for (int i = 0; i < TM; ++i)
-#pragma unroll
-            for (int j = 0; j < TN; ++j)
+            for (int i = 0; i < TM; ++i) {
 #pragma unroll
                 for (int r = 0; r < 16; ++r) {
-                    const int64_t row = m0 + i * 32 + 8 * (r / 4) + half + r % 4, col = n0 + j * 32 + (lane & 31);
-                    if (row >= g.m || col >= g.n) continue;
-                    if constexpr (WHAT == kSum) {
-                        float* to = g.sum + ((int64_t)at.split * g.m + row) * g.sum_stride + col;
-                        *to = g.add ? *to + acc[i][j][r] : acc[i][j][r];
-                    } else if (g.out_type == HGB_F32) {
-                        ((float*)g.out)[row * g.out_stride + col] = acc[i][j][r] * factor;
-                    } else {
-                        ((T*)g.out)[row * g.out_stride + col] = (T)(acc[i][j][r] * factor);
+                    const int64_t row = m0 + i * 32 + 8 * (r / 4) + half + r % 4;
+                    if (row < g.m) {
+                        auto* to = out + row * stride + col;
+#pragma unroll
+                        for (int j = 0; j < TN; ++j)
+                            if (j * 32 < cols) {
+                                const float v = acc[i][j][r] * factor;
+                                to[j * 32] = (std::remove_reference_t<decltype(*to)>)(add ? (float)to[j * 32] + v : v);
+                            }
                     }
+                    __builtin_amdgcn_sched_barrier(0);   // else all rows' addresses are made first
                 }
+            }
+        };
+        if constexpr (WHAT == kSum) store(g.sum + (int64_t)at.split * g.m * g.sum_stride, g.sum_stride, g.add);
+        else if (g.out_type == HGB_F32) store((float*)g.out, g.out_stride, false);
+        else store((T*)g.out, g.out_stride, false);
     }
 }
 

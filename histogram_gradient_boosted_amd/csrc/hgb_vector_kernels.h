@@ -69,13 +69,6 @@ __device__ inline uint2 sort_load(const SortIn& in, int64_t i, bool* bad)
     return make_uint2(live ? (uint32_t)t : (uint32_t)in.limit, (uint32_t)i);
 }
 
-__device__ inline void wave_order()
-{
-    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-    __builtin_amdgcn_wave_barrier();
-    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
-}
-
 // Ranks of a tile's digits.  Item i of lane l of wave w is element
 // w * 64 * ITEMS + i * 64 + l, so that a wave meets its elements in order.
 // rank[i]: the elements of the same digit before it in its wave; on return

@@ -79,6 +79,14 @@ __device__ inline void store_vals(const float (&r)[V], T* p, int64_t left, bool 
 // A block's number in a grid of span_blocks.
 __device__ inline uint32_t block_number() { return (blockIdx.z << kGridLog) + blockIdx.x; }
 
+// Keeps a wave's accesses to LDS before and after in order.
+__device__ inline void wave_order()
+{
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
 // x plus the value of the lane that CTRL names in its row of 16.
 template <int CTRL>
 __device__ inline float dpp_add(float x)
