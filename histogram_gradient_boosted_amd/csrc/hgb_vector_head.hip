@@ -70,12 +70,12 @@ template <typename T, int BM, int BN, int WM, int WN, bool A_BY_K, bool B_BY_K, 
 hgb_status launch_tile(hgb_ctx* c, ProductArgs g, const ProductPlan& p)
 {
     auto* kernel = k_product<T, BM, BN, WM, WN, A_BY_K, B_BY_K, WHAT>;
-    constexpr size_t lds = 2 * (BM + BN) * kStepBytes;
+    constexpr int lds = product_lds(BM, BN, WM * WN, WHAT != kStats), blocks = product_blocks(BM, BN, WM * WN, WHAT != kStats);
     if (lds > 65536) HGB_TRY(raise_lds(c, kernel));
     g.splits = p.splits;
     g.tiles_m = (int)p.tiles_m;
     g.tiles_n = (int)p.tiles_n;
-    kernel<<<(unsigned)p.blocks(), 64 * WM * WN, lds, c->stream>>>(g);
+    kernel<<<(unsigned)std::min<int64_t>(p.blocks(), (int64_t)blocks * c->n_cu), 64 * WM * WN, lds, c->stream>>>(g);
     HGB_LAUNCHED(c, "k_product");
     return HGB_OK;
 }
@@ -225,20 +225,20 @@ hgb_status run_backward(hgb_ctx* c, const Head& h, const HeadGrad& o, const Head
         z.rate = rate;
         z.unit = unit;
         z.dz = dz;
-        z.dz_stride = p.piece;
+        z.dz_stride = p.stride;
         z.dz_plane = p.planes > 1 ? p.plane : 0;
         ProductPlan zp = p.z;
         zp.tiles_n = vec_ceil(tokens, zp.bn);
         HGB_TRY((launch_product<T, false, false, kGrad>(c, z, zp)));
         if (h.teacher) {
             k_distill_dz<T><<<fill_blocks(c, h.n * 64), 256, 0, c->stream>>>(h.n, h.slots(), o.lse, o.picked, rate, unit, (int)first,
-                                                                            (int)tokens, dz, p.piece, z.dz_plane);
+                                                                            (int)tokens, dz, p.stride, z.dz_plane);
             HGB_LAUNCHED(c, "k_distill_dz");
         }
 
         // dx: the sum over the piece's tokens; the pieces' sums in one buffer
         ProductArgs x{};
-        x.a = Factor{dz, p.piece, h.n, p.piece, 0};
+        x.a = Factor{dz, p.stride, h.n, p.piece, 0};
         x.b = piece;
         x.m = (int)h.n;
         x.n = (int)h.dim;
@@ -250,7 +250,7 @@ hgb_status run_backward(hgb_ctx* c, const Head& h, const HeadGrad& o, const Head
         HGB_TRY((launch_product<T, false, true, kSum>(c, x, p.dx)));
 
         ProductArgs w{};
-        w.a = Factor{dz, p.piece, h.n, p.piece, p.plane};
+        w.a = Factor{dz, p.stride, h.n, p.piece, p.plane};
         w.b = fx;
         w.m = (int)tokens;
         w.n = (int)h.dim;

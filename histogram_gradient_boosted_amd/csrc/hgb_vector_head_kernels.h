@@ -123,74 +123,66 @@ __device__ inline int by_k_place(int k, int chunk)
     return bytes >= 256 ? chunk ^ ((k & 3) << 2) : bytes == 128 ? chunk ^ (((k >> 1) & 1) << 2) : chunk;
 }
 
-// Loads a factor's tile of R rows (by k: columns), a step at a time: a wave's N
-// loads of a step one by one, then next().  Past the last step zeros are loaded.
+// Loads a factor's tiles of R rows (by k: columns), a step at a time: a wave's N
+// loads of a step one by one, then next().
 template <typename T, int R, int WAVES, bool BY_K>
 struct Loader {
     static constexpr int N = R / 8 / WAVES;   // loads of a wave
     static constexpr int SIZE = sizeof(T), STEP = kStepBytes / SIZE;
     uint32_t offset[N];
-    int tail[2];       // along: the first value of the lane's chunk in the step, of even and odd loads
-    const char* base;  // of the step
-    int64_t left;      // bytes from there to the factor's end
-    int64_t step, back;   // bytes from a step to the next, and from a plane's last step to the next plane's first
-    int live;          // along: values of the rows from the step on
-    int cols, k, steps, to_go;
+    int head[N];         // the first value of the lane's chunk: in the step, by k in the tile
+    const char* base;    // of the step
+    int bytes;           // from there to the end of the step's rows
+    int live;            // values of the rows from the step (by k: the tile) on
+    int step;            // bytes from a step to the next
+    int rows;            // by k: from the step on
 
-    // the steps [t0, t1) of all the planes'
-    __device__ __forceinline__ void init(const Factor& f, int64_t first, int wave, int lane, int k_steps, int64_t plane, int t0, int t1)
+    __device__ __forceinline__ void init(const Factor& f, int wave, int lane)
     {
+        const int stride = (int)(f.stride * SIZE);
 #pragma unroll
         for (int i = 0; i < N; ++i) {
-            const int at = (wave * N + i) * 1024 + lane * 16;
-            if (BY_K) {
-                constexpr int row_bytes = R * SIZE;
-                const int kk = at / row_bytes, chunk = by_k_place<T, R>(kk, at % row_bytes / 16);
-                const int64_t col = first + chunk * (16 / SIZE);
-                offset[i] = col < f.cols ? (uint32_t)(kk * f.stride * SIZE + chunk * 16) : kNowhere;
-            } else {
-                const int row = at / kStepBytes, chunk = along_place(row, at % kStepBytes / 16);
-                offset[i] = (uint32_t)(row * f.stride * SIZE + chunk * 16);
-                tail[i & 1] = chunk * (16 / SIZE);
-                static_assert(R / 8 % 2 == 0 && (N % 2 == 0 || N == 1), "chunks go by a load's parity");
-            }
+            const int at = (wave * N + i) * 1024 + lane * 16, width = BY_K ? R * SIZE : kStepBytes;
+            const int row = at / width, place = at % width / 16;
+            const int chunk = BY_K ? by_k_place<T, R>(row, place) : along_place(row, place);
+            offset[i] = (uint32_t)(row * stride + chunk * 16);
+            head[i] = chunk * (16 / SIZE);
         }
-        steps = k_steps;
-        const int at_plane = uniform(t0 / k_steps);
-        k = t0 - at_plane * k_steps;
-        to_go = t1 - t0;
-        step = BY_K ? STEP * f.stride * SIZE : kStepBytes;
-        back = plane * SIZE - step * (k_steps - 1);
-        const int64_t row = BY_K ? (int64_t)k * STEP : first, col = BY_K ? first : (int64_t)k * STEP;
-        base = (const char*)f.p + (at_plane * plane + row * f.stride + col) * SIZE;
-        left = ((f.rows - 1 - row) * f.stride + f.cols - col) * SIZE;
-        cols = (int)f.cols;
-        live = cols - k * STEP;
+        step = BY_K ? STEP * stride : kStepBytes;
+    }
+
+    // to the tile from row (column) `first` on, at step k of a plane
+    __device__ __forceinline__ void begin(const Factor& f, int first, int plane, int k)
+    {
+        const int row = BY_K ? k * STEP : first, col = BY_K ? first : k * STEP, stride = (int)f.stride;
+        base = (const char*)f.p + (plane * f.plane + (int64_t)row * stride + col) * SIZE;
+        live = (int)f.cols - col;
+        rows = (int)f.rows - row;
+        bytes = ((min(rows, BY_K ? STEP : R) - 1) * stride + live) * SIZE;
     }
 
     // the wave's load i to its place from `lds` on
     __device__ __forceinline__ void load(int i, uint32_t lds) const
     {
         const uint64_t b = (uint64_t)base;
-        const uint32_t bytes = to_go > 0 ? (uint32_t)min(left, (int64_t)0x7ffffff0) : 0;
-        const Rsrc r = {uniform((int)(uint32_t)b), uniform((int)((uint32_t)(b >> 32) & 0xffffu)), uniform((int)bytes), 0x00027000};
-        load_lds(lds + i * 1024, BY_K || tail[i & 1] < live ? offset[i] : kNowhere, r);
+        const Rsrc r = {uniform((int)(uint32_t)b), uniform((int)((uint32_t)(b >> 32) & 0xffffu)), uniform(bytes), 0x00027000};
+        load_lds(lds + i * 1024, head[i] < live ? offset[i] : kNowhere, r);
     }
 
     __device__ __forceinline__ void next()
     {
-        --to_go;
-        if (++k == steps) {
-            k = 0;
-            base += back;
-            left += step * (steps - 1);
-            live = cols;
+        base += step;
+        if (BY_K) {
+            rows -= STEP;
+            bytes = (min(rows, STEP) - 1) * (step / STEP) + live * SIZE;
         } else {
-            base += step;
-            left -= step;
             live -= STEP;
+            bytes -= kStepBytes;
         }
     }
+
+    // from here on zeros
+    __device__ __forceinline__ void stop() { bytes = live = 0; }
 };
 
 // Lane's part of 32 rows (columns) of a tile in LDS, sub-step s of the step.
@@ -232,91 +224,207 @@ __device__ inline float swap_halves(float x)
     return __uint_as_float((threadIdx.x & 32) ? v[0] : v[1]);
 }
 
-// A wave's 32 rows of TN * 32 columns, as the matrix instructions leave them (a
+// 32 rows of 64 columns of a wave's, as the matrix instructions leave them (a
 // lane has a row's values, four side by side), to memory by whole rows: through
-// the wave's own part of LDS, so that a store takes runs of 128 bytes and more.
+// the wave's own 8 KB of LDS, so that a store takes runs of 128 bytes and more.
 // Stored straight from the registers, 8 bytes here and there, the logits'
 // gradient of 8,192 x 32,768 took twice as long as its product.
-template <typename T, int TN>
-__device__ __forceinline__ void store_strip(const Acc (&acc)[TN], char* strip, int lane, int rows, T* out, int64_t stride)
+// LEFT: what the rounding to T left goes `plane` values further on.
+// ADD: to what is there.  Of the columns `cols` are stored, 16 bytes at a time
+// where they are all of them and rows start at 16 bytes (`whole`).
+constexpr int kStripBytes = 8192;
+
+template <bool LEFT = false, bool ADD = false, typename T>
+__device__ __forceinline__ void store_strip(const float (&v)[2][16], char* strip, int lane, int rows, int cols, bool whole, T* out,
+                                            int64_t stride, int64_t plane = 0)
 {
-    constexpr int V = 16 / sizeof(T), CHUNKS = TN * 32 / V, ROW = CHUNKS * 16;
+    constexpr int V = 16 / sizeof(T), CHUNKS = 64 / V, ROW = CHUNKS * 16, PLANE = 32 * ROW, AT_ONCE = 64 / CHUNKS;
+    static_assert(PLANE * (LEFT ? 2 : 1) <= kStripBytes, "a strip fits its part of LDS");
     auto place = [](int row, int chunk) { return row * ROW + (chunk ^ (CHUNKS >= 16 ? row & (CHUNKS - 1) : (row >> 1) & 7)) * 16; };
+    typedef T Four __attribute__((ext_vector_type(4)));
+    typedef T Chunk __attribute__((ext_vector_type(V)));
     const int row = lane & 31, half = lane >> 5;
     wave_order();
 #pragma unroll
-    for (int j = 0; j < TN; ++j)
+    for (int j = 0; j < 2; ++j)
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
             const int col = j * 32 + q * 8 + half * 4;
-            typedef T Four __attribute__((ext_vector_type(4)));
-            Four v;
+            char* to = strip + place(row, col / V) + col % V * (int)sizeof(T);
+            Four f;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) v[e] = (T)acc[j][4 * q + e];
-            *(Four*)(strip + place(row, col / V) + col % V * (int)sizeof(T)) = v;
+            for (int e = 0; e < 4; ++e) f[e] = (T)v[j][4 * q + e];
+            *(Four*)to = f;
+            if (LEFT) {
+                Four rest;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) rest[e] = (T)(v[j][4 * q + e] - (float)f[e]);
+                *(Four*)(to + PLANE) = rest;
+            }
         }
     wave_order();
+    const int first = lane / CHUNKS, chunk = lane % CHUNKS;
+    auto store = [&](const char* from, T* to) {
+        to += first * stride + chunk * V;
+        if (whole && rows >= 32) {
+            Chunk old[ADD ? 32 / AT_ONCE : 1];
+            if (ADD) {   // all loads, then all stores: a load waits for the stores before it
+                T* p = to;
 #pragma unroll
-    for (int k = 0; k < 32 * CHUNKS / 64; ++k) {
-        const int at = k * 64 + lane, r = at / CHUNKS, chunk = at % CHUNKS;
-        if (r < rows) *(uint4*)(out + r * stride + chunk * V) = *(const uint4*)(strip + place(r, chunk));
-    }
+                for (int k = 0; k < 32 / AT_ONCE; ++k) {
+                    old[ADD ? k : 0] = *(const Chunk*)p;
+                    p += AT_ONCE * stride;
+                    asm volatile("" : "+v"(p));   // one pointer, moved on, for all rows
+                }
+            }
+#pragma unroll
+            for (int k = 0; k < 32 / AT_ONCE; ++k) {
+                Chunk c = *(const Chunk*)(from + place(k * AT_ONCE + first, chunk));
+                if (ADD) c += old[ADD ? k : 0];
+                *(Chunk*)to = c;
+                to += AT_ONCE * stride;
+                asm volatile("" : "+v"(to));
+            }
+        } else {
+            for (int k = 0; k < 32 / AT_ONCE; ++k) {
+                const int r = k * AT_ONCE + first;
+                if (r < rows)
+                    for (int e = 0; e < V; ++e)
+                        if (chunk * V + e < cols) {
+                            const T x = *(const T*)(from + place(r, chunk) + e * (int)sizeof(T));
+                            to[e] = ADD ? to[e] + x : x;
+                        }
+                to += AT_ONCE * stride;
+            }
+        }
+    };
+    store(strip, out);
+    if (LEFT) store(strip + PLANE, out + plane);
 }
 
-// A block's tile of C.
-struct TilePlace {
+// The arguments once more, for use off the inner loop: behind a pointer that
+// the compiler cannot follow, so that it does not keep them all in registers
+// (it had put the loop's own out to lanes of vector registers).
+__device__ __forceinline__ const ProductArgs& cold_args()
+{
+    typedef const __attribute__((address_space(4))) ProductArgs* Constant;
+    Constant p = (Constant)__builtin_amdgcn_kernarg_segment_ptr();   // the kernel's only argument
+    asm volatile("" : "+s"(p));
+    return *(const ProductArgs*)p;
+}
+
+// An item of work: a tile of C and a share of its steps.
+struct Item {
     int m, n, split;
+    int t0, t1;
 };
 
-// Blocks go round the 8 XCDs: each gets a run of tiles, eight rows of tiles at
-// a time, so that the tiles in flight on one share rows and columns in its L2.
-__device__ inline TilePlace tile_place(const ProductArgs& g)
+__device__ inline Item item_at(const ProductArgs& g, uint32_t at)
 {
-    const uint32_t tiles = (uint32_t)g.tiles_m * (uint32_t)g.tiles_n, total = tiles * (uint32_t)g.splits;
-    const uint32_t xcd = blockIdx.x & 7, per = total / 8, more = total % 8;
-    const uint32_t at = xcd * per + min(xcd, more) + blockIdx.x / 8;
-    const uint32_t tile = at % tiles, width = 8 * (uint32_t)g.tiles_n, band = tile / width, first = band * 8;
-    const uint32_t rows = min(8u, (uint32_t)g.tiles_m - first), in = tile % width;
-    return {uniform((int)(first + in % rows)), uniform((int)(in / rows)), uniform((int)(at / tiles))};
+    // eight rows of tiles at a time, so that neighbours share rows and columns
+    const uint32_t tiles = (uint32_t)g.tiles_m * (uint32_t)g.tiles_n;
+    const uint32_t split = at / tiles, tile = at - split * tiles, width = 8 * (uint32_t)g.tiles_n, band = tile / width;
+    const uint32_t first = band * 8, rows = min(8u, (uint32_t)g.tiles_m - first), in = tile - band * width, n = in / rows;
+    const int steps = g.k_steps * g.planes;
+    const uint64_t t0 = (uint64_t)steps * split, t1 = t0 + steps;
+    return {uniform((int)(first + in - n * rows)), uniform((int)n), uniform((int)split),
+            uniform(g.splits == 1 ? 0 : (int)(t0 / (uint32_t)g.splits)), uniform(g.splits == 1 ? steps : (int)(t1 / (uint32_t)g.splits))};
 }
 
-// One product: C = a b over the tiles.  A block of WM x WN waves makes a tile
-// of BM x BN, each wave BM / WM x BN / WN of it in blocks of 32 x 32.  Steps of
+// A lane's row of partial maxima and sums (in units of log2), of the wave's
+// TN * 32 columns, of which `left` are tokens.  Per value: a maximum (of three),
+// an fma, an exponential (four times an instruction's time) and a sum.
+// RARE: some are no tokens, or the scale is not positive (`sign` is its sign).
+template <bool RARE, int TN>
+__device__ __forceinline__ float2 row_stats(const Acc (&acc)[TN], float scale, float sign, int left)
+{
+    const int quad = (threadIdx.x & 32) / 8;
+    auto value = [&](int j, int r) {
+        if (!RARE) return acc[j][r];
+        return j * 32 + 8 * (r / 4) + quad + r % 4 < left ? acc[j][r] * sign : -INFINITY;
+    };
+    float top = -INFINITY;
+#pragma unroll
+    for (int j = 0; j < TN; ++j)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) top = fmaxf(top, value(j, r));
+    top = fmaxf(top, swap_halves(top));
+    top = top == -INFINITY ? 0.0f : top * scale;   // 2^-infinity is 0 from anywhere
+    float sum[4] = {};
+#pragma unroll
+    for (int j = 0; j < TN; ++j)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) sum[r % 4] += __builtin_amdgcn_exp2f(__builtin_fmaf(value(j, r), scale, -top));
+    float all = (sum[0] + sum[1]) + (sum[2] + sum[3]);
+    all += swap_halves(all);
+    return make_float2(top, all);
+}
+
+// Blocks of a product's tile that a CU holds at a time.
+constexpr int product_lds(int bm, int bn, int waves, bool strips)
+{
+    return 2 * (bm + bn) * kStepBytes + (strips ? waves * kStripBytes : 0);
+}
+constexpr int product_blocks(int bm, int bn, int waves, bool strips) { return kLdsBytes / product_lds(bm, bn, waves, strips); }
+
+// One product: C = a b over the tiles.  A block of WM x WN waves makes tiles of
+// BM x BN, each wave BM / WM x BN / WN of them in blocks of 32 x 32.  Steps of
 // 128 bytes of the summed values go through two halves of LDS: one is filled
-// while the other is multiplied.
+// while the other is multiplied.  A block takes its tiles one after the other
+// as one run of steps, so that a tile's first steps are loaded while the one
+// before is finished.
 template <typename T, int BM, int BN, int WM, int WN, bool A_BY_K, bool B_BY_K, int WHAT>
-__global__ __launch_bounds__(64 * WM * WN) void k_product(const ProductArgs g)
+__global__ __launch_bounds__(64 * WM * WN) void k_product(const ProductArgs args)
 {
     constexpr int WAVES = WM * WN, TM = BM / WM / 32, TN = BN / WN / 32;
     constexpr int STAGE = (BM + BN) * kStepBytes;
-    constexpr bool LANE_IS_ROW = WHAT == kStats || WHAT == kGrad;   // else a lane holds a column's values
     extern __shared__ __align__(16) char smem[];
     const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
     const int wm = wave / WN, wn = wave % WN;
-    const TilePlace at = tile_place(g);
-    const int64_t row0 = (int64_t)at.m * BM, col0 = (int64_t)at.n * BN;
-    const int steps = g.k_steps * g.planes;
-    const int t0 = uniform((int)((int64_t)steps * at.split / g.splits)), t1 = uniform((int)((int64_t)steps * (at.split + 1) / g.splits));
+
+    // Blocks go round the 8 XCDs: each XCD has a run of the items, which its
+    // blocks take in turn, so that those in flight share its L2.
+    const uint32_t total = (uint32_t)args.tiles_m * (uint32_t)args.tiles_n * (uint32_t)args.splits;
+    const uint32_t xcds = min(8u, gridDim.x), xcd = blockIdx.x % 8, per = total / xcds, more = total % xcds;
+    const uint32_t turn = uniform((gridDim.x - xcd + 7) / 8), end = uniform((xcd + 1) * per + min(xcd + 1, more));
+    uint32_t at = uniform(xcd * per + min(xcd, more) + blockIdx.x / 8);   // the item that is multiplied, and
+    uint32_t ahead = at;                                                  // the one that is loaded
+    if (at >= end) return;
 
     Loader<T, BM, WAVES, A_BY_K> la;
     Loader<T, BN, WAVES, B_BY_K> lb;
-    la.init(g.a, row0, wave, lane, g.k_steps, g.a.plane, t0, t1);
-    lb.init(g.b, col0, wave, lane, g.k_steps, 0, t0, t1);
+    la.init(args.a, wave, lane);
+    lb.init(args.b, wave, lane);
     const uint32_t lds = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) char*)smem;
     const uint32_t lds_a = lds + wave * (la.N * 1024), lds_b = lds + BM * kStepBytes + wave * (lb.N * 1024);
+    constexpr int LOADS = la.N + lb.N, FIRST = LOADS / 2;
     auto load = [&](int i, uint32_t half) {   // one of a step's loads
         if (i < la.N) la.load(i, lds_a + half);
         else lb.load(i - la.N, lds_b + half);
     };
-    constexpr int LOADS = la.N + lb.N, FIRST = LOADS / 2;
-
-    Acc acc[TM][TN];
-#pragma unroll
-    for (int i = 0; i < TM; ++i)
-#pragma unroll
-        for (int j = 0; j < TN; ++j)
-#pragma unroll
-            for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.0f;
+    int to_load = 1, to_wrap = 1;   // steps that are left of the item ahead, and of the plane
+    ahead -= turn;
+    auto next = [&] {
+        if (to_load == 0) return;
+        --to_load;
+        if (--to_wrap != 0) {
+            la.next();
+            lb.next();
+        } else {   // the next plane, or the next item
+            if (to_load == 0 && (ahead += turn, (int)(end - ahead) <= 0)) {
+                la.stop();
+                lb.stop();
+                return;
+            }
+            const ProductArgs& g = cold_args();
+            const Item w = item_at(g, ahead);
+            if (to_load == 0) to_load = w.t1 - w.t0;
+            const int t = w.t1 - to_load, plane = uniform(t / g.k_steps), k = t - plane * g.k_steps;
+            la.begin(g.a, w.m * BM, plane, k);
+            lb.begin(g.b, w.n * BN, 0, k);
+            to_wrap = min(to_load, g.k_steps - k);
+        }
+    };
 
     // A step is four sub-steps; each sub-step's fragments are read while the
     // one before is multiplied.  Before the last sub-step every wave has read
@@ -325,161 +433,176 @@ __global__ __launch_bounds__(64 * WM * WN) void k_product(const ProductArgs g)
     // The loads take two sub-steps, the last of this step and the first of the
     // next: 64 KB at 64 bytes a cycle are 1,024 cycles, two sub-steps' products.
     // (All in the one: 1,120 against 1,097 us, 16,384 x 32,768 x 1,024.)
+    Acc acc[TM][TN];
     typename Frag<T>::type fa[2][TM], fb[2][TN];
-    auto read = [&](int i, int half, int s, int to) {   // one of a sub-step's fragments
-        const char* tile = smem + half * STAGE;
+    int half = 0;
+    auto read = [&](int i, int from, int s, int to) {   // one of a sub-step's fragments
+        const char* tile = smem + from * STAGE;
         if (i < TM) fa[to][i] = fragment<T, BM, A_BY_K>(tile, wm * TM + i, s, lane);
         else fb[to][i - TM] = fragment<T, BN, B_BY_K>(tile + BM * kStepBytes, wn * TN + i - TM, s, lane);
     };
-    if (t0 < t1) {
+    auto sub_step = [&](auto which) {
+        constexpr int s = decltype(which)::value, MMAS = TM * TN, READS = TM + TN;
+        // between the products: the next fragments, and after the barrier the loads
 #pragma unroll
-        for (int i = 0; i < LOADS; ++i) load(i, 0);
-        la.next();
-        lb.next();
+        for (int n = 0; n < MMAS; ++n) {
+            const int i = n / TN, j = n % TN;
+            acc[i][j] = mma(fb[s & 1][j], fa[s & 1][i], acc[i][j]);
 #pragma unroll
-        for (int i = 0; i < FIRST; ++i) load(i, STAGE);
-        asm volatile("s_waitcnt vmcnt(%0)" ::"n"(FIRST) : "memory");
-        __builtin_amdgcn_s_barrier();
-        asm volatile("" ::: "memory");
-#pragma unroll
-        for (int i = 0; i < TM + TN; ++i) read(i, 0, 0, 0);
-    }
-    for (int t = t0; t < t1; ++t) {
-        const int half = (t - t0) & 1;
-#pragma unroll
-        for (int s = 0; s < 4; ++s) {
+            for (int r = n * READS / MMAS; r < (n + 1) * READS / MMAS; ++r)
+                read(r, s == 3 ? half ^ 1 : half, (s + 1) & 3, (s + 1) & 1);
             if (s == 3) {
-                asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
-                __builtin_amdgcn_s_barrier();
-                asm volatile("" ::: "memory");
-            }
-            // between the sub-step's products: the next one's fragments, and after the barrier the loads
-            constexpr int MMAS = TM * TN, READS = TM + TN;
 #pragma unroll
-            for (int n = 0; n < MMAS; ++n) {
-                const int i = n / TN, j = n % TN;
-                acc[i][j] = LANE_IS_ROW ? mma(fb[s & 1][j], fa[s & 1][i], acc[i][j]) : mma(fa[s & 1][i], fb[s & 1][j], acc[i][j]);
-#pragma unroll
-                for (int r = n * READS / MMAS; r < (n + 1) * READS / MMAS; ++r)
-                    read(r, s == 3 ? half ^ 1 : half, (s + 1) & 3, (s + 1) & 1);
-                if (s == 3) {
-#pragma unroll
-                    for (int l = n * FIRST / MMAS; l < (n + 1) * FIRST / MMAS; ++l) load(l, half * STAGE);
-                }
-                if (s == 0) {
-#pragma unroll
-                    for (int l = n * (LOADS - FIRST) / MMAS; l < (n + 1) * (LOADS - FIRST) / MMAS; ++l)
-                        load(FIRST + l, (half ^ 1) * STAGE);
-                }
-                __builtin_amdgcn_sched_barrier(0);
+                for (int l = n * FIRST / MMAS; l < (n + 1) * FIRST / MMAS; ++l) load(l, half * STAGE);
             }
             if (s == 0) {
-                la.next();
-                lb.next();
+#pragma unroll
+                for (int l = n * (LOADS - FIRST) / MMAS; l < (n + 1) * (LOADS - FIRST) / MMAS; ++l)
+                    load(FIRST + l, (half ^ 1) * STAGE);
             }
+            __builtin_amdgcn_sched_barrier(0);
         }
-    }
-    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");   // LDS is written to no longer
+    };
+    next();
+#pragma unroll
+    for (int i = 0; i < LOADS; ++i) load(i, 0);
+    next();
+#pragma unroll
+    for (int i = 0; i < FIRST; ++i) load(i, STAGE);
+    asm volatile("s_waitcnt vmcnt(%0)" ::"n"(FIRST) : "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+#pragma unroll
+    for (int i = 0; i < TM + TN; ++i) read(i, 0, 0, 0);
 
-    // Value r of a 32 x 32 block's lane: the lane's row (column) is lane % 32,
-    // the other place 8 (r / 4) + 4 (lane / 32) + r % 4.
-    const int half = (lane >> 5) * 4;
-    const int64_t m0 = row0 + wm * TM * 32, n0 = col0 + wn * TN * 32;
-    if constexpr (WHAT == kStats) {
-        const bool ragged = n0 + TN * 32 > g.limit;
+    for (; at < end; at += turn) {
+        // Value r of a 32 x 32 block's lane: row lane % 32, column
+        // 8 (r / 4) + 4 (lane / 32) + r % 4.
+        const int quad = (lane >> 5) * 4;
 #pragma unroll
-        for (int i = 0; i < TM; ++i) {
-            const int64_t row = m0 + i * 32 + (lane & 31);
-            const bool live = row < g.m;
-            if (g.target) {
-                const int32_t target = live ? g.target[row] : -1;
-#pragma unroll
-                for (int j = 0; j < TN; ++j) {
-                    const int64_t to = (int64_t)target - n0 - j * 32;
-                    if (__ballot((uint64_t)to < 32u)) {
-#pragma unroll
-                        for (int r = 0; r < 16; ++r)
-                            if (to == 8 * (r / 4) + half + r % 4 && target < g.limit) g.hit[row] = acc[i][j][r] * g.scale;
-                    }
-                }
-            }
-            float top = -INFINITY;
+        for (int i = 0; i < TM; ++i)
 #pragma unroll
             for (int j = 0; j < TN; ++j)
 #pragma unroll
-                for (int r = 0; r < 16; ++r) {
-                    float v = acc[i][j][r] * g.scale;
-                    if (ragged && n0 + j * 32 + 8 * (r / 4) + half + r % 4 >= g.limit) v = -INFINITY;
-                    acc[i][j][r] = v;
-                    top = fmaxf(top, v);
-                }
-            top = fmaxf(top, swap_halves(top));
-            const float from = top == -INFINITY ? 0.0f : top;
-            float sum = 0.0f;
-#pragma unroll
-            for (int j = 0; j < TN; ++j)
-#pragma unroll
-                for (int r = 0; r < 16; ++r) sum += __builtin_amdgcn_exp2f(acc[i][j][r] - from);
-            sum += swap_halves(sum);
-            if (live && lane < 32) g.part[((int64_t)at.n * WN + wn) * g.m + row] = make_float2(top, sum);
+                for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.0f;
+        int t;
+        {
+            const ProductArgs& g = cold_args();
+            const Item w = item_at(g, at);
+            t = w.t1 - w.t0;
         }
-    } else if constexpr (WHAT == kGrad) {
-        const float unit = g.unit[0];
-        __syncthreads();   // the tiles in LDS are read
-        char* strip = smem + wave * (32 * TN * 32 * (int)sizeof(T));
-#pragma unroll
-        for (int i = 0; i < TM; ++i) {
-            const int64_t row = m0 + i * 32 + (lane & 31);
-            const bool live = row < g.m;
-            const float rate = live ? g.rate[row] * unit : 0.0f;
-            const float lse = live ? g.lse[row] : 0.0f;
-            const int64_t target = live && g.target ? (int64_t)g.target[row] - g.first : -1;
-#pragma unroll
-            for (int j = 0; j < TN; ++j)
-#pragma unroll
-                for (int r = 0; r < 16; ++r) {
-                    const int64_t col = n0 + j * 32 + 8 * (r / 4) + half + r % 4;
-                    const float p = __builtin_amdgcn_exp2f(__builtin_fmaf(acc[i][j][r], g.scale, -lse) * kLog2e);
-                    const float d = rate * (col == target ? p - 1.0f : p);
-                    acc[i][j][r] = rate != 0.0f && col < g.limit ? d : 0.0f;
-                }
-            T* to = (T*)g.dz + (m0 + i * 32) * g.dz_stride + n0;
-            store_strip<T, TN>(acc[i], strip, lane, (int)min((int64_t)32, g.m - m0 - i * 32), to, g.dz_stride);
-            if (g.dz_plane) {   // what the rounding left
-#pragma unroll
-                for (int j = 0; j < TN; ++j)
-#pragma unroll
-                    for (int r = 0; r < 16; ++r) acc[i][j][r] -= (float)(T)acc[i][j][r];
-                store_strip<T, TN>(acc[i], strip, lane, (int)min((int64_t)32, g.m - m0 - i * 32), to + g.dz_plane, g.dz_stride);
-            }
+        for (; t > 0; --t) {
+            sub_step(std::integral_constant<int, 0>());
+            next();
+            sub_step(std::integral_constant<int, 1>());
+            sub_step(std::integral_constant<int, 2>());
+            asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+            __builtin_amdgcn_s_barrier();
+            asm volatile("" ::: "memory");
+            sub_step(std::integral_constant<int, 3>());
+            half ^= 1;
         }
-    } else {
-        const float factor = WHAT == kOut && g.factor ? g.factor[0] : 1.0f;
-        const int64_t col = n0 + (lane & 31);
-        const int cols = (int)min((int64_t)(TN * 32), g.n - col);   // of the lane's, 32 apart
-        auto store = [&](auto* out, int64_t stride, bool add) {
+
+        const ProductArgs& g = cold_args();
+        const Item w = item_at(g, at);
+        const int m0 = w.m * BM + wm * TM * 32, n0 = w.n * BN + wn * TN * 32;
+        if constexpr (WHAT == kStats || WHAT == kGrad) {
+            const int left = g.limit - n0;
+            // What the rows' lanes need, before the first store: a load waits for
+            // the stores before it.
+            int to[TM];   // the target's place from the wave's first column on
+            float rate[TM], lse[TM];
 #pragma unroll
             for (int i = 0; i < TM; ++i) {
-#pragma unroll
-                for (int r = 0; r < 16; ++r) {
-                    const int64_t row = m0 + i * 32 + 8 * (r / 4) + half + r % 4;
-                    if (row < g.m) {
-                        auto* to = out + row * stride + col;
-#pragma unroll
-                        for (int j = 0; j < TN; ++j)
-                            if (j * 32 < cols) {
-                                const float v = acc[i][j][r] * factor;
-                                to[j * 32] = (std::remove_reference_t<decltype(*to)>)(add ? (float)to[j * 32] + v : v);
-                            }
-                    }
-                    __builtin_amdgcn_sched_barrier(0);   // else all rows' addresses are made first
+                const int row = m0 + i * 32 + (lane & 31);
+                to[i] = row < g.m && g.target ? g.target[row] - g.first - n0 : -1;
+                if (WHAT == kGrad) {
+                    rate[i] = row < g.m ? g.rate[row] * g.unit[0] : 0.0f;
+                    lse[i] = rate[i] != 0.0f ? g.lse[row] : 0.0f;
                 }
             }
-        };
-        if constexpr (WHAT == kSum) store(g.sum + (int64_t)at.split * g.m * g.sum_stride, g.sum_stride, g.add);
-        else if (g.out_type == HGB_F32) store((float*)g.out, g.out_stride, false);
-        else store((T*)g.out, g.out_stride, false);
+#pragma unroll
+            for (int i = 0; i < TM; ++i) {
+                const int row = m0 + i * 32 + (lane & 31);
+                if constexpr (WHAT == kStats) {
+#pragma unroll
+                    for (int j = 0; j < TN; ++j) {
+                        const int in = to[i] - j * 32;
+                        if (!__ballot((uint32_t)in < 32u)) continue;   // few blocks hold a row's target
+                        float v = 0.0f;
+#pragma unroll
+                        for (int r = 0; r < 16; ++r) v = in == 8 * (r / 4) + quad + r % 4 ? acc[i][j][r] : v;
+                        if ((uint32_t)in < 32u && (in & 4) == quad && to[i] < left) g.hit[row] = v * g.scale;
+                    }
+                    float2 s;
+                    if (left >= TN * 32 && g.scale > 0.0f) s = row_stats<false>(acc[i], g.scale, 1.0f, left);
+                    else if (g.scale != 0.0f) s = row_stats<true>(acc[i], fabsf(g.scale), g.scale > 0.0f ? 1.0f : -1.0f, left);
+                    else s = row_stats<true>(acc[i], 1.0f, 0.0f, left);
+                    if (row < g.m && lane < 32) g.part[((int64_t)w.n * WN + wn) * g.m + row] = s;
+                    __builtin_amdgcn_sched_barrier(0);
+                } else {
+                    T* out = (T*)g.dz + (int64_t)(m0 + i * 32) * g.dz_stride + n0;
+#pragma unroll
+                    for (int j = 0; j < TN; j += 2) {
+                        float v[2][16];
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            const int in = to[i] - (j + h) * 32;
+#pragma unroll
+                            for (int r = 0; r < 16; ++r)
+                                v[h][r] = rate[i] * __builtin_amdgcn_exp2f(__builtin_fmaf(acc[i][j + h][r], g.scale, -lse[i]) * kLog2e);
+                            if (__ballot((uint32_t)in < 32u)) {
+#pragma unroll
+                                for (int r = 0; r < 16; ++r) v[h][r] -= in == 8 * (r / 4) + quad + r % 4 ? rate[i] : 0.0f;
+                            }
+                            if (left < (j + h + 1) * 32) {   // past the tokens
+#pragma unroll
+                                for (int r = 0; r < 16; ++r) v[h][r] = (j + h) * 32 + 8 * (r / 4) + quad + r % 4 < left ? v[h][r] : 0.0f;
+                            }
+                        }
+                        char* strip = smem + 2 * STAGE + wave * kStripBytes;
+                        if constexpr (sizeof(T) < 4)
+                            if (g.dz_plane) {
+                                store_strip<true>(v, strip, lane, g.m - m0 - i * 32, 64, true, out + j * 32, g.dz_stride, g.dz_plane);
+                                continue;
+                            }
+                        store_strip(v, strip, lane, g.m - m0 - i * 32, 64, true, out + j * 32, g.dz_stride);
+                        __builtin_amdgcn_sched_barrier(0);
+                    }
+                }
+            }
+        } else {
+            char* strip = smem + 2 * STAGE + wave * kStripBytes;
+            auto store = [&](auto add, auto* out, int64_t stride, float factor) {
+                using U = std::remove_reference_t<decltype(*out)>;
+                const bool aligned = ((uint64_t)out | (uint64_t)stride * sizeof(U)) % 16 == 0;
+#pragma unroll
+                for (int i = 0; i < TM; ++i)
+#pragma unroll
+                    for (int j = 0; j < TN; j += 2) {
+                        float v[2][16];
+#pragma unroll
+                        for (int h = 0; h < 2; ++h)
+#pragma unroll
+                            for (int r = 0; r < 16; ++r) v[h][r] = acc[i][j + h][r] * factor;
+                        const int row = m0 + i * 32, cols = g.n - n0 - j * 32;
+                        store_strip<false, decltype(add)::value>(v, strip, lane, g.m - row, cols, aligned && cols >= 64,
+                                                                 out + row * stride + n0 + j * 32, stride);
+                        __builtin_amdgcn_sched_barrier(0);
+                    }
+            };
+            if constexpr (WHAT == kSum) {
+                float* sum = g.sum + (int64_t)w.split * g.m * g.sum_stride;
+                if (g.add) store(std::true_type(), sum, g.sum_stride, 1.0f);
+                else store(std::false_type(), sum, g.sum_stride, 1.0f);
+            } else {
+                const float factor = g.factor ? g.factor[0] : 1.0f;
+                if (g.out_type == HGB_F32) store(std::false_type(), (float*)g.out, g.out_stride, factor);
+                else store(std::false_type(), (T*)g.out, g.out_stride, factor);
+            }
+        }
     }
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");   // nothing is on its way to LDS when the block ends
 }
 
 // Rows copied to where they start at 16 bytes, with zeros behind their end,

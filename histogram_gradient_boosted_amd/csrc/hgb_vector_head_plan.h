@@ -10,7 +10,7 @@ namespace hgb {
 constexpr int64_t kHeadMaxRows = 1 << 24;
 constexpr int64_t kHeadMaxVocab = 1 << 24;
 constexpr int64_t kHeadMaxDim = 32768;
-constexpr int64_t kHeadMaxStride = 1 << 21;   // of rows that are read in place: a tile's 256 rows lie within 2^31 bytes
+constexpr int64_t kHeadMaxStride = 1 << 20;   // of rows that are read in place: a tile's 256 rows lie within 2^30 bytes
 constexpr int kDistillMaxTop = 256;
 constexpr int kHeadCus = 256;                 // splits are made for this many CUs
 
@@ -90,6 +90,7 @@ struct HeadGradPlan {
     int64_t piece = 0;         // tokens of a piece, whole tiles
     int64_t pieces = 0;
     int planes = 1;            // of the logits' gradient: 2 beside a 32-bit dtable of 16-bit inputs
+    int64_t stride = 0;        // values of a row of the logits' gradient
     int64_t plane = 0;         // values of a plane
     int64_t width = 0;         // floats of a partial row
     ProductPlan z, dx, dw;     // of a whole piece
@@ -105,7 +106,9 @@ inline HeadGradPlan plan_head_grad(bool copy_table, int size, int dtable_size, i
     const int64_t whole = vec_up(vocab, kTileCols);
     p.piece = std::min(whole, std::max<int64_t>(kTileCols, kPieceBytes / (n * size * p.planes) / kTileCols * kTileCols));
     p.pieces = vec_ceil(vocab, p.piece);
-    p.plane = n * p.piece;
+    // rows a large power of two apart would share the channels of L2 and memory
+    p.stride = p.piece + 128 / size;
+    p.plane = n * p.stride;
     p.width = vec_up(dim, 4);
     const int step = kStepBytes / size;
     p.z = plan_product(n, p.piece, 1, false, false);

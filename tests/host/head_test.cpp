@@ -55,9 +55,10 @@ static void plans()
                     for (int out : {2, 4}) {
                         if (out < size) continue;
                         const HeadGradPlan p = plan_head_grad(true, size, out, n, vocab, dim);
-                        CHECK(p.planes == (out > size ? 2 : 1) && p.piece % kTileCols == 0 && p.plane == n * p.piece);
+                        CHECK(p.planes == (out > size ? 2 : 1) && p.piece % kTileCols == 0 && p.stride > p.piece && p.stride * size % 16 == 0);
+                        CHECK(p.plane == n * p.stride);
                         CHECK(p.pieces * p.piece >= vocab && (p.pieces - 1) * p.piece < vocab);
-                        CHECK(p.piece == kTileCols || p.plane * p.planes * size <= kPieceBytes);
+                        CHECK(p.piece == kTileCols || n * p.piece * p.planes * size <= kPieceBytes);
                         const int step = kStepBytes / size;
                         check_product(p.z, n, p.piece, 1);
                         check_product(p.dx, n, dim, p.piece / step);
