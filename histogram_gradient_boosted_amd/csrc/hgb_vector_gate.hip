@@ -65,13 +65,16 @@ hgb_status hgb_gate(hgb_ctx* c, const void* logits, int32_t type, int64_t stride
         HGB_HIP(c, hipSetDevice(c->device));
         ProfScope ps(c, HGB_KERNEL_GATE);
         const GatePlan p = plan_gate(n_experts);
-        const GateArgs g{logits, stride, n_rows, n_experts, score, bias, groups, keep, best, top, renormalise, scale, p.log_group,
-                         experts, share, c->dev_words + kWordVectors};
-        const size_t lds = groups > 1 ? (size_t)p.per_block * groups * 8 : 0;
+        const bool exact = bias || groups > 1 || type == HGB_F32;
+        const GateArgs g{logits, stride, n_rows, n_experts, score, bias, groups, keep, best, per, top, renormalise, scale, p.log_group,
+                         gate_wave_bytes(p, n_experts, groups, exact), experts, share, c->dev_words + kWordVectors};
+        const size_t lds = gate_lds(p, n_experts, groups, top, exact);
         return by_values(type, p, [&](auto* t, auto values) -> hgb_status {
             using T = std::remove_pointer_t<decltype(t)>;
             const GridSpan blocks = span_blocks(vec_ceil(n_rows, p.per_block));
-            k_gate<T, decltype(values)::value><<<dim3(blocks.x, 1, blocks.z), 256, lds, c->stream>>>(g);
+            auto* kernel = k_gate<T, decltype(values)::value>;
+            if (lds > 65536) HGB_TRY(raise_lds(c, kernel));
+            kernel<<<dim3(blocks.x, 1, blocks.z), 256, lds, c->stream>>>(g);
             HGB_LAUNCHED(c, "k_gate");
             return HGB_OK;
         });

@@ -130,10 +130,23 @@ struct GatePlan {
     int per_block = 1;   // rows of a block of 256 threads
 };
 
+// LDS of a block: the rows' choices; then of each of its four waves the worths
+// of its rows' groups and whether they are kept, or the keys and worths of an
+// exact choice.
+constexpr int gate_list_bytes(int rows, int top) { return (rows * top * 4 + 7) / 8 * 8; }
+inline int gate_wave_bytes(const GatePlan& p, int experts, int groups, bool exact)
+{
+    return std::max(groups > 1 ? p.per_block / 4 * groups * 8 : 0, exact ? (experts + groups) * 8 : 0);
+}
+inline int gate_lds(const GatePlan& p, int experts, int groups, int top, bool exact)
+{
+    return gate_list_bytes(p.per_block, top) + 4 * gate_wave_bytes(p, experts, groups, exact);
+}
+
 inline GatePlan plan_gate(int experts)
 {
     GatePlan p;
-    p.values = experts > 512 ? 16 : 8;
+    p.values = experts > 128 ? 16 : 8;
     while ((p.values << p.log_group) < experts) ++p.log_group;
     p.per_block = 256 >> p.log_group;
     return p;

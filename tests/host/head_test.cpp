@@ -75,6 +75,8 @@ static void plans()
         const GatePlan p = plan_gate(e);
         CHECK((p.values << p.log_group) >= e && p.log_group <= 6 && p.per_block << p.log_group == 256);
         CHECK(p.log_group == 0 || (p.values << (p.log_group - 1)) < e);
+        for (int groups : {1, e})
+            for (int top : {1, std::min(e, 64)}) CHECK(gate_lds(p, e, groups, top, true) <= 163840 && gate_lds(p, e, groups, top, false) <= 65536);
     }
     alignas(16) char row[64];
     CHECK(in_place(row, 16, 8, 2) && !in_place(row + 2, 16, 8, 2) && !in_place(row, 15, 8, 2) && !in_place(row, 16, 7, 2));
