@@ -83,9 +83,10 @@ hgb_status launch_tile(hgb_ctx* c, ProductArgs g, const ProductPlan& p)
 template <typename T, bool A_BY_K, bool B_BY_K, int WHAT>
 hgb_status launch_product(hgb_ctx* c, const ProductArgs& g, const ProductPlan& p)
 {
-    if (p.bm == kTileFew) return launch_tile<T, 32, 256, 1, 4, A_BY_K, B_BY_K, WHAT>(c, g, p);
+    if (p.tile == kTileLow) return launch_tile<T, 32, 256, 1, 4, A_BY_K, B_BY_K, WHAT>(c, g, p);
+    if (p.tile == kTileMiddle) return launch_tile<T, 128, 128, 2, 2, A_BY_K, B_BY_K, WHAT>(c, g, p);
     if constexpr (WHAT == kSum || WHAT == kOut)
-        if (p.bn == kTileNarrow) return launch_tile<T, 256, 64, 4, 1, A_BY_K, B_BY_K, WHAT>(c, g, p);
+        if (p.tile == kTileNarrow) return launch_tile<T, 256, 64, 4, 1, A_BY_K, B_BY_K, WHAT>(c, g, p);
     return launch_tile<T, 256, 256, 2, 2, A_BY_K, B_BY_K, WHAT>(c, g, p);
 }
 

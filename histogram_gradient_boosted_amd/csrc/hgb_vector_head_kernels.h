@@ -224,29 +224,33 @@ __device__ inline float swap_halves(float x)
     return __uint_as_float((threadIdx.x & 32) ? v[0] : v[1]);
 }
 
-// 32 rows of 64 columns of a wave's, as the matrix instructions leave them (a
-// lane has a row's values, four side by side), to memory by whole rows: through
-// the wave's own 8 KB of LDS, so that a store takes runs of 128 bytes and more.
-// Stored straight from the registers, 8 bytes here and there, the logits'
-// gradient of 8,192 x 32,768 took twice as long as its product.
+// 32 rows of W * 32 columns of a wave's, as the matrix instructions leave them
+// (a lane has a row's values, four side by side), to memory by whole rows:
+// through the wave's own part of LDS, so that a store takes runs of 64 bytes
+// and more.  Stored straight from the registers, 8 bytes here and there, the
+// logits' gradient of 8,192 x 32,768 took twice as long as its product.
 // LEFT: what the rounding to T left goes `plane` values further on.
 // ADD: to what is there.  Of the columns `cols` are stored, 16 bytes at a time
 // where they are all of them and rows start at 16 bytes (`whole`).
-constexpr int kStripBytes = 8192;
+constexpr int strip_bytes(int bm, int bn) { return bm * bn >= 256 * 256 ? 8192 : 4096; }   // of a wave
+constexpr int strip_width(int bytes, int tn, int size, bool left)   // W
+{
+    return tn >= 2 && 32 * 64 * size * (left ? 2 : 1) <= bytes ? 2 : 1;
+}
 
-template <bool LEFT = false, bool ADD = false, typename T>
-__device__ __forceinline__ void store_strip(const float (&v)[2][16], char* strip, int lane, int rows, int cols, bool whole, T* out,
+template <bool LEFT = false, bool ADD = false, int W, typename T>
+__device__ __forceinline__ void store_strip(const float (&v)[W][16], char* strip, int lane, int rows, int cols, bool whole, T* out,
                                             int64_t stride, int64_t plane = 0)
 {
-    constexpr int V = 16 / sizeof(T), CHUNKS = 64 / V, ROW = CHUNKS * 16, PLANE = 32 * ROW, AT_ONCE = 64 / CHUNKS;
-    static_assert(PLANE * (LEFT ? 2 : 1) <= kStripBytes, "a strip fits its part of LDS");
-    auto place = [](int row, int chunk) { return row * ROW + (chunk ^ (CHUNKS >= 16 ? row & (CHUNKS - 1) : (row >> 1) & 7)) * 16; };
+    constexpr int V = 16 / sizeof(T), CHUNKS = W * 32 / V, ROW = CHUNKS * 16, PLANE = 32 * ROW, AT_ONCE = 64 / CHUNKS;
+    // (rows of 256 bytes: chunk by row; shorter ones: so that the rows of 256 bytes differ)
+    auto place = [](int row, int chunk) { return row * ROW + (chunk ^ ((CHUNKS >= 16 ? row : row / (16 / CHUNKS)) & (CHUNKS - 1))) * 16; };
     typedef T Four __attribute__((ext_vector_type(4)));
     typedef T Chunk __attribute__((ext_vector_type(V)));
     const int row = lane & 31, half = lane >> 5;
     wave_order();
 #pragma unroll
-    for (int j = 0; j < 2; ++j)
+    for (int j = 0; j < W; ++j)
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
             const int col = j * 32 + q * 8 + half * 4;
@@ -363,7 +367,7 @@ __device__ __forceinline__ float2 row_stats(const Acc (&acc)[TN], float scale, f
 // Blocks of a product's tile that a CU holds at a time.
 constexpr int product_lds(int bm, int bn, int waves, bool strips)
 {
-    return 2 * (bm + bn) * kStepBytes + (strips ? waves * kStripBytes : 0);
+    return 2 * (bm + bn) * kStepBytes + (strips ? waves * strip_bytes(bm, bn) : 0);
 }
 constexpr int product_blocks(int bm, int bn, int waves, bool strips) { return kLdsBytes / product_lds(bm, bn, waves, strips); }
 
@@ -377,7 +381,7 @@ template <typename T, int BM, int BN, int WM, int WN, bool A_BY_K, bool B_BY_K, 
 __global__ __launch_bounds__(64 * WM * WN) void k_product(const ProductArgs args)
 {
     constexpr int WAVES = WM * WN, TM = BM / WM / 32, TN = BN / WN / 32;
-    constexpr int STAGE = (BM + BN) * kStepBytes;
+    constexpr int STAGE = (BM + BN) * kStepBytes, STRIP = strip_bytes(BM, BN);
     extern __shared__ __align__(16) char smem[];
     const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
     const int wm = wave / WN, wn = wave % WN;
@@ -542,51 +546,58 @@ __global__ __launch_bounds__(64 * WM * WN) void k_product(const ProductArgs args
                     __builtin_amdgcn_sched_barrier(0);
                 } else {
                     T* out = (T*)g.dz + (int64_t)(m0 + i * 32) * g.dz_stride + n0;
+                    char* strip = smem + 2 * STAGE + wave * STRIP;
+                    auto store = [&](auto left_over) {
+                        constexpr bool LEFT = decltype(left_over)::value;
+                        constexpr int W = strip_width(STRIP, TN, sizeof(T), LEFT);
 #pragma unroll
-                    for (int j = 0; j < TN; j += 2) {
-                        float v[2][16];
+                        for (int j = 0; j < TN; j += W) {
+                            float v[W][16];
 #pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            const int in = to[i] - (j + h) * 32;
+                            for (int h = 0; h < W; ++h) {
+                                const int in = to[i] - (j + h) * 32;
 #pragma unroll
-                            for (int r = 0; r < 16; ++r)
-                                v[h][r] = rate[i] * __builtin_amdgcn_exp2f(__builtin_fmaf(acc[i][j + h][r], g.scale, -lse[i]) * kLog2e);
-                            if (__ballot((uint32_t)in < 32u)) {
+                                for (int r = 0; r < 16; ++r)
+                                    v[h][r] = rate[i] * __builtin_amdgcn_exp2f(__builtin_fmaf(acc[i][j + h][r], g.scale, -lse[i]) * kLog2e);
+                                if (__ballot((uint32_t)in < 32u)) {
 #pragma unroll
-                                for (int r = 0; r < 16; ++r) v[h][r] -= in == 8 * (r / 4) + quad + r % 4 ? rate[i] : 0.0f;
+                                    for (int r = 0; r < 16; ++r) v[h][r] -= in == 8 * (r / 4) + quad + r % 4 ? rate[i] : 0.0f;
+                                }
+                                if (left < (j + h + 1) * 32) {   // past the tokens
+#pragma unroll
+                                    for (int r = 0; r < 16; ++r)
+                                        v[h][r] = (j + h) * 32 + 8 * (r / 4) + quad + r % 4 < left ? v[h][r] : 0.0f;
+                                }
                             }
-                            if (left < (j + h + 1) * 32) {   // past the tokens
-#pragma unroll
-                                for (int r = 0; r < 16; ++r) v[h][r] = (j + h) * 32 + 8 * (r / 4) + quad + r % 4 < left ? v[h][r] : 0.0f;
-                            }
+                            store_strip<LEFT>(v, strip, lane, g.m - m0 - i * 32, W * 32, true, out + j * 32, g.dz_stride, g.dz_plane);
+                            __builtin_amdgcn_sched_barrier(0);
                         }
-                        char* strip = smem + 2 * STAGE + wave * kStripBytes;
-                        if constexpr (sizeof(T) < 4)
-                            if (g.dz_plane) {
-                                store_strip<true>(v, strip, lane, g.m - m0 - i * 32, 64, true, out + j * 32, g.dz_stride, g.dz_plane);
-                                continue;
-                            }
-                        store_strip(v, strip, lane, g.m - m0 - i * 32, 64, true, out + j * 32, g.dz_stride);
-                        __builtin_amdgcn_sched_barrier(0);
+                    };
+                    if constexpr (sizeof(T) < 4) {
+                        if (g.dz_plane) store(std::true_type());
+                        else store(std::false_type());
+                    } else {
+                        store(std::false_type());
                     }
                 }
             }
         } else {
-            char* strip = smem + 2 * STAGE + wave * kStripBytes;
+            char* strip = smem + 2 * STAGE + wave * STRIP;
             auto store = [&](auto add, auto* out, int64_t stride, float factor) {
                 using U = std::remove_reference_t<decltype(*out)>;
+                constexpr int W = strip_width(STRIP, TN, sizeof(U), false);
                 const bool aligned = ((uint64_t)out | (uint64_t)stride * sizeof(U)) % 16 == 0;
 #pragma unroll
                 for (int i = 0; i < TM; ++i)
 #pragma unroll
-                    for (int j = 0; j < TN; j += 2) {
-                        float v[2][16];
+                    for (int j = 0; j < TN; j += W) {
+                        float v[W][16];
 #pragma unroll
-                        for (int h = 0; h < 2; ++h)
+                        for (int h = 0; h < W; ++h)
 #pragma unroll
                             for (int r = 0; r < 16; ++r) v[h][r] = acc[i][j + h][r] * factor;
                         const int row = m0 + i * 32, cols = g.n - n0 - j * 32;
-                        store_strip<false, decltype(add)::value>(v, strip, lane, g.m - row, cols, aligned && cols >= 64,
+                        store_strip<false, decltype(add)::value>(v, strip, lane, g.m - row, cols, aligned && cols >= W * 32,
                                                                  out + row * stride + n0 + j * 32, stride);
                         __builtin_amdgcn_sched_barrier(0);
                     }
@@ -692,6 +703,7 @@ __global__ __launch_bounds__(256) void k_head_join(const float* sum, int64_t sum
         const int c = (int)(at - row * per) * 4;
         float v[4] = {};
         if (!rate || rate[row] != 0.0f)
+#pragma unroll 8
             for (int s = 0; s < splits; ++s) {
                 const float4 u = *(const float4*)(sum + ((int64_t)s * rows + row) * sum_stride + c);
                 v[0] += u.x;

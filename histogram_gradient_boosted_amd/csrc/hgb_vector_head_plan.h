@@ -14,35 +14,64 @@ constexpr int64_t kHeadMaxStride = 1 << 20;   // of rows that are read in place:
 constexpr int kDistillMaxTop = 256;
 constexpr int kHeadCus = 256;                 // splits are made for this many CUs
 
-constexpr int kTileRows = 256;    // of a product's tile, and
-constexpr int kTileFew = 32;      // where there are no more rows than that
+constexpr int kTileRows = 256;    // of the largest tile
 constexpr int kTileCols = 256;
-constexpr int kTileNarrow = 64;   // columns, where there are no more than that
+constexpr int kTileFew = 32;      // of the tile for no more rows than that
 constexpr int kStepBytes = 128;   // of a row that one step of a product's sum takes
 
 constexpr int64_t kPieceBytes = (int64_t)1 << 30;   // of the logits' gradient that is held at a time
-constexpr int64_t kStatBytes = (int64_t)1 << 28;    // of the forward pass's partial sums
+constexpr int64_t kStatBytes = (int64_t)1 << 29;    // of the forward pass's partial sums
+
+// The tiles of a product: rows x columns of a block of four waves, side by side
+// in `wn` columns; how many such blocks a CU's LDS holds; and how much of the
+// largest tile's rate their products reach, in 16 and in 32 bits (the products
+// of 32-bit values take eight times as long, and hide the rest).
+struct Tile {
+    int bm, bn, wn, per_cu;
+    float rate16, rate32;
+};
+constexpr Tile kTiles[] = {{256, 256, 2, 1, 1.0f, 1.0f}, {128, 128, 2, 2, 0.75f, 0.95f}, {256, 64, 1, 1, 0.5f, 0.9f}, {32, 256, 4, 1, 0.3f, 0.5f}};
+enum { kTileLarge, kTileMiddle, kTileNarrow, kTileLow };
 
 // A product's launch: C [m][n], summed over k in steps, in `splits` shares of
 // the steps.
 struct ProductPlan {
+    int tile = kTileLarge;
     int bm = kTileRows, bn = kTileCols;
     int64_t tiles_m = 1, tiles_n = 1;
     int splits = 1;
     int64_t blocks() const { return tiles_m * tiles_n * splits; }
 };
 
-inline ProductPlan plan_product(int64_t m, int64_t n, int64_t steps, bool narrow, bool split)
+// The tile whose blocks, in whole rounds of the CUs, take the least time for
+// their steps and as much as `ends` steps for their first loads and last
+// stores.  `split`: a sum may be shared by as many blocks as fill the CUs once,
+// of four steps at least.  The narrow tile is not for the logits, and rows that
+// fit the low one take it.
+inline ProductPlan plan_product(int64_t m, int64_t n, int64_t steps, int size, bool logits, bool split)
 {
-    ProductPlan p;
-    p.bm = m <= kTileFew ? kTileFew : kTileRows;
-    p.bn = narrow && n <= kTileNarrow && p.bm == kTileRows ? kTileNarrow : kTileCols;
-    p.tiles_m = vec_ceil(m, p.bm);
-    p.tiles_n = vec_ceil(n, p.bn);
-    // as many shares as fill the CUs once, of four steps at least
-    if (split)
-        p.splits = (int)std::max<int64_t>(1, std::min<int64_t>(kHeadCus / (p.tiles_m * p.tiles_n), steps / 4));
-    return p;
+    ProductPlan best;
+    double least = 0;
+    const double ends = size == 4 ? 0.5 : 3;
+    for (int t = 0; t < 4; ++t) {
+        const Tile& tile = kTiles[t];
+        if ((t == kTileNarrow && logits) || (t == kTileLow) != (m <= kTileFew)) continue;
+        ProductPlan p;
+        p.tile = t;
+        p.bm = tile.bm;
+        p.bn = tile.bn;
+        p.tiles_m = vec_ceil(m, p.bm);
+        p.tiles_n = vec_ceil(n, p.bn);
+        const int64_t room = (int64_t)kHeadCus * tile.per_cu;
+        if (split) p.splits = (int)std::max<int64_t>(1, std::min<int64_t>(room / (p.tiles_m * p.tiles_n), steps / 4));
+        const double rounds = (double)vec_ceil(p.blocks(), room) * tile.per_cu;
+        const double time = rounds * p.bm * p.bn * ((double)steps / p.splits / (size == 4 ? tile.rate32 : tile.rate16) + ends);
+        if (least == 0 || time < least) {
+            least = time;
+            best = p;
+        }
+    }
+    return best;
 }
 
 // Whether rows can be read in place: each starts at 16 bytes and ends with them.
@@ -62,18 +91,16 @@ struct HeadPlan {
     int64_t off_x = 0, off_table = 0, off_part = 0, off_hit = 0, bytes = 0;
 };
 
-constexpr int tile_parts(int bm) { return bm == kTileRows ? 2 : 4; }   // waves side by side in a tile's columns
-
 inline HeadPlan plan_head(bool copy_x, bool copy_table, int size, int64_t n, int64_t vocab, int64_t dim)
 {
     HeadPlan p;
     p.copy_x = copy_x;
     p.copy_table = copy_table;
     p.dp = vec_up(dim, 16 / size);
-    const int bm = n <= kTileFew ? kTileFew : kTileRows;
-    p.parts = vec_ceil(vocab, kTileCols) * tile_parts(bm);
-    p.piece = std::min(n, std::max<int64_t>(kTileRows, kStatBytes / (8 * p.parts) / kTileRows * kTileRows));
-    p.z = plan_product(p.piece, vocab, 1, false, false);
+    const int64_t most = vec_ceil(vocab, 64);   // partial pairs of a row, whatever the tile
+    p.piece = std::min(n, std::max<int64_t>(kTileRows, kStatBytes / (8 * most) / kTileRows * kTileRows));
+    p.z = plan_product(p.piece, vocab, vec_ceil(dim * size, kStepBytes), size, true, false);
+    p.parts = p.z.tiles_n * kTiles[p.z.tile].wn;
     p.off_table = copy_x ? vec_up(n * p.dp * size, 256) : 0;
     p.off_part = p.off_table + (copy_table ? vec_up(vocab * p.dp * size, 256) : 0);
     p.off_hit = p.off_part + vec_up(p.parts * p.piece * 8, 256);
@@ -111,9 +138,9 @@ inline HeadGradPlan plan_head_grad(bool copy_table, int size, int dtable_size, i
     p.plane = n * p.stride;
     p.width = vec_up(dim, 4);
     const int step = kStepBytes / size;
-    p.z = plan_product(n, p.piece, 1, false, false);
-    p.dx = plan_product(n, dim, p.piece / step, true, true);
-    p.dw = plan_product(p.piece, dim, vec_ceil(n, step) * p.planes, true, true);
+    p.z = plan_product(n, p.piece, vec_ceil(dim, step), size, true, false);
+    p.dx = plan_product(n, dim, std::min(p.piece, vocab) / step, size, false, true);
+    p.dw = plan_product(std::min(p.piece, vocab), dim, vec_ceil(n, step) * p.planes, size, false, true);
     p.off_table = vec_up(n * p.dp * size, 256);
     p.off_rate = p.off_table + (copy_table ? vec_up(vocab * p.dp * size, 256) : 0);
     p.off_z = p.off_rate + vec_up((n + 2) * 4, 256);

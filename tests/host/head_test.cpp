@@ -29,8 +29,8 @@ static const int64_t kDims[] = {1, 3, 8, 64, 65, 129, 512, 1024, 5000, 32768};
 
 static void check_product(const ProductPlan& p, int64_t m, int64_t n, int64_t steps)
 {
-    CHECK((p.bm == kTileRows || p.bm == kTileFew) && (p.bn == kTileCols || p.bn == kTileNarrow));
-    CHECK(p.bm != kTileFew || (m <= kTileFew && p.bn == kTileCols));
+    CHECK(p.bm == kTiles[p.tile].bm && p.bn == kTiles[p.tile].bn);
+    CHECK((p.tile == kTileLow) == (m <= kTileFew));
     CHECK(p.tiles_m * p.bm >= m && (p.tiles_m - 1) * p.bm < m && p.tiles_n * p.bn >= n && (p.tiles_n - 1) * p.bn < n);
     CHECK(p.splits >= 1 && (p.splits == 1 || p.splits <= steps));   // no share is empty
     CHECK(p.blocks() * 256 < (int64_t)1 << 32);
@@ -47,7 +47,7 @@ static void plans()
                         CHECK(p.dp >= dim && p.dp * size % 16 == 0 && p.dp - dim < 16 / size);
                         CHECK(p.piece >= 1 && p.piece <= n && (p.piece == n || p.piece % kTileRows == 0));
                         check_product(p.z, p.piece, vocab, 1);
-                        CHECK(p.parts == p.z.tiles_n * tile_parts(p.z.bm));
+                        CHECK(p.parts == p.z.tiles_n * kTiles[p.z.tile].wn && p.z.tile != kTileNarrow);
                         CHECK(p.off_table >= (p.copy_x ? n * p.dp * size : 0) && p.off_table % 256 == 0);
                         CHECK(p.off_part >= p.off_table + (p.copy_table ? vocab * p.dp * size : 0) && p.off_part % 256 == 0);
                         CHECK(p.off_hit >= p.off_part + p.parts * p.piece * 8 && p.bytes >= p.off_hit + n * 4);
@@ -61,8 +61,8 @@ static void plans()
                         CHECK(p.piece == kTileCols || n * p.piece * p.planes * size <= kPieceBytes);
                         const int step = kStepBytes / size;
                         check_product(p.z, n, p.piece, 1);
-                        check_product(p.dx, n, dim, p.piece / step);
-                        check_product(p.dw, p.piece, dim, vec_ceil(n, step) * p.planes);
+                        check_product(p.dx, n, dim, std::min(p.piece, vocab) / step);
+                        check_product(p.dw, std::min(p.piece, vocab), dim, vec_ceil(n, step) * p.planes);
                         CHECK(p.width >= dim && p.width % 4 == 0);
                         CHECK(p.off_table >= n * p.dp * size && p.off_rate >= p.off_table + vocab * p.dp * size);
                         CHECK(p.off_z >= p.off_rate + (n + 2) * 4 && p.off_dx >= p.off_z + p.plane * p.planes * size);
