@@ -204,7 +204,9 @@ hgb_status run_backward(hgb_ctx* c, const Head& h, const HeadGrad& o, const Head
         fw = Factor{ws + p.off_table, p.dp, h.vocab, p.dp, 0};
     }
     constexpr int STEP = kStepBytes / (int)sizeof(T);
-    T* dz = (T*)(ws + p.off_z);
+    // Where dz has a second plane, what its rounding left, that comes first: the
+    // sum over both then adds up the small values before the large.
+    T *planes = (T*)(ws + p.off_z), *dz = planes + (p.planes > 1 ? p.plane : 0);
     float *sum = (float*)(ws + p.off_dx), *dw = (float*)(ws + p.off_dw);
     for (int64_t first = 0; first < h.vocab; first += p.piece) {
         const int64_t tokens = std::min(p.piece, h.vocab - first);
@@ -227,7 +229,7 @@ hgb_status run_backward(hgb_ctx* c, const Head& h, const HeadGrad& o, const Head
         z.unit = unit;
         z.dz = dz;
         z.dz_stride = p.stride;
-        z.dz_plane = p.planes > 1 ? p.plane : 0;
+        z.dz_plane = planes - dz;
         ProductPlan zp = p.z;
         zp.tiles_n = vec_ceil(tokens, zp.bn);
         HGB_TRY((launch_product<T, false, false, kGrad>(c, z, zp)));
@@ -251,7 +253,7 @@ hgb_status run_backward(hgb_ctx* c, const Head& h, const HeadGrad& o, const Head
         HGB_TRY((launch_product<T, false, true, kSum>(c, x, p.dx)));
 
         ProductArgs w{};
-        w.a = Factor{dz, p.stride, h.n, p.piece, p.plane};
+        w.a = Factor{planes, p.stride, h.n, p.piece, p.plane};
         w.b = fx;
         w.m = (int)tokens;
         w.n = (int)h.dim;
