@@ -93,10 +93,11 @@ hgb_status launch_product(hgb_ctx* c, const ProductArgs& g, const ProductPlan& p
 unsigned fill_blocks(const hgb_ctx* c, int64_t threads) { return (unsigned)std::min<int64_t>(vec_ceil(threads, 256), 16 * c->n_cu); }
 
 template <typename T>
-hgb_status copy_rows(hgb_ctx* c, const void* x, int64_t stride, int64_t n, int64_t dim, int64_t dp, const float* rate, void* out)
+hgb_status copy_rows(hgb_ctx* c, const void* x, int64_t stride, int64_t n, int64_t dim, int64_t dp, float* rate, int rate_blocks,
+                     void* out)
 {
     k_head_copy<T><<<fill_blocks(c, n * dp * (int64_t)sizeof(T) / 16), 256, 0, c->stream>>>((const T*)x, stride, n, (int)dim, (int)dp,
-                                                                                            rate, (T*)out);
+                                                                                            rate, rate_blocks, (T*)out);
     HGB_LAUNCHED(c, "k_head_copy");
     return HGB_OK;
 }
@@ -108,12 +109,12 @@ hgb_status run_forward(hgb_ctx* c, const Head& h, const HeadPlan& p, float* loss
     const int64_t dp = h.copy_x() ? p.dp : h.dim, wp = h.copy_table() ? p.dp : h.dim;
     Factor fx{h.x, h.x_stride, h.n, dp, 0}, fw{h.table, h.table_stride, h.vocab, wp, 0};
     if (p.copy_x) {
-        HGB_TRY(copy_rows<T>(c, h.x, h.x_stride, h.n, h.dim, p.dp, nullptr, ws));
+        HGB_TRY(copy_rows<T>(c, h.x, h.x_stride, h.n, h.dim, p.dp, nullptr, 0, ws));
         fx.p = ws;
         fx.stride = p.dp;
     }
     if (p.copy_table) {
-        HGB_TRY(copy_rows<T>(c, h.table, h.table_stride, h.vocab, h.dim, p.dp, nullptr, ws + p.off_table));
+        HGB_TRY(copy_rows<T>(c, h.table, h.table_stride, h.vocab, h.dim, p.dp, nullptr, 0, ws + p.off_table));
         fw.p = ws + p.off_table;
         fw.stride = p.dp;
     }
@@ -193,14 +194,15 @@ hgb_status run_backward(hgb_ctx* c, const Head& h, const HeadGrad& o, const Head
     const float *unit = rate + h.n, *factor = rate + h.n + 1;
     // d (the logits' product): a cross entropy's scale; a distillation's T^2 / T
     RateArgs ra{o.grad, h.teacher ? h.heat : h.scale, h.n, (int32_t)h.vocab, h.token, h.top, h.pad, h.teacher, h.teacher_type,
-                h.type == HGB_F16, rate, c->dev_words + kWordVectors};
-    k_head_rate<<<1, 1024, 0, c->stream>>>(ra);
+                rate, c->dev_words + kWordVectors};
+    const int rate_blocks = (int)std::min<int64_t>(kRateBlocks, vec_ceil(h.n, 256));
+    k_head_rate<<<rate_blocks, 256, 0, c->stream>>>(ra);
     HGB_LAUNCHED(c, "k_head_rate");
-    HGB_TRY(copy_rows<T>(c, h.x, h.x_stride, h.n, h.dim, p.dp, rate, ws));
+    HGB_TRY(copy_rows<T>(c, h.x, h.x_stride, h.n, h.dim, p.dp, rate, rate_blocks, ws));
     const Factor fx{ws, p.dp, h.n, p.dp, 0};
     Factor fw{h.table, h.table_stride, h.vocab, h.dim, 0};
     if (p.copy_table) {
-        HGB_TRY(copy_rows<T>(c, h.table, h.table_stride, h.vocab, h.dim, p.dp, nullptr, ws + p.off_table));
+        HGB_TRY(copy_rows<T>(c, h.table, h.table_stride, h.vocab, h.dim, p.dp, nullptr, 0, ws + p.off_table));
         fw = Factor{ws + p.off_table, p.dp, h.vocab, p.dp, 0};
     }
     constexpr int STEP = kStepBytes / (int)sizeof(T);

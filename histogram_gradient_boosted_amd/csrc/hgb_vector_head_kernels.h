@@ -616,29 +616,8 @@ __global__ __launch_bounds__(64 * WM * WN) void k_product(const ProductArgs args
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");   // nothing is on its way to LDS when the block ends
 }
 
-// Rows copied to where they start at 16 bytes, with zeros behind their end,
-// and instead of rows whose rate is zero.
-template <typename T>
-__global__ __launch_bounds__(256) void k_head_copy(const T* x, int64_t stride, int64_t n, int dim, int dp, const float* rate,
-                                                   T* out)
-{
-    constexpr int V = 16 / sizeof(T);
-    const int per = dp / V;
-    const int64_t total = n * per;
-    for (int64_t at = (int64_t)blockIdx.x * 256 + threadIdx.x; at < total; at += (int64_t)gridDim.x * 256) {
-        const int64_t row = at / per;
-        const int c = (int)(at - row * per) * V;
-        typename Vals<T, V>::type v{};
-        if (!rate || rate[row] != 0.0f) v = load_raw<V>(x + row * stride + c, dim - c);
-        *(typename Vals<T, V>::type*)(out + row * dp + c) = v;
-    }
-}
-
 // Each row's rate, the factor of its logits' gradient (zero without one), and
-// what the gradient is multiplied by for its type: fp16 holds values of 2^-24
-// to 2^16, and a rate times a probability is often less than the former, so
-// the largest rate is brought between 2^14 and 2^15.  Powers of two: exact.
-// One block.
+// the blocks' largest.
 struct RateArgs {
     const float* grad;
     float scale;
@@ -649,8 +628,7 @@ struct RateArgs {
     int32_t pad;
     const void* teacher;   // or null
     int teacher_type;
-    int half;              // fp16
-    float* rate;           // [n], then the factor and one over it
+    float* rate;           // [n], then kRateWords
     uint32_t* err;
 };
 
@@ -659,12 +637,12 @@ __device__ inline float teacher_at(const void* p, int type, int64_t i)
     return type == HGB_F32 ? ((const float*)p)[i] : type == HGB_BF16 ? (float)((const __bf16*)p)[i] : (float)((const _Float16*)p)[i];
 }
 
-__global__ __launch_bounds__(1024) void k_head_rate(const RateArgs a)
+__global__ __launch_bounds__(256) void k_head_rate(const RateArgs a)
 {
-    __shared__ float most[16];
+    __shared__ float most[4];
     float top = 0.0f;
     bool bad = false;
-    for (int64_t i = threadIdx.x; i < a.n; i += 1024) {
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < a.n; i += (int64_t)gridDim.x * 256) {
         bool live = false;
         for (int k = 0; k < a.top; ++k) {
             const int32_t t = a.token[i * a.top + k];
@@ -680,13 +658,44 @@ __global__ __launch_bounds__(1024) void k_head_rate(const RateArgs a)
     for (int s = 32; s > 0; s >>= 1) top = fmaxf(top, __shfl_xor(top, s));
     if ((threadIdx.x & 63) == 0) most[threadIdx.x >> 6] = top;
     __syncthreads();
+    if (threadIdx.x == 0) a.rate[a.n + 2 + blockIdx.x] = fmaxf(fmaxf(most[0], most[1]), fmaxf(most[2], most[3]));
+}
+
+// What the logits' gradient is multiplied by for its type, and one over it:
+// fp16 holds values of 2^-24 to 2^16, and a rate times a probability is often
+// less than the former, so the largest rate (of `blocks` blocks') is brought
+// between 2^14 and 2^15.  Powers of two: exact.
+__device__ inline void rate_unit(float* words, int blocks, bool half)
+{
+    float top = 0.0f;
+    for (int i = threadIdx.x; i < blocks; i += 64) top = fmaxf(top, words[2 + i]);
+    for (int s = 32; s > 0; s >>= 1) top = fmaxf(top, __shfl_xor(top, s));
     if (threadIdx.x == 0) {
-        for (int w = 0; w < 16; ++w) top = fmaxf(top, most[w]);
         int e = 0;   // top in [2^(e - 1), 2^e)
-        if (a.half && top > 0.0f && top < INFINITY) (void)frexpf(top, &e);
-        e = a.half ? max(-100, min(100, 15 - e)) : 0;
-        a.rate[a.n] = ldexpf(1.0f, e);
-        a.rate[a.n + 1] = ldexpf(1.0f, -e);
+        if (half && top > 0.0f && top < INFINITY) (void)frexpf(top, &e);
+        e = half ? max(-100, min(100, 15 - e)) : 0;
+        words[0] = ldexpf(1.0f, e);
+        words[1] = ldexpf(1.0f, -e);
+    }
+}
+
+// Rows copied to where they start at 16 bytes, with zeros behind their end,
+// and instead of rows whose rate is zero.  With rates, the first wave makes
+// their unit.
+template <typename T>
+__global__ __launch_bounds__(256) void k_head_copy(const T* x, int64_t stride, int64_t n, int dim, int dp, float* rate, int blocks,
+                                                   T* out)
+{
+    if (rate && blockIdx.x == 0 && threadIdx.x < 64) rate_unit(rate + n, blocks, std::is_same<T, _Float16>::value);
+    constexpr int V = 16 / sizeof(T);
+    const int per = dp / V;
+    const int64_t total = n * per;
+    for (int64_t at = (int64_t)blockIdx.x * 256 + threadIdx.x; at < total; at += (int64_t)gridDim.x * 256) {
+        const int64_t row = at / per;
+        const int c = (int)(at - row * per) * V;
+        typename Vals<T, V>::type v{};
+        if (!rate || rate[row] != 0.0f) v = load_raw<V>(x + row * stride + c, dim - c);
+        *(typename Vals<T, V>::type*)(out + row * dp + c) = v;
     }
 }
 

@@ -19,6 +19,9 @@ constexpr int kTileCols = 256;
 constexpr int kTileFew = 32;      // of the tile for no more rows than that
 constexpr int kStepBytes = 128;   // of a row that one step of a product's sum takes
 
+constexpr int kRateBlocks = 256;
+constexpr int kRateWords = 2 + kRateBlocks;   // behind the rates: their unit, one over it, the blocks' largest
+
 constexpr int64_t kPieceBytes = (int64_t)1 << 30;   // of the logits' gradient that is held at a time
 constexpr int64_t kStatBytes = (int64_t)1 << 29;    // of the forward pass's partial sums
 
@@ -143,7 +146,7 @@ inline HeadGradPlan plan_head_grad(bool copy_table, int size, int dtable_size, i
     p.dw = plan_product(std::min(p.piece, vocab), dim, vec_ceil(n, step) * p.planes, size, false, true);
     p.off_table = vec_up(n * p.dp * size, 256);
     p.off_rate = p.off_table + (copy_table ? vec_up(vocab * p.dp * size, 256) : 0);
-    p.off_z = p.off_rate + vec_up((n + 2) * 4, 256);
+    p.off_z = p.off_rate + vec_up((n + kRateWords) * 4, 256);
     p.off_dx = p.off_z + vec_up(p.plane * p.planes * size, 256);
     p.off_dw = p.off_dx + vec_up(p.dx.splits * n * p.width * 4, 256);
     p.bytes = p.off_dw + (p.dw.splits > 1 ? vec_up(p.dw.splits * p.piece * p.width * 4, 256) : 0);

@@ -65,7 +65,7 @@ static void plans()
                         check_product(p.dw, std::min(p.piece, vocab), dim, vec_ceil(n, step) * p.planes);
                         CHECK(p.width >= dim && p.width % 4 == 0);
                         CHECK(p.off_table >= n * p.dp * size && p.off_rate >= p.off_table + vocab * p.dp * size);
-                        CHECK(p.off_z >= p.off_rate + (n + 2) * 4 && p.off_dx >= p.off_z + p.plane * p.planes * size);
+                        CHECK(p.off_z >= p.off_rate + (n + kRateWords) * 4 && p.off_dx >= p.off_z + p.plane * p.planes * size);
                         CHECK(p.off_dw >= p.off_dx + p.dx.splits * n * p.width * 4);
                         CHECK(p.bytes >= p.off_dw + (p.dw.splits > 1 ? p.dw.splits * p.piece * p.width * 4 : 0));
                         CHECK(p.off_table % 16 == 0 && p.off_z % 16 == 0 && p.off_dx % 16 == 0 && p.off_dw % 16 == 0);
