@@ -46,7 +46,7 @@ struct ProductArgs {
     int first;           // row of x, or token, that C's first row or column stands for
 
     // z and dz
-    float scale;         // of the logits (kStats: times log2(e))
+    float scale;         // of the logits (the softmax's sums: times log2(e))
     int limit;           // C's columns beyond this are no tokens
     const int32_t* target;
     float2* part;        // [n_part][m]: maxima and sums
@@ -67,6 +67,8 @@ struct ProductArgs {
     const float* factor;   // of C, or null
 };
 
+// What becomes of C: the logits' maxima and sums by rows and parts of 64 to 128
+// tokens; the logits' gradient dz; a sum in 32 bits, by shares; or C itself.
 enum { kStats, kGrad, kSum, kOut };
 
 template <typename T>
@@ -377,6 +379,15 @@ constexpr int product_blocks(int bm, int bn, int waves, bool strips) { return kL
 // while the other is multiplied.  A block takes its tiles one after the other
 // as one run of steps, so that a tile's first steps are loaded while the one
 // before is finished.
+//
+// Four waves of 128 x 128 read the least of LDS for their products (8 KB each
+// for 16 matrix instructions, half of what LDS gives in that time; eight waves
+// of 128 x 64 would take three quarters, beside a quarter for the loads), and
+// their 256 results a lane leave 256 registers for all else: one wave a SIMD.
+// Bound by the matrix instructions (64% of the time at 8,192^3 bf16, 1.20
+// PFLOP/s; the rest are waits at the step's barrier and for fragments), and for
+// short sums by the tiles' ends: 16,384 x 32,768 logits of 1,024 values 0.99 ms
+// (1.11 PFLOP/s), of 512 0.57 (0.97).
 template <typename T, int BM, int BN, int WM, int WN, bool A_BY_K, bool B_BY_K, int WHAT>
 __global__ __launch_bounds__(64 * WM * WN) void k_product(const ProductArgs args)
 {
@@ -699,7 +710,8 @@ __global__ __launch_bounds__(256) void k_head_copy(const T* x, int64_t stride, i
     }
 }
 
-// A sum's shares added up: rows of zero rate are zero.
+// A sum's shares added up: rows of zero rate are zero.  8 shares of 4,096 x 512:
+// 14 us (67 MB, 5 TB/s).
 template <typename T>
 __global__ __launch_bounds__(256) void k_head_join(const float* sum, int64_t sum_stride, int splits, int64_t rows, int dim,
                                                    const float* rate, const float* factor, T* out, int64_t stride)
@@ -736,6 +748,7 @@ __global__ __launch_bounds__(256) void k_head_zero(char* out, int64_t stride, in
 
 // The rows' partial maxima and sums (of 2^z) joined: lse, and the loss of a
 // target.  2^log_rows rows a block, the other threads side by side in parts.
+// 16,384 rows of 256 parts: 13 us (2.5 TB/s).
 struct LossArgs {
     const float2* part;
     int64_t parts, rows;
@@ -848,7 +861,9 @@ __device__ inline TeacherRow teacher_row(const TeacherArgs& a, int64_t row, int 
     return w;
 }
 
-// The student's logits at the teacher's tokens: a wave a slot.
+// The student's logits at the teacher's tokens: a wave a slot.  Bound by the
+// tokens' vectors, out of the caches: 8,192 rows of 64 slots of 2 KB 144 us (7.4
+// TB/s).  Picked out of the logits' tiles instead they cost those 359 us more.
 template <typename T>
 __global__ __launch_bounds__(256) void k_distill_pick(const T* x, int64_t x_stride, const T* table, int64_t table_stride,
                                                       int64_t n, int dim, const TeacherArgs a, float* picked)

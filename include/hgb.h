@@ -678,8 +678,8 @@ hgb_status hgb_gate_backward(hgb_ctx* ctx, const float* grad_dev, const void* lo
  * The cross entropy of each row's target under a softmax over the vocabulary:
  *   z[i][v] = scale * <x[i], table[v]>,  lse[i] = log of the sum of exp(z[i][v])
  *   loss[i] = lse[i] - z[i][target[i]]
- * The logits z are not kept: a block of kernels' tile of them lives in
- * registers.  Products are of the inputs' type, sums of 32-bit floats.
+ * The logits z are not kept: a tile of them at a time lives in registers.
+ * Products are of the inputs' type, sums of 32-bit floats.
  *
  * x_dev:       [n_rows][dim], rows x_stride apart; table_dev: [vocab][dim],
  *              rows table_stride apart, both of type `type`.

@@ -269,3 +269,43 @@ def test_gate_of_the_largest_sizes(torch, ctx):
     top = key.topk(2, 1).indices
     assert torch.equal(chosen.long(), top)
     ctx.sync()
+
+
+@pytest.mark.parametrize("n,vocab,dim,kind", [(5, 300, 32768, "bf16"), (40, 270, 32768, "f32"), (300, 70, 20001, "f16"), (33, 4, 9999, "bf16")])
+def test_the_widest_rows(torch, ctx, n, vocab, dim, kind):
+    """Many steps of the logits' sum, and many tiles of the gradients' columns."""
+    say("wide", n, vocab, dim, kind)
+    g, x, table, target = problem(torch, n, vocab, dim, kind, 0, 0, 51)
+    p = Plain(torch, x, table, 1.0)
+    loss, lse = ctx.cross_entropy(x, table, target)
+    check(torch, lse, p.lse, p.lse_off, "lse")
+    grad = randn(torch, g, n) * (64.0 if kind == "f16" else 1.0)
+    got = ctx.cross_entropy_backward(grad, x, table, target, lse)
+    q = torch.exp(p.z - lse.double()[:, None])
+    dz = q.clone()
+    dz[torch.arange(n, device="cuda"), target.long()] -= 1
+    rate = grad.double()[:, None]
+    check_grads(torch, got, x, table, dz * rate, q * p.q_off[:, None] * rate.abs() + 2 * U * dz.abs() * rate.abs(), kind, kind,
+                rate.abs().max(), "wide")
+    ctx.sync()
+
+
+def test_many_rows_of_few_tokens(torch, ctx):
+    """A sum over the rows in as many shares as fill the CUs, and partial sums of one tile."""
+    n, vocab, dim = 300001, 3, 33
+    g, x, table, target = problem(torch, n, vocab, dim, "f32", 0, 0, 61)
+    target[::7] = -1
+    loss, lse = ctx.cross_entropy(x, table, target)
+    p = Plain(torch, x, table, 1.0)
+    check(torch, lse, p.lse, p.lse_off, "lse")
+    grad = randn(torch, g, n)
+    dx, dw = ctx.cross_entropy_backward(grad, x, table, target, lse)
+    live = (target >= 0).double()[:, None]
+    q = torch.exp(p.z - lse.double()[:, None])
+    dz = (q - torch.nn.functional.one_hot(target.clamp(min=0).long(), vocab)) * grad.double()[:, None] * live
+    err = q * p.q_off[:, None] * grad.double().abs()[:, None] * live + 4 * U * dz.abs()
+    check(torch, dx, dz @ table.double(), err @ table.double().abs() + 40 * U * (dz.abs() @ table.double().abs()), "dx")
+    # of a share: steps of 32 rows, one after the other; then the shares
+    terms = n // 100 + 600
+    check(torch, dw, dz.T @ x.double(), err.T @ x.double().abs() + terms * U * (dz.abs().T @ x.double().abs()), "dtable")
+    ctx.sync()
