@@ -252,7 +252,9 @@ hgb_status run_backward(hgb_ctx* c, const Head& h, const HeadGrad& o, const Head
         x.sum = sum;
         x.sum_stride = p.width;
         x.add = first > 0;
-        HGB_TRY((launch_product<T, false, true, kSum>(c, x, p.dx)));
+        ProductPlan xp = p.dx;
+        xp.splits = std::min(xp.splits, x.k_steps);   // the last piece may be short: no share of it is empty
+        HGB_TRY((launch_product<T, false, true, kSum>(c, x, xp)));
 
         ProductArgs w{};
         w.a = Factor{planes, p.stride, h.n, p.piece, p.plane};

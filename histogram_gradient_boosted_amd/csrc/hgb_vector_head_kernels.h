@@ -319,7 +319,8 @@ __device__ __forceinline__ const ProductArgs& cold_args()
     return *(const ProductArgs*)p;
 }
 
-// An item of work: a tile of C and a share of its steps.
+// An item of work: a tile of C and a share of its steps, one at least (the
+// launch sees to that: no more shares than steps).
 struct Item {
     int m, n, split;
     int t0, t1;

@@ -176,13 +176,14 @@ def test_two_contexts_at_once(torch, hgb):
         c.close()
 
 
-@pytest.mark.parametrize("kind,out_kind", [("bf16", "bf16"), ("bf16", "f32"), ("f32", "f32")])
-def test_several_pieces_of_the_vocabulary(torch, ctx, kind, out_kind):
-    """More of the logits' gradient than is held at a time: sums over the pieces, and a target in each."""
+@pytest.mark.parametrize("kind,out_kind,last", [("bf16", "bf16", 0), ("bf16", "f32", 0), ("f32", "f32", 0), ("bf16", "bf16", 1), ("f32", "f32", 70)])
+def test_several_pieces_of_the_vocabulary(torch, ctx, kind, out_kind, last):
+    """More of the logits' gradient than is held at a time: sums over the pieces, and a target in each; a last piece of few tokens."""
     size = 4 if kind == "f32" else 2
     planes = 2 if out_kind != kind else 1
     n, dim = 5000, 24
-    vocab = (1 << 30) // (n * size * planes) * 5 // 2   # two pieces and a half
+    piece = (1 << 30) // (n * size * planes) // 256 * 256
+    vocab = piece + last if last else piece * 5 // 2
     say("pieces", n, vocab, dim, kind, out_kind)
     g, x, table, target = problem(torch, n, vocab, dim, kind, 0, 0, 31)
     target = (torch.rand(n, generator=g, device="cuda").double() * vocab).int()
