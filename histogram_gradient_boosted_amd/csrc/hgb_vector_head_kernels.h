@@ -105,7 +105,7 @@ __device__ inline Acc mma(const Frag<float>::type& a, const Frag<float>::type& b
 __device__ __forceinline__ void load_lds(uint32_t lds, uint32_t offset, const Rsrc& r)
 {
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(lds), "v"(offset), "s"(r)
-                 : "memory");
+                 : "memory", "m0");
 }
 
 constexpr uint32_t kNowhere = 0x80000000u;
