@@ -46,24 +46,6 @@ struct GateGradArgs {
     uint32_t* err;
 };
 
-// Reductions over the 2^log_group lanes that share a row.
-template <typename K, typename F>
-__device__ inline K row_reduce(K x, int log_group, F f)
-{
-    for (int s = 1; s < (1 << log_group); s *= 2) x = f(x, __shfl_xor(x, s));
-    return x;
-}
-template <typename K>
-__device__ inline K row_max(K x, int log_group)
-{
-    return row_reduce(x, log_group, [](K a, K b) { return a > b ? a : b; });
-}
-template <typename K>
-__device__ inline K row_sum(K x, int log_group)
-{
-    return row_reduce(x, log_group, [](K a, K b) { return a + b; });
-}
-
 // A logit as the gate takes it: NaN and +infinity are masked, and reported.
 __device__ inline float gate_logit(float l, bool* bad)
 {
