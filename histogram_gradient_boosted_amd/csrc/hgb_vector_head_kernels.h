@@ -356,15 +356,16 @@ __device__ __forceinline__ float2 row_stats(const Acc (&acc)[TN], float scale, f
 #pragma unroll
         for (int r = 0; r < 16; ++r) top = fmaxf(top, value(j, r));
     top = fmaxf(top, swap_halves(top));
-    top = top == -INFINITY ? 0.0f : top * scale;   // 2^-infinity is 0 from anywhere
+    top *= scale;
+    const float from = top == -INFINITY ? 0.0f : top;   // 2^-infinity is 0 from anywhere
     float sum[4] = {};
 #pragma unroll
     for (int j = 0; j < TN; ++j)
 #pragma unroll
-        for (int r = 0; r < 16; ++r) sum[r % 4] += __builtin_amdgcn_exp2f(__builtin_fmaf(value(j, r), scale, -top));
+        for (int r = 0; r < 16; ++r) sum[r % 4] += __builtin_amdgcn_exp2f(__builtin_fmaf(value(j, r), scale, -from));
     float all = (sum[0] + sum[1]) + (sum[2] + sum[3]);
     all += swap_halves(all);
-    return make_float2(top, all);
+    return make_float2(top, all);   // of no tokens (-infinity, 0), which joins nothing
 }
 
 // Blocks of a product's tile that a CU holds at a time.

@@ -289,6 +289,30 @@ def test_gradients_against_differences(torch, ctx, kind):
         assert bool(((dx.double() * way).sum(1) - rate).abs().le(bound).all()), (kind, heat)
 
 
+@pytest.mark.parametrize("kind", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("n,vocab", [(1, 1), (3, 65), (40, 200), (70, 129), (300, 257), (300, 1600)])
+@pytest.mark.parametrize("scale", [1.0, -1.0])
+def test_logits_all_far_from_zero(torch, ctx, kind, n, vocab, scale):
+    """Every logit near -600 or 600: places behind the vocabulary must not count as logits of zero."""
+    g = gen(torch, 71)
+    for side in (-1.0, 1.0):
+        x = torch.ones(n, 8, dtype=dt(torch, kind), device="cuda") + randn(torch, g, n, 8, dtype=dt(torch, kind), scale=0.05)
+        table = (75.0 * side * torch.ones(vocab, 8, device="cuda") + randn(torch, g, vocab, 8)).to(dt(torch, kind))
+        target = (torch.rand(n, generator=g, device="cuda") * vocab).int().clamp_(max=vocab - 1)
+        p = Plain(torch, x, table, scale)
+        loss, lse = ctx.cross_entropy(x, table, target, scale)
+        check(torch, lse, p.lse, p.lse_off, "lse")
+        want = p.lse - p.z.gather(1, target[:, None].long())[:, 0]
+        check(torch, loss, want, p.lse_off + p.z_off + 4 * U * p.z.abs().amax(1), "loss")
+        grad = torch.ones(n, device="cuda")
+        got = ctx.cross_entropy_backward(grad, x, table, target, lse, scale)
+        q = torch.exp(p.z - lse.double()[:, None])
+        dz = q.clone()
+        dz[torch.arange(n, device="cuda"), target.long()] -= 1
+        check_grads(torch, got, x, table, dz * scale, q * p.q_off[:, None] + 2 * U * dz.abs(), kind, kind, 1.0, "far")
+    ctx.sync()
+
+
 def test_batches_of_rows_and_other_streams(torch, hgb, ctx):
     g, x, table, target = problem(torch, 60, 90, 16, "bf16", 0, 0, 8)
     want, lse = ctx.cross_entropy(x, table, target)
