@@ -141,16 +141,18 @@ struct Loader {
 
     __device__ __forceinline__ void init(const Factor& f, int wave, int lane)
     {
-        const int stride = (int)(f.stride * SIZE);
+        // a tile's rows behind the last may wrap round 2^32: only what is in the
+        // factor is read, and those rows' results are not stored
+        const uint32_t stride = (uint32_t)(f.stride * SIZE);
 #pragma unroll
         for (int i = 0; i < N; ++i) {
             const int at = (wave * N + i) * 1024 + lane * 16, width = BY_K ? R * SIZE : kStepBytes;
             const int row = at / width, place = at % width / 16;
             const int chunk = BY_K ? by_k_place<T, R>(row, place) : along_place(row, place);
-            offset[i] = (uint32_t)(row * stride + chunk * 16);
+            offset[i] = (uint32_t)row * stride + (uint32_t)chunk * 16;
             head[i] = chunk * (16 / SIZE);
         }
-        step = BY_K ? STEP * stride : kStepBytes;
+        step = BY_K ? (int)(STEP * stride) : kStepBytes;
     }
 
     // to the tile from row (column) `first` on, at step k of a plane

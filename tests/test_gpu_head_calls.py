@@ -310,3 +310,61 @@ def test_many_rows_of_few_tokens(torch, ctx):
     terms = n // 100 + 600
     check(torch, dw, dz.T @ x.double(), err.T @ x.double().abs() + terms * U * (dz.abs().T @ x.double().abs()), "dtable")
     ctx.sync()
+
+
+@pytest.mark.parametrize("n,vocab,dim,kind,out_kind", [(1 << 24, 40, 8, "bf16", "bf16"), (1 << 23, 7, 24, "f32", "f32"), (8, 1 << 24, 8, "bf16", "f32"),
+                                                       (3, 1 << 24, 12, "f32", "f32"), (300, 1 << 24, 136, "bf16", "bf16")])
+def test_the_most_rows_and_tokens(torch, ctx, n, vocab, dim, kind, out_kind):
+    """Rows, table and logits' gradient beyond 4 GB, against 64 bits at some rows and some tokens."""
+    say("most", n, vocab, dim, kind, out_kind)
+    g, x, table, target = problem(torch, n, vocab, dim, kind, 0, 0, 83)
+    loss, lse = ctx.cross_entropy(x, table, target)
+    grad = randn(torch, g, n)
+    dx, dw = ctx.cross_entropy_backward(grad, x, table, target, lse, dtype=dt(torch, out_kind))
+    ctx.sync()
+    assert bool(dx.isfinite().all()) and bool(dw.isfinite().all())
+    step, tiny = half_step(torch, dt(torch, kind)) if kind != "f32" else (0.0, 0.0)
+    step2, tiny2 = half_step(torch, dt(torch, out_kind)) if out_kind != "f32" else (0.0, 0.0)
+    parts = 4 * ((vocab + 255) // 256)
+
+    def logits(rows, tokens):
+        """z, and how far 32 bits may be off."""
+        xd, wd = x[rows].double(), table[tokens].double()
+        return xd @ wd.T, (dim + 2) * U * (xd.abs() @ wd.abs().T)
+
+    def rates(rows, tokens):
+        """dz, and how far it may be off before its rounding."""
+        z, off = logits(rows, tokens)
+        q = torch.exp(z - lse[rows].double()[:, None])
+        rate = grad[rows].double()[:, None]
+        dz = (q - (target[rows].long()[:, None] == tokens[None]).double()) * rate
+        top = z.abs().amax() + lse[rows].double().abs().amax()
+        return dz, q * rate.abs() * (off + 8 * U * (top + 1)) + 2 * U * dz.abs()
+
+    some = torch.cat([torch.arange(min(n, 3), device="cuda"), torch.arange(max(0, n - 3), n, device="cuda"),
+                      torch.randint(0, n, (4,), generator=g, device="cuda")])
+    sums = torch.full((len(some),), -float("inf"), dtype=torch.float64, device="cuda")
+    off, top = torch.zeros_like(sums), torch.zeros_like(sums)
+    want, bound = torch.zeros(len(some), dim, dtype=torch.float64, device="cuda"), torch.zeros(len(some), dim, dtype=torch.float64, device="cuda")
+    for tokens in torch.arange(vocab, device="cuda").split(1 << 20):
+        z, far = logits(some, tokens)
+        sums = torch.logaddexp(sums, torch.logsumexp(z, 1))
+        off, top = torch.maximum(off, far.amax(1)), torch.maximum(top, z.abs().amax(1))
+        dz, far = rates(some, tokens)
+        wd = table[tokens].double()
+        want += dz @ wd
+        bound += (far + (step * 1.001 + (vocab + 300) * U) * dz.abs()) @ wd.abs()
+    check(torch, lse[some], sums, off + U * (128 + parts + 8 * top + 4 * sums.abs() + 8), "lse")
+    check(torch, dx[some], want, bound * (1 + step) + want.abs() * step * 1.001 + tiny, "dx")
+
+    some = torch.cat([torch.arange(min(vocab, 3), device="cuda"), torch.arange(max(0, vocab - 3), vocab, device="cuda"),
+                      torch.randint(0, vocab, (4,), generator=g, device="cuda")])
+    want, bound = torch.zeros(len(some), dim, dtype=torch.float64, device="cuda"), torch.zeros(len(some), dim, dtype=torch.float64, device="cuda")
+    held = step if out_kind == kind else step * step
+    terms = n // 100 + 600 if n > 100000 else 2 * n + 300   # many rows: more than 100 shares, then the shares
+    for rows in torch.arange(n, device="cuda").split(1 << 20):
+        dz, far = rates(rows, some)
+        xd = x[rows].double()
+        want += dz.T @ xd
+        bound += (far + (held * 1.001 + terms * U) * dz.abs()).T @ xd.abs()
+    check(torch, dw[some], want, bound * (1 + step2) + want.abs() * step2 * 1.001 + tiny2, "dtable")
