@@ -814,7 +814,7 @@ constexpr int kTeacherSlots = kDistillMaxTop / 64;
 
 struct TeacherRow {
     int32_t token[kTeacherSlots];
-    float t[kTeacherSlots];   // teacher / T - max
+    float t[kTeacherSlots];   // (teacher - max) / T
     float p[kTeacherSlots];
     float log_sum;
     bool some, bad;
@@ -841,7 +841,7 @@ __device__ inline TeacherRow teacher_row(const TeacherArgs& a, int64_t row, int 
             const int32_t t = a.token[row * a.top + k];
             if (t >= 0 && t < a.vocab) {
                 w.token[i] = t;
-                w.t[i] = teacher_at(a.teacher, a.teacher_type, row * a.top + k) / a.heat;
+                w.t[i] = teacher_at(a.teacher, a.teacher_type, row * a.top + k);
             } else if (t != -1) {
                 w.bad = true;
             }
@@ -854,7 +854,7 @@ __device__ inline TeacherRow teacher_row(const TeacherArgs& a, int64_t row, int 
     float sum = 0.0f;
 #pragma unroll
     for (int i = 0; i < kTeacherSlots; ++i) {
-        w.t[i] = w.t[i] == -INFINITY ? -INFINITY : w.t[i] - top;
+        w.t[i] = w.t[i] == -INFINITY ? -INFINITY : (w.t[i] - top) / a.heat;   // over T first, the largest values would be infinite
         w.p[i] = expf(w.t[i]);
         sum += w.p[i];
     }

@@ -170,6 +170,35 @@ def test_distill_and_its_gradients(torch, ctx, n, vocab, dim, kind, out_kind, sc
     ctx.sync()
 
 
+@pytest.mark.parametrize("kind", ["f32", "bf16"])
+@pytest.mark.parametrize("heat", [0.5, 1.0, 4.0])
+def test_teachers_of_the_types_lowest_and_largest_values(torch, ctx, kind, heat):
+    """A teacher masked with its type's lowest value, whole rows too: over the temperature that is no longer finite."""
+    g, x, table, _ = problem(torch, 5, 300, 16, kind, 0, 0, 3)
+    low, inf = torch.finfo(dt(torch, kind)).min, float("inf")
+    teacher = torch.full((5, 6), low, device="cuda")
+    teacher[1, 2] = 1.0
+    teacher[2, :3] = -inf
+    teacher[3, :2] = torch.tensor([1.0, 2.0], device="cuda")
+    teacher[4] = -low
+    tokens = torch.randperm(300, generator=g, device="cuda")[:30].view(5, 6).int()
+    p = Plain(torch, x, table, 1.0 / heat)
+    loss, lse, picked = ctx.distill(x, table, tokens, teacher.to(dt(torch, kind)), heat)
+    prob = torch.softmax((teacher.double() - teacher.double().amax(1, keepdim=True)) / heat, 1)
+    logp = torch.where(prob > 0, prob.log(), 0.0)
+    z = p.z.gather(1, tokens.long())
+    size = (prob * (logp.abs() + z.abs() + p.lse.abs()[:, None])).sum(1)
+    teacher_off = 24 * U
+    off = heat * heat * (p.lse_off + p.z_off + 4 * U * p.z.abs().amax(1) + (teacher_off + 14 * U) * (1 + size))
+    check(torch, loss, heat * heat * (prob * (logp - z + p.lse[:, None])).sum(1), off, "loss")
+    got = ctx.distill_backward(torch.ones(5, device="cuda"), x, table, tokens, teacher.to(dt(torch, kind)), lse, picked, heat)
+    q = torch.exp(p.z - lse.double()[:, None])
+    big = torch.zeros_like(q).scatter_add_(1, tokens.long(), prob)
+    off = (q * p.q_off[:, None] + big * teacher_off + 4 * U * (q + big)) * heat
+    check_grads(torch, got, x, table, (q - big) * heat, off, kind, kind, heat, "distill_backward")
+    ctx.sync()
+
+
 @pytest.mark.parametrize("kind", ["f32", "bf16", "f16"])
 def test_rows_without_a_target_reach_nothing(torch, ctx, kind):
     """NaN and infinities in padded rows, and beside what is read."""
