@@ -2,6 +2,7 @@
 // the logits' gradient.  Internal header: included by hgb_vector_gate.hip only.
 #pragma once
 
+#include <float.h>
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -274,6 +275,8 @@ __global__ __launch_bounds__(256) void k_gate(const GateArgs g)
             const float off = 2 * slack + 8 * 0x1p-24f * __uint_as_float(lanes_max(big, log_group));
             const bool even = per % V == 0 && (per / V & (per / V - 1)) == 0;   // a group is the whole of 2^k lanes
             const int mine = first / per;
+            // -infinity only where a key is: two finite keys may pass the lowest float
+            auto worth = [&](float a, float b) { return g.best == 1 ? a : b == -INFINITY ? b : fmaxf(a + b, -FLT_MAX); };
             if (even) {
                 float a = -INFINITY, b = -INFINITY;
 #pragma unroll
@@ -286,7 +289,7 @@ __global__ __launch_bounds__(256) void k_gate(const GateArgs g)
                     b = fmaxf(fminf(a, c), fmaxf(b, d));
                     a = fmaxf(a, c);
                 }
-                if (first < g.experts) sums[mine] = g.best == 1 ? a : a + b;   // all its lanes the same
+                if (first < g.experts) sums[mine] = worth(a, b);   // all its lanes the same
             } else {
                 for (int q = 0; q < g.groups; ++q) {
                     float a = -INFINITY, b = -INFINITY;
@@ -302,7 +305,7 @@ __global__ __launch_bounds__(256) void k_gate(const GateArgs g)
                         b = fmaxf(fminf(a, c), fmaxf(b, d));
                         a = fmaxf(a, c);
                     }
-                    if (l == 0) sums[q] = g.best == 1 ? a : a + b;
+                    if (l == 0) sums[q] = worth(a, b);
                 }
             }
             wave_order();

@@ -120,6 +120,31 @@ def test_ties_go_to_the_lower_expert_and_group(torch, ctx, score):
             check(torch, got[1], want[1], want[1] * SHARE + 2.0 ** -120, "share")
 
 
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("experts,groups", [(64, 4), (32, 4), (30, 5), (256, 8), (9, 3)])
+def test_biases_of_the_lowest_and_largest_values(torch, ctx, score, experts, groups):
+    """Two such keys are not finite in sum, and a group of them is still worth more than a masked one."""
+    g = gen(torch, 19)
+    most, per = torch.finfo(torch.float32).max, experts // groups
+    z = randn(torch, g, 70, experts)
+    low = torch.full((experts,), -most, device="cuda")
+    low[:per] = float("-inf")
+    mixed = low.clone()
+    mixed[-1] = 0.0
+    high = torch.zeros(experts, device="cuda")
+    high[per:] = most
+    last = low.clone()
+    last[per:] = float("-inf")
+    last[-per:] = -most
+    for bias in (low, mixed, high, last):
+        for keep in (1, 2):
+            got = ctx.gate(z, 2, score, bias, groups, keep)
+            want = reference(torch, z, 2, score, bias, groups, keep, 2, True, 1.0)
+            assert torch.equal(got[0].long(), want[0]), (keep, got[0][0], want[0][0])
+            check(torch, got[1], want[1], want[1] * SHARE + 2.0 ** -120, "share")
+    ctx.sync()
+
+
 def test_keys_closer_than_32_bits_hold_are_told_apart(torch, ctx):
     """The second expert's key is the larger by about 2^-30, and the lower index has the lesser."""
     n = 4096
