@@ -191,7 +191,7 @@ __device__ __forceinline__ int choose_exactly(const GateArgs& g, const T* logits
 // whole number, and the order is exact.  Elsewhere the number within the lane,
 // cut from the key's precision, and two keys that follow each other in a row's
 // order may be closer than their error:
-//   the cut        V 2^-23 |key|
+//   the cut        V 2^-23 |key|, of a key among the smallest numbers V 2^-149
 //   a softmax      27 2^-24 of the row's largest, 1 / sum: exp of a difference
 //                  d by exp2 is off by (2 |d| + 2) 2^-24 with |d| e^-|d| < 0.4,
 //                  the sum by 20 roundings, the quotient by 3
@@ -238,7 +238,8 @@ __global__ __launch_bounds__(256) void k_gate(const GateArgs g)
         float v[V];
         if (by_logit) {
 #pragma unroll
-            for (int j = 0; j < V; ++j) v[j] = z[j];
+            for (int j = 0; j < V; ++j) v[j] = z[j] + 0.0f;   // one zero
+            slack = FLT_MIN;   // zeros tie, whatever the cut makes of them
         } else {
             float bias[V];
             if (g.bias) load_vals<V>(bias, g.bias + first, g.experts - first);
