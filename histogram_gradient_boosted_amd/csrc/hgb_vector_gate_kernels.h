@@ -496,18 +496,36 @@ __global__ __launch_bounds__(256) void k_gate_grad(const GateGradArgs g)
         }
         dot = group_sum(dot, g.log_group);
     }
-    for (int k = l; k < g.top; k += lanes) {
-        int32_t e;
-        const float v = slot(k, &e);
-        if (v == -INFINITY) continue;
-        float d = g.grad[row * g.top + k];
-        if (!dense) {
+    // Gate names an expert once in a row, a caller may name it in several slots:
+    // those are summed in the slots' order, which float atomics do not keep.  A
+    // lane that does not find its own mark shares its expert.
+    for (int first = 0; first < g.top; first += lanes) {
+        const int k = first + l;
+        int32_t e = -1;
+        const float v = k < g.top ? slot(k, &e) : -INFINITY;
+        const bool counts = v != -INFINITY;
+        const float before = counts && first > 0 ? ds[e] : 0.0f;
+        wave_order();
+        if (counts) ds[e] = __int_as_float(l);
+        float d = counts ? g.grad[row * g.top + k] : 0.0f;
+        if (!dense && counts) {
             d = (d - dot) * (score(v) * over);
             if (g.score == HGB_SIGMOID) d *= 1.0f / (1.0f + expf(v));   // 1 - s
         }
-        atomicAdd(ds + e, d);
+        wave_order();
+        float all = before + d;
+        if (__ballot(counts && __float_as_int(ds[e]) != l)) {
+            all = before;
+            for (int j = 0; j < min(lanes, g.top - first); ++j) {
+                const int named = __shfl(counts ? e : -1, j, lanes);
+                const float add = __shfl(d, j, lanes);
+                if (named == e) all += add;
+            }
+        }
+        wave_order();
+        if (counts) ds[e] = all;   // the lanes of one expert the same
+        wave_order();
     }
-    wave_order();
 #pragma unroll
     for (int c = 0; c < V / W; ++c) {
         float out[W];

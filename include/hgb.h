@@ -666,7 +666,7 @@ hgb_status hgb_gate(hgb_ctx* ctx, const void* logits_dev, int32_t type, int64_t 
  * experts_dev: int32 [n_rows][top], as hgb_gate wrote them; the slots of -1
  *              are left out, and so are those of any other value outside
  *              [0, n_experts), which the next hgb_sync reports.  An expert that
- *              is named twice in a row counts twice.
+ *              a row names in several slots gets the sum of theirs, in order.
  * logits_dev, dlogits_dev: [n_rows][n_experts] of type `type`.
  * Errors: as for hgb_gate.
  */
