@@ -632,7 +632,8 @@ __global__ __launch_bounds__(64 * WM * WN) void k_product(const ProductArgs args
 }
 
 // Each row's rate, the factor of its logits' gradient (zero without one), and
-// the blocks' largest.
+// the blocks' largest finite one (from a rate that is not, no unit could be
+// made for the other rows).
 struct RateArgs {
     const float* grad;
     float scale;
@@ -667,7 +668,7 @@ __global__ __launch_bounds__(256) void k_head_rate(const RateArgs a)
         }
         const float r = live ? a.grad[i] * a.scale : 0.0f;
         a.rate[i] = r;
-        top = fmaxf(top, fabsf(r));
+        if (fabsf(r) < INFINITY) top = fmaxf(top, fabsf(r));
     }
     if (bad) atomicOr(a.err, kVecErrToken);
     for (int s = 32; s > 0; s >>= 1) top = fmaxf(top, __shfl_xor(top, s));
@@ -687,7 +688,7 @@ __device__ inline void rate_unit(float* words, int blocks, bool half)
     for (int s = 32; s > 0; s >>= 1) top = fmaxf(top, __shfl_xor(top, s));
     if (threadIdx.x == 0) {
         int e = 0;   // top in [2^(e - 1), 2^e)
-        if (half && top > 0.0f && top < INFINITY) (void)frexpf(top, &e);
+        if (half && top > 0.0f) (void)frexpf(top, &e);
         e = half ? max(-100, min(100, 15 - e)) : 0;
         words[0] = ldexpf(1.0f, e);
         words[1] = ldexpf(1.0f, -e);
