@@ -680,7 +680,8 @@ __global__ __launch_bounds__(256) void k_head_rate(const RateArgs a)
 // What the logits' gradient is multiplied by for its type, and one over it:
 // fp16 holds values of 2^-24 to 2^16, and a rate times a probability is often
 // less than the former, so the largest rate (of `blocks` blocks') is brought
-// between 2^14 and 2^15.  Powers of two: exact.
+// between 2^14 and 2^15 (below 2^-112 as near as 2^126 brings it, whose inverse
+// is the least normal number).  Powers of two: exact.
 __device__ inline void rate_unit(float* words, int blocks, bool half)
 {
     float top = 0.0f;
@@ -689,7 +690,7 @@ __device__ inline void rate_unit(float* words, int blocks, bool half)
     if (threadIdx.x == 0) {
         int e = 0;   // top in [2^(e - 1), 2^e)
         if (half && top > 0.0f) (void)frexpf(top, &e);
-        e = half ? max(-100, min(100, 15 - e)) : 0;
+        e = half ? min(126, 15 - e) : 0;   // -113 at least: top is below 2^128
         words[0] = ldexpf(1.0f, e);
         words[1] = ldexpf(1.0f, -e);
     }
