@@ -467,7 +467,7 @@ PyObject* gate(const Call& c)
     const float scale = real(c.args[8], "scale");
     if (z.dim > INT32_MAX) return status(kTooLarge);
     if (c.elsewhere()) return status(kElsewhere);
-    const int64_t slots = top > 0 ? top : 0;   // refused below
+    const int64_t slots = top > 0 && top <= z.dim ? top : 0;   // others are refused below
     const Tensor experts = c.make({z.n, slots}, at::kInt), share = c.make({z.n, slots}, at::kFloat);
     const hgb_status s = hgb_gate(c.ctx, z.p, z.type, z.stride, z.n, (int32_t)z.dim, score, (const float*)ptr(bias), groups, keep, best,
                                   top, renormalise, scale, (int32_t*)experts.data_ptr(), (float*)share.data_ptr());
