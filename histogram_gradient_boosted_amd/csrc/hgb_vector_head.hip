@@ -312,7 +312,7 @@ hgb_status backward(hgb_ctx* c, const Head& h, const HeadGrad& o, void* workspac
     HGB_HIP(c, hipSetDevice(c->device));
     ProfScope ps(c, HGB_KERNEL_HEAD);
     if (h.n == 0) {   // no rows: the table's gradient is zero
-        k_head_zero<<<fill_blocks(c, h.vocab * h.dim / 16), 256, 0, c->stream>>>((char*)o.dtable, o.dtable_stride * elem_size(o.dtable_type),
+        k_head_zero<<<fill_blocks(c, vec_ceil(h.vocab * h.dim, 16)), 256, 0, c->stream>>>((char*)o.dtable, o.dtable_stride * elem_size(o.dtable_type),
                                                                                h.vocab, h.dim * elem_size(o.dtable_type));
         HGB_LAUNCHED(c, "k_head_zero");
         return HGB_OK;

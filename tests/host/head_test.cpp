@@ -1,7 +1,7 @@
 // The gate and the head's losses on the host alone: their plans, what their C
 // entry points refuse, and what they ask of the runtime, whose launch functions
 // are this program's and run nothing.  No buffer is touched: addresses are made
-// up.  Usage: head_test plan | refusals | grids
+// up.  Usage: head_test plan | refusals | grids | no_rows
 #include "hgb_vector_head_plan.h"
 #ifdef WITH_LIBRARY
 #include "hgb_ctx.h"
@@ -162,6 +162,25 @@ static void grids()
     CHECK(launches > 0);
 }
 
+// Gradients of no rows: one launch each, which clears the table's gradient.
+static void no_rows()
+{
+    hgb_ctx c;   // no device behind it
+    c.dev_words = (uint32_t*)4096;
+    void *w = at(3), *dw = at(6);
+    for (int32_t type : {HGB_F32, HGB_BF16, HGB_F16})
+        for (int64_t vocab : {1, 2, 3, 5, 8, 15, 16, 17, 300, 1 << 24})
+            for (int64_t dim : {1, 2, 3, 4, 5, 7, 8, 16, 17, 1024})
+                for (int32_t out : {type, (int32_t)HGB_F32}) {
+                    const int before = launches;
+                    CHECK(hgb_cross_entropy_backward(&c, nullptr, nullptr, type, dim, 0, dim, w, dim, vocab, nullptr, -1, 1, nullptr,
+                                                     nullptr, dim, dw, out, dim, nullptr, 0) == HGB_OK);
+                    CHECK(hgb_distill_backward(&c, nullptr, nullptr, type, dim, 0, dim, w, dim, vocab, nullptr, nullptr, type, 4, 2,
+                                               nullptr, nullptr, nullptr, dim, dw, out, dim, nullptr, 0) == HGB_OK);
+                    CHECK(launches == before + 2);
+                }
+}
+
 static void refusals()
 {
     hgb_ctx c;   // no device behind it
@@ -275,6 +294,7 @@ int main(int argc, char** argv)
 #ifdef WITH_LIBRARY
     if (argc > 1 && !std::strcmp(argv[1], "refusals")) refusals();
     if (argc > 1 && !std::strcmp(argv[1], "grids")) grids();
+    if (argc > 1 && !std::strcmp(argv[1], "no_rows")) no_rows();
 #endif
     CHECK(checks > 0);
     std::printf(failures ? "%d of %d checks failed\n" : "%d of %d failed: all checks passed\n", failures, checks);

@@ -46,6 +46,10 @@ def test_every_accepted_size_fits_a_launch(program):
     run(program, "grids")
 
 
+def test_gradients_of_no_rows_fit_a_launch(program):
+    run(program, "no_rows")
+
+
 @pytest.fixture()
 def ctx():
     import torch
