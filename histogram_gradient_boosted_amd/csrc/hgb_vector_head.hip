@@ -47,7 +47,7 @@ hgb_status check_head(hgb_ctx* c, const Head& h)
     if (h.dim > kHeadMaxDim) return fail(c, HGB_E_UNSUPPORTED, "%s: dim is above %lld", h.verb, (long long)kHeadMaxDim);
     HGB_TRY(check_rows(c, h.verb, "x", h.x, h.type, h.n, h.dim, h.x_stride));
     HGB_TRY(check_rows(c, h.verb, "table", h.table, h.type, h.vocab, h.dim, h.table_stride));
-    if (!std::isfinite(h.scale)) return fail(c, HGB_E_INVALID, "%s: the logits' scale is not finite", h.verb);
+    if (!std::isfinite(h.scale * kLog2e)) return fail(c, HGB_E_INVALID, "%s: the logits' scale times log2(e) is not finite", h.verb);
     if (h.top < 1) return fail(c, HGB_E_INVALID, "%s: top must be positive", h.verb);
     if (h.top > kDistillMaxTop) return fail(c, HGB_E_UNSUPPORTED, "%s: top is above %d", h.verb, kDistillMaxTop);
     if (h.n > 0 && !h.token) return fail(c, HGB_E_INVALID, "%s: the tokens are null", h.verb);
@@ -59,6 +59,7 @@ hgb_status check_teacher(hgb_ctx* c, const Head& h, float temperature)
 {
     if (!(temperature > 0.0f) || std::isinf(temperature))
         return fail(c, HGB_E_INVALID, "%s: the temperature must be positive and finite", h.verb);
+    if (std::isinf(temperature * temperature)) return fail(c, HGB_E_INVALID, "%s: the temperature's square is not finite", h.verb);
     if (h.n > 0 && !h.teacher) return fail(c, HGB_E_INVALID, "%s: teacher is null", h.verb);
     HGB_TRY(check_rows(c, h.verb, "teacher", h.teacher, h.teacher_type, h.n, 1, 1));
     if (h.teacher_type != h.type && h.teacher_type != HGB_F32)

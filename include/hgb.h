@@ -691,8 +691,8 @@ hgb_status hgb_gate_backward(hgb_ctx* ctx, const float* grad_dev, const void* lo
  *              start at 16 bytes, or end inside 16, are copied there first.
  * A row with a logit that is NaN or +infinity has no finite loss.
  * Errors: HGB_E_INVALID for null or misaligned pointers, n_rows below 0, vocab
- *         or dim below 1, strides below dim, a scale that is not finite, a
- *         workspace too small; HGB_E_UNSUPPORTED for n_rows or vocab above
+ *         or dim below 1, strides below dim, a scale that times log2(e) is not
+ *         finite, a workspace too small; HGB_E_UNSUPPORTED for n_rows or vocab above
  *         2^24 or dim above 32,768.
  */
 hgb_status hgb_cross_entropy(hgb_ctx* ctx, const void* x_dev, int32_t type, int64_t x_stride, int64_t n_rows, int64_t dim,
@@ -743,8 +743,9 @@ hgb_status hgb_cross_entropy_backward(hgb_ctx* ctx, const float* grad_dev, const
  * teacher_dev: [n_rows][top] of type teacher_type, `type` or HGB_F32.
  * picked_dev:  float [n_rows][top]; written: z at the slots' tokens, 0 for a
  *              slot that is left out for its token.
- * Errors: as for hgb_cross_entropy, and HGB_E_INVALID for a temperature that is
- *         not positive and finite, top below 1; HGB_E_UNSUPPORTED for top above
+ * Errors: as for hgb_cross_entropy (with 1 / T as the scale), and HGB_E_INVALID
+ *         for a temperature that is not positive, or whose square is not finite,
+ *         top below 1; HGB_E_UNSUPPORTED for top above
  *         256 or another teacher_type.
  */
 hgb_status hgb_distill(hgb_ctx* ctx, const void* x_dev, int32_t type, int64_t x_stride, int64_t n_rows, int64_t dim,

@@ -1,7 +1,7 @@
 // The gate and the head's losses on the host alone: their plans, what their C
 // entry points refuse, and what they ask of the runtime, whose launch functions
 // are this program's and run nothing.  No buffer is touched: addresses are made
-// up.  Usage: head_test plan | refusals | grids | no_rows
+// up.  Usage: head_test plan | refusals | grids | no_rows | factors
 #include "hgb_vector_head_plan.h"
 #ifdef WITH_LIBRARY
 #include "hgb_ctx.h"
@@ -162,6 +162,31 @@ static void grids()
     CHECK(launches > 0);
 }
 
+// Factors that are finite, and not so as the kernels take them: the logits'
+// times log2(e), the loss's T^2.
+static void factors()
+{
+    hgb_ctx c;   // no device behind it
+    c.dev_words = (uint32_t*)4096;
+    void *x = at(1), *w = at(3), *dx = at(5), *dw = at(6), *ws = at(14), *teacher = at(7);
+    float *loss = (float*)at(8), *lse = (float*)at(9), *picked = (float*)at(10), *grad = (float*)at(11);
+    int32_t* tok = (int32_t*)at(12);
+    auto takes = [&](float scale) {
+        return hgb_cross_entropy(&c, x, HGB_F32, 4, 2, 4, w, 4, 9, tok, -1, scale, loss, lse, ws, kRoom) == HGB_OK;
+    };
+    auto heats = [&](float t) {
+        const hgb_status s = hgb_distill(&c, x, HGB_F32, 4, 2, 4, w, 4, 9, tok, teacher, HGB_F32, 3, t, loss, lse, picked, ws, kRoom);
+        const hgb_status b = hgb_distill_backward(&c, grad, x, HGB_F32, 4, 2, 4, w, 4, 9, tok, teacher, HGB_F32, 3, t, lse, picked, dx, 4,
+                                                  dw, HGB_F32, 4, ws, kRoom);
+        CHECK(s == b && (s == HGB_OK || s == HGB_E_INVALID));
+        return s == HGB_OK;
+    };
+    CHECK(takes(2.3e38f) && takes(-2.3e38f) && takes(0.0f) && takes(-0.5f) && takes(1e-45f));
+    CHECK(!takes(2.4e38f) && !takes(-3.4e38f) && !takes(NAN));
+    CHECK(heats(1.8e19f) && heats(1.0f) && heats(1e-18f) && heats(5e-39f));
+    CHECK(!heats(1.9e19f) && !heats(3.4e38f) && !heats(4e-39f) && !heats(1e-45f));
+}
+
 // Gradients of no rows: one launch each, which clears the table's gradient.
 static void no_rows()
 {
@@ -295,6 +320,7 @@ int main(int argc, char** argv)
     if (argc > 1 && !std::strcmp(argv[1], "refusals")) refusals();
     if (argc > 1 && !std::strcmp(argv[1], "grids")) grids();
     if (argc > 1 && !std::strcmp(argv[1], "no_rows")) no_rows();
+    if (argc > 1 && !std::strcmp(argv[1], "factors")) factors();
 #endif
     CHECK(checks > 0);
     std::printf(failures ? "%d of %d checks failed\n" : "%d of %d failed: all checks passed\n", failures, checks);

@@ -50,6 +50,10 @@ def test_gradients_of_no_rows_fit_a_launch(program):
     run(program, "no_rows")
 
 
+def test_factors_that_overflow_in_the_kernels_are_refused(program):
+    run(program, "factors")
+
+
 @pytest.fixture()
 def ctx():
     import torch
