@@ -101,11 +101,16 @@ __device__ inline Acc mma(const Frag<float>::type& a, const Frag<float>::type& b
 }
 
 // 64 lanes' 16 bytes each, from memory to consecutive places in LDS.  An
-// offset past the descriptor's bytes gives zeros.
+// offset past the descriptor's bytes gives zeros.  m0, which holds the place in
+// LDS, is the asm's own: an output of the s_mov (as a clobber it gives a
+// warning, being a reserved register).
 __device__ __forceinline__ void load_lds(uint32_t lds, uint32_t offset, const Rsrc& r)
 {
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(lds), "v"(offset), "s"(r)
-                 : "memory", "m0");
+    uint32_t m0;
+    asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tbuffer_load_dwordx4 %2, %3, 0 offen lds"
+                 : "={m0}"(m0)
+                 : "s"(lds), "v"(offset), "s"(r)
+                 : "memory");
 }
 
 constexpr uint32_t kNowhere = 0x80000000u;
