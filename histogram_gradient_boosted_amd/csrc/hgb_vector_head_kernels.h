@@ -392,13 +392,15 @@ constexpr int product_blocks(int bm, int bn, int waves, bool strips) { return kL
 // Four waves of 128 x 128 read the least of LDS for their products (8 KB each
 // for 16 matrix instructions, half of what LDS gives in that time; eight waves
 // of 128 x 64 would take three quarters, beside a quarter for the loads), and
-// their 256 results a lane leave 256 registers for all else: one wave a SIMD.
+// their 256 results a lane leave 256 registers for all else: one wave a SIMD
+// (12 to 164 bytes a lane go to scratch where a tile of logits, dz or C itself
+// is finished, none between the products).  Tiles of 128 x 128 have two.
 // Bound by the matrix instructions (64% of the time at 8,192^3 bf16, 1.20
 // PFLOP/s; the rest are waits at the step's barrier and for fragments), and for
 // short sums by the tiles' ends: 16,384 x 32,768 logits of 1,024 values 0.99 ms
 // (1.11 PFLOP/s), of 512 0.57 (0.97).
 template <typename T, int BM, int BN, int WM, int WN, bool A_BY_K, bool B_BY_K, int WHAT>
-__global__ __launch_bounds__(64 * WM * WN) void k_product(const ProductArgs args)
+__global__ __launch_bounds__(64 * WM * WN, tile_blocks(BM, BN) * WM * WN / 4) void k_product(const ProductArgs args)
 {
     constexpr int WAVES = WM * WN, TM = BM / WM / 32, TN = BN / WN / 32;
     constexpr int STAGE = (BM + BN) * kStepBytes, STRIP = strip_bytes(BM, BN);

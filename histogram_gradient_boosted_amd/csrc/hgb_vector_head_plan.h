@@ -26,15 +26,22 @@ constexpr int64_t kPieceBytes = (int64_t)1 << 30;   // of the logits' gradient t
 constexpr int64_t kStatBytes = (int64_t)1 << 29;    // of the forward pass's partial sums
 
 // The tiles of a product: rows x columns of a block of four waves, side by side
-// in `wn` columns; how many such blocks a CU's LDS holds; and how much of the
-// largest tile's rate their products reach, in 16 and in 32 bits (the products
-// of 32-bit values take eight times as long, and hide the rest).
+// in `wn` columns; how many such blocks a CU holds, by its LDS and by its
+// registers (the kernels are built for that many); and how much of the largest
+// tile's rate their products reach, in 16 and in 32 bits (the products of
+// 32-bit values take eight times as long, and hide the rest).
 struct Tile {
     int bm, bn, wn, per_cu;
     float rate16, rate32;
 };
 constexpr Tile kTiles[] = {{256, 256, 2, 1, 1.0f, 1.0f}, {128, 128, 2, 2, 0.75f, 0.95f}, {256, 64, 1, 1, 0.5f, 0.9f}, {32, 256, 4, 1, 0.3f, 0.5f}};
 enum { kTileLarge, kTileMiddle, kTileNarrow, kTileLow };
+constexpr int tile_blocks(int bm, int bn)
+{
+    for (const Tile& t : kTiles)
+        if (t.bm == bm && t.bn == bn) return t.per_cu;
+    return 0;
+}
 
 // A product's launch: C [m][n], summed over k in steps, in `splits` shares of
 // the steps.
