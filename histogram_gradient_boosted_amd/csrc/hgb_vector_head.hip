@@ -188,6 +188,8 @@ struct HeadGrad {
     int64_t dtable_stride;
 };
 
+int wide_planes(int32_t type) { return type == HGB_BF16 ? kPlanesBf16 : kPlanesF16; }
+
 template <typename T>
 hgb_status run_backward(hgb_ctx* c, const Head& h, const HeadGrad& o, const HeadGradPlan& p, char* ws)
 {
@@ -207,9 +209,9 @@ hgb_status run_backward(hgb_ctx* c, const Head& h, const HeadGrad& o, const Head
         fw = Factor{ws + p.off_table, p.dp, h.vocab, p.dp, 0};
     }
     constexpr int STEP = kStepBytes / (int)sizeof(T);
-    // Where dz has a second plane, what its rounding left, that comes first: the
-    // sum over both then adds up the small values before the large.
-    T *planes = (T*)(ws + p.off_z), *dz = planes + (p.planes > 1 ? p.plane : 0);
+    // Where dz has more planes, what its rounding left, they come first, the last
+    // one in front: the sum over all then adds up the small values before the large.
+    T *planes = (T*)(ws + p.off_z), *dz = planes + (p.planes - 1) * p.plane;
     float *sum = (float*)(ws + p.off_dx), *dw = (float*)(ws + p.off_dw);
     for (int64_t first = 0; first < h.vocab; first += p.piece) {
         const int64_t tokens = std::min(p.piece, h.vocab - first);
@@ -232,7 +234,7 @@ hgb_status run_backward(hgb_ctx* c, const Head& h, const HeadGrad& o, const Head
         z.unit = unit;
         z.dz = dz;
         z.dz_stride = p.stride;
-        z.dz_plane = planes - dz;
+        z.dz_plane = p.planes > 1 ? -p.plane : 0;
         ProductPlan zp = p.z;
         zp.tiles_n = vec_ceil(tokens, zp.bn);
         HGB_TRY((launch_product<T, false, false, kGrad>(c, z, zp)));
@@ -302,7 +304,8 @@ hgb_status backward(hgb_ctx* c, const Head& h, const HeadGrad& o, void* workspac
     if (h.n > 0 && (!o.grad || !o.lse || (h.teacher && !o.picked))) return fail(c, HGB_E_INVALID, "%s: an input is null", h.verb);
     HGB_TRY(check_words(c, h.verb, {o.grad, o.lse, o.picked}));
     const int64_t n = std::max<int64_t>(h.n, 1);
-    const HeadGradPlan p = plan_head_grad(h.copy_table(), h.size(), elem_size(o.dtable_type), n, h.vocab, h.dim);
+    const HeadGradPlan p = plan_head_grad(h.copy_table(), h.size(), elem_size(o.dtable_type), n, h.vocab, h.dim,
+                                         wide_planes(h.type));
     if (h.n > 0) HGB_TRY(check_workspace(c, h.verb, workspace, workspace_bytes, p.bytes));
     HGB_TRY(check_apart(c, h.verb,
                         {span(o.dx, h.type, h.n, h.dim, o.dx_stride), span(o.dtable, o.dtable_type, h.vocab, h.dim, o.dtable_stride),
@@ -348,7 +351,8 @@ int64_t hgb_head_backward_workspace(const void*, int64_t, const void* table, int
     if (!head_sizes(type, n_rows, vocab, dim) || !is_type(dtable_type)) return -1;
     if (n_rows == 0) return 0;
     const int size = elem_size(type);
-    return plan_head_grad(!in_place(table, table_stride, dim, size), size, elem_size(dtable_type), n_rows, vocab, dim).bytes;
+    return plan_head_grad(!in_place(table, table_stride, dim, size), size, elem_size(dtable_type), n_rows, vocab, dim, wide_planes(type))
+        .bytes;
 }
 
 hgb_status hgb_cross_entropy(hgb_ctx* c, const void* x, int32_t type, int64_t x_stride, int64_t n_rows, int64_t dim, const void* table,

@@ -55,7 +55,7 @@ struct ProductArgs {
     const float* rate;
     const float* unit;   // what dz is multiplied by
     void* dz;
-    int64_t dz_stride, dz_plane;
+    int64_t dz_stride, dz_plane;   // from dz to the plane of what its rounding left, and on to the next; 0: none
 
     // sums
     float* sum;          // [splits][m][sum_stride]
@@ -66,6 +66,10 @@ struct ProductArgs {
     int out_type;
     const float* factor;   // of C, or null
 };
+
+// The planes that dz has where it has more than one.
+template <typename T>
+constexpr int kPlanes = std::is_same<T, __bf16>::value ? kPlanesBf16 : kPlanesF16;
 
 // What becomes of C: the logits' maxima and sums by rows and parts of 64 to 128
 // tokens; the logits' gradient dz; a sum in 32 bits, by shares; or C itself.
@@ -592,6 +596,16 @@ __global__ __launch_bounds__(64 * WM * WN, tile_blocks(BM, BN) * WM * WN / 4) vo
                                 }
                             }
                             store_strip<LEFT>(v, strip, lane, g.m - m0 - i * 32, W * 32, true, out + j * 32, g.dz_stride, g.dz_plane);
+                            if constexpr (LEFT && kPlanes<T> == 3) {
+#pragma unroll
+                                for (int h = 0; h < W; ++h)
+#pragma unroll
+                                    for (int r = 0; r < 16; ++r) {
+                                        v[h][r] -= (float)(T)v[h][r];
+                                        v[h][r] -= (float)(T)v[h][r];
+                                    }
+                                store_strip(v, strip, lane, g.m - m0 - i * 32, W * 32, true, out + 2 * g.dz_plane + j * 32, g.dz_stride);
+                            }
                             __builtin_amdgcn_sched_barrier(0);
                         }
                     };
@@ -957,7 +971,11 @@ __global__ __launch_bounds__(256) void k_distill_dz(int64_t n, const TeacherArgs
             const float d = r * (q - p[i]);
             T* at = dz + row * dz_stride + to;
             *at = (T)d;
-            if (dz_plane) at[dz_plane] = (T)(d - (float)(T)d);
+            if (dz_plane) {
+                const float rest = d - (float)(T)d;
+                at[dz_plane] = (T)rest;
+                if (kPlanes<T> == 3) at[2 * dz_plane] = (T)(rest - (float)(T)rest);
+            }
         }
     }
 }

@@ -22,7 +22,15 @@ constexpr int kStepBytes = 128;   // of a row that one step of a product's sum t
 constexpr int kRateBlocks = 256;
 constexpr int kRateWords = 2 + kRateBlocks;   // behind the rates: their unit, one over it, the blocks' largest
 
-constexpr int64_t kPieceBytes = (int64_t)1 << 30;   // of the logits' gradient that is held at a time
+// Of the logits' gradient that is held at a time, for up to two planes (a third
+// takes half as much again: in pieces of as many bytes 4,096 x 262,144 x 512
+// took 8.2 ms for 6.7); at least a tile's tokens of every row.
+constexpr int64_t kPieceBytes = (int64_t)1 << 30;
+// Planes of the logits' gradient beside a 32-bit dtable of 16-bit inputs, each
+// what the ones before it left: together they hold 24 bits.  Two of bf16 would
+// hold 17, and dtable's error would be 1.75 times that of one from 32-bit
+// values (2.6e-6 and 1.5e-6 for 4,096 x 262,144 x 512).
+constexpr int kPlanesBf16 = 3, kPlanesF16 = 2;
 constexpr int64_t kStatBytes = (int64_t)1 << 29;    // of the forward pass's partial sums
 
 // The tiles of a product: rows x columns of a block of four waves, side by side
@@ -126,7 +134,7 @@ struct HeadGradPlan {
     int64_t dp = 0;
     int64_t piece = 0;         // tokens of a piece, whole tiles
     int64_t pieces = 0;
-    int planes = 1;            // of the logits' gradient: 2 beside a 32-bit dtable of 16-bit inputs
+    int planes = 1;            // of the logits' gradient
     int64_t stride = 0;        // values of a row of the logits' gradient
     int64_t plane = 0;         // values of a plane
     int64_t width = 0;         // floats of a partial row
@@ -134,14 +142,16 @@ struct HeadGradPlan {
     int64_t off_table = 0, off_rate = 0, off_z = 0, off_dx = 0, off_dw = 0, bytes = 0;
 };
 
-inline HeadGradPlan plan_head_grad(bool copy_table, int size, int dtable_size, int64_t n, int64_t vocab, int64_t dim)
+inline HeadGradPlan plan_head_grad(bool copy_table, int size, int dtable_size, int64_t n, int64_t vocab, int64_t dim,
+                                   int wide = kPlanesF16)   // planes beside a wider dtable
 {
     HeadGradPlan p;
     p.copy_table = copy_table;
     p.dp = vec_up(dim, 16 / size);
-    p.planes = dtable_size > size ? 2 : 1;
+    p.planes = dtable_size > size ? wide : 1;
     const int64_t whole = vec_up(vocab, kTileCols);
-    p.piece = std::min(whole, std::max<int64_t>(kTileCols, kPieceBytes / (n * size * p.planes) / kTileCols * kTileCols));
+    const int64_t room = kPieceBytes / (n * size * std::min(p.planes, 2));
+    p.piece = std::min(whole, std::max<int64_t>(kTileCols, room / kTileCols * kTileCols));
     p.pieces = vec_ceil(vocab, p.piece);
     // rows a large power of two apart would share the channels of L2 and memory
     p.stride = p.piece + 128 / size;

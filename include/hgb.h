@@ -714,8 +714,8 @@ int64_t hgb_head_backward_workspace(const void* x_dev, int64_t x_stride, const v
  * in pieces of the vocabulary: a piece of dz, computed again from x and table,
  * is the most that the workspace holds of it.  dz is rounded to the inputs'
  * type as a factor of the two products (beside a 32-bit dtable of 16-bit
- * inputs, to twice its bits for dtable).  What x holds in rows without a
- * gradient reaches nothing; dx is zero there.
+ * inputs, to three parts of bf16 or two of fp16 for dtable).  What x holds in
+ * rows without a gradient reaches nothing; dx is zero there.
  *
  * grad_dev:   float [n_rows].  lse_dev: as hgb_cross_entropy wrote it.
  * dx_dev:     [n_rows][dim] of type `type`.

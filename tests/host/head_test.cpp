@@ -1,7 +1,7 @@
 // The gate and the head's losses on the host alone: their plans, what their C
 // entry points refuse, and what they ask of the runtime, whose launch functions
 // are this program's and run nothing.  No buffer is touched: addresses are made
-// up.  Usage: head_test plan | refusals | grids | no_rows | factors
+// up.  Usage: head_test plan | planes | refusals | grids | no_rows | factors
 #include "hgb_vector_head_plan.h"
 #ifdef WITH_LIBRARY
 #include "hgb_ctx.h"
@@ -81,6 +81,21 @@ static void plans()
     alignas(16) char row[64];
     CHECK(in_place(row, 16, 8, 2) && !in_place(row + 2, 16, 8, 2) && !in_place(row, 15, 8, 2) && !in_place(row, 16, 7, 2));
     CHECK(in_place(row, 4, 4, 4) && !in_place(row, kHeadMaxStride + 8, 8, 2));
+}
+
+// Three planes of bf16's logits' gradient beside a 32-bit dtable.
+static void planes()
+{
+    for (int64_t n : kRows)
+        for (int64_t vocab : kVocabs)
+            for (int64_t dim : kDims) {
+                const HeadGradPlan p = plan_head_grad(true, 2, 4, n, vocab, dim, kPlanesBf16);
+                CHECK(p.planes == 3 && plan_head_grad(true, 2, 2, n, vocab, dim, kPlanesBf16).planes == 1);
+                CHECK(p.piece == kTileCols || n * p.piece * 2 * 2 <= kPieceBytes);   // a third plane takes half as much again
+                CHECK(p.piece % kTileCols == 0 && p.pieces * p.piece >= vocab && (p.pieces - 1) * p.piece < vocab);
+                CHECK(p.plane == n * p.stride && p.off_dx >= p.off_z + 3 * p.plane * 2 && p.off_dx % 16 == 0);
+                check_product(p.dw, std::min(p.piece, vocab), dim, vec_ceil(n, kStepBytes / 2) * 3);
+            }
 }
 
 #ifdef WITH_LIBRARY
@@ -316,6 +331,7 @@ static void refusals()
 int main(int argc, char** argv)
 {
     if (argc > 1 && !std::strcmp(argv[1], "plan")) plans();
+    if (argc > 1 && !std::strcmp(argv[1], "planes")) planes();
 #ifdef WITH_LIBRARY
     if (argc > 1 && !std::strcmp(argv[1], "refusals")) refusals();
     if (argc > 1 && !std::strcmp(argv[1], "grids")) grids();

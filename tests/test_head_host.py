@@ -26,6 +26,12 @@ def test_plans_under_sanitizers(tmp_path):
     run(exe, "plan", ASAN_OPTIONS="detect_leaks=1:abort_on_error=0")
 
 
+def test_plans_of_three_planes_under_sanitizers(tmp_path):
+    exe = str(tmp_path / "head_test")
+    subprocess.run(["g++", "-std=c++17", "-O1", *SAN, "-I", os.path.join(PKG, "csrc"), "-o", exe, SOURCE], check=True)
+    run(exe, "planes", ASAN_OPTIONS="detect_leaks=1:abort_on_error=0")
+
+
 @pytest.fixture(scope="module")
 def program(tmp_path_factory):
     if not os.path.exists(os.path.join(PKG, "libhgb.so")):
