@@ -544,8 +544,9 @@ class Context:
         [experts], for the choice alone) are chosen, out of the `keep` of `groups` equal
         runs of experts whose `best` largest are largest in sum.  share: scale
         times the score, over the chosen scores' sum with renormalise.  An
-        expert of logit or bias -inf is masked; a row with too few left has
-        expert -1 and share 0 behind them."""
+        expert of logit or bias -inf is masked (a group of fewer than `best`
+        others counts as one of none); a row with too few left has expert -1
+        and share 0 behind them."""
         return self._verb("gate", logits, top, score, bias, groups, keep, best, renormalise, scale)
 
     def gate_backward(self, grad, logits, experts, score: str = "softmax", renormalise: bool = True, scale: float = 1.0,
@@ -565,7 +566,10 @@ class Context:
     def cross_entropy_backward(self, grad, x, table, targets, lse, scale: float = 1.0, pad: int = -1, dtype=None, out=None):
         """Gradients of cross_entropy: (dx, dtable), from the losses' gradients
         `grad` (float32).  dtable: [vocab, dim] of `dtype` (x's type, or
-        float32); out: where dx goes."""
+        float32); out: where dx goes.  The logits' gradient is rounded to x's
+        type on the way (for a float32 dtable to two or three parts of it); in
+        float16 by steps of 2^-38 of the largest scale * grad, which rows of
+        much smaller gradients feel."""
         return self._verb("cross_entropy_backward", grad, x, table, targets, lse, scale, pad, dtype, out)
 
     def distill(self, x, table, tokens, teacher, temperature: float = 1.0):

@@ -106,8 +106,8 @@ __device__ __forceinline__ void wave_first(double* best, int* at)
 
 // The chosen experts of one row in order into list[0 .. top), by keys in 64
 // bits and by a whole wave: key[experts] and worth[groups] in LDS are its own.
-// Returns how many.  Seldom run, but then the last wave of a call may run it:
-// 2 us a row of 256 experts, 8 of them in order.
+// Returns how many.  2 us a row of 256 experts, 8 of them in order, one row of
+// the wave after the other: the last wave of a call may run it.
 template <typename T>
 __device__ __forceinline__ int choose_exactly(const GateArgs& g, const T* logits, float most, double* key, double* worth, int32_t* list)
 {
@@ -196,11 +196,14 @@ __device__ __forceinline__ int choose_exactly(const GateArgs& g, const T* logits
 //                  d by exp2 is off by (2 |d| + 2) 2^-24 with |d| e^-|d| < 0.4,
 //                  the sum by 20 roundings, the quotient by 3
 //   a sigmoid      3 2^-24: s (1 - s) (2 |z| + 2) < 1, and two roundings
-// and the sum with the bias 2^-24 |key|.  Such a row (about one in 1,300 of
-// 256 experts) is chosen again by its whole wave in 64 bits.  Bound by vector
-// instructions: a row of 256 costs a wave about 300, half of them for the 9
-// maxima.  32,768 rows of 256, 8 of them out of 4 of 8 groups: 38 us, 27
-// without the rows that are chosen again; with 64-bit keys throughout 103.
+// and the sum with the bias 2^-24 |key|.  Such a row is chosen again by its
+// whole wave in 64 bits: about one in 1,300 of 256 distinct 32-bit logits, but
+// one in three of 256 logits of bf16 whose keys are equal where they are (with
+// groups, or a bias of zeros).  Bound by vector instructions: a row of 256
+// costs a wave about 300, half of them for the 9 maxima.  32,768 rows of 256, 8
+// of them out of 4 of 8 groups: 38 to 49 us, as the last wave falls, 27 without
+// the rows that are chosen again, with 64-bit keys throughout 103; bf16 without
+// a bias 109, logits that are all equal 130.
 template <typename T, int V>
 __global__ __launch_bounds__(256) void k_gate(const GateArgs g)
 {
@@ -292,6 +295,9 @@ __global__ __launch_bounds__(256) void k_gate(const GateArgs g)
                 }
                 if (first < g.experts) sums[mine] = worth(a, b);   // all its lanes the same
             } else {
+                // One group after the other, each by all lanes: for few groups.
+                // 32,768 rows, 16 experts chosen: 990 in 33 groups 0.49 ms, 1,008
+                // in 63 (whole lanes) 0.24, 1,023 in 341 6.6, in 1,023 50.
                 for (int q = 0; q < g.groups; ++q) {
                     float a = -INFINITY, b = -INFINITY;
 #pragma unroll

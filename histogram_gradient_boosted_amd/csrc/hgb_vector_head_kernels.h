@@ -573,6 +573,10 @@ __global__ __launch_bounds__(64 * WM * WN, tile_blocks(BM, BN) * WM * WN / 4) vo
                 } else {
                     T* out = (T*)g.dz + (int64_t)(m0 + i * 32) * g.dz_stride + n0;
                     char* strip = smem + 2 * STAGE + wave * STRIP;
+                    // dz is rounded to T, its products' type: half a step of each
+                    // value, and in dx of bf16 an error of 2.4e-3 where rounding
+                    // the result alone leaves 1.7e-3.  More planes in dx too would
+                    // double its steps; they are for a 32-bit dtable (kPlanes).
                     auto store = [&](auto left_over) {
                         constexpr bool LEFT = decltype(left_over)::value;
                         constexpr int W = strip_width(STRIP, TN, sizeof(T), LEFT);

@@ -632,8 +632,10 @@ hgb_status hgb_route_combine_backward(hgb_ctx* ctx, const void* grad_dev, int32_
  *   share = scale * s, or with renormalise scale * s / the sum of the chosen s
  *
  * An expert whose logit or bias is -infinity is masked: its key is -infinity
- * (also in its group's worth), it is never chosen, and its softmax is 0 where
- * the logit is.  So is one whose logit or bias is NaN or +infinity, which the
+ * (also in its group's worth: with `best` 2, a group of which fewer than two
+ * experts are left is worth as little as one of none, and a tie of such groups
+ * goes to the lower one), it is never chosen, and its softmax is 0 where the
+ * logit is.  So is one whose logit or bias is NaN or +infinity, which the
  * next hgb_sync reports.  Where fewer than `top` experts are left, the slots
  * behind them get expert -1 (dropped by hgb_route) and share 0.
  *
@@ -659,8 +661,8 @@ hgb_status hgb_gate(hgb_ctx* ctx, const void* logits_dev, int32_t type, int64_t 
 /*
  * The logits' gradient from the shares': which experts are chosen counts as
  * given (the bias has no gradient).  All of dlogits is written: zeros for
- * masked experts, and for those not chosen, except where the shares are the
- * softmax itself (renormalise 0), which every logit changes.
+ * experts whose logit masks them, and for those not chosen, except where the
+ * shares are the softmax itself (renormalise 0), which every logit changes.
  *
  * grad_dev:    float [n_rows][top], of the shares.
  * experts_dev: int32 [n_rows][top], as hgb_gate wrote them; the slots of -1
@@ -714,8 +716,12 @@ int64_t hgb_head_backward_workspace(const void* x_dev, int64_t x_stride, const v
  * in pieces of the vocabulary: a piece of dz, computed again from x and table,
  * is the most that the workspace holds of it.  dz is rounded to the inputs'
  * type as a factor of the two products (beside a 32-bit dtable of 16-bit
- * inputs, to three parts of bf16 or two of fp16 for dtable).  What x holds in
- * rows without a gradient reaches nothing; dx is zero there.
+ * inputs, to three parts of bf16 or two of fp16 for dtable).  fp16's dz is held
+ * times a power of two that brings the call's largest finite scale * grad to
+ * 2^14 to 2^15, and is off by up to 2^-39 of that, in rows of much smaller
+ * gradients too: over a large vocabulary a row's dx loses bits where its
+ * gradient is below 2^-10 of the largest, and is mostly rounding below 2^-20.
+ * What x holds in rows without a gradient reaches nothing; dx is zero there.
  *
  * grad_dev:   float [n_rows].  lse_dev: as hgb_cross_entropy wrote it.
  * dx_dev:     [n_rows][dim] of type `type`.
