@@ -628,7 +628,8 @@ hgb_status hgb_route_combine_backward(hgb_ctx* ctx, const void* grad_dev, int32_
  * `keep` groups worth most are eligible.  The row's experts are the `top`
  * eligible ones with the largest keys, largest first; ties, between groups
  * too, go to the lower index.  Keys closer than the error of 32 bits are
- * compared in 64.
+ * compared in 64; without a bias and groups the logits themselves are, also
+ * where their scores are the same in 64 bits.
  *   share = scale * s, or with renormalise scale * s / the sum of the chosen s
  *
  * An expert whose logit or bias is -infinity is masked: its key is -infinity
